@@ -499,6 +499,114 @@ int rar_bucketed_prepare(void* const* tensors, const size_t* counts, size_t nten
 int rar_bucketed_launch(const rar_bucketed_plan* plan, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Operators next to the rings: the reductions that make and finish the    */
+/* gradients of a data-parallel step.  Embedding and layer-norm gradients  */
+/* are sums over a batch's tokens, the rings sum them over the ranks, and  */
+/* the global norm is taken over the reduced tensors.                      */
+/* Device pointers of these calls need only their element's alignment      */
+/* (workspaces: 16 bytes); rows may lie any number of elements apart, so    */
+/* views of flat buffers and rows of odd length are served as they are.    */
+/* Sums are held in binary32 or more and formed in a fixed order: equal    */
+/* inputs give equal bits.  Host memory that runs out in a call's checks   */
+/* is reported as RAR_EHIP.                                                */
+/* ---------------------------------------------------------------------- */
+
+/* Types of token ids. */
+typedef enum rar_id_type { RAR_I32 = 0, RAR_I64 = 1 } rar_id_type;
+
+/* Global norms: the root of the sum of squares, or the largest absolute
+ * value. */
+typedef enum rar_norm_type { RAR_NORM_L2 = 0, RAR_NORM_MAX = 1 } rar_norm_type;
+
+/* A set of gradient tensors prepared once and measured or clipped many
+ * times.  Plain data owned by the caller; filled by rar_grad_prepare. */
+typedef struct {
+  void* workspace;          /* the prepared workspace */
+  uint64_t desc_offset;     /* bytes from workspace to the tile descriptors */
+  uint64_t partial_offset;  /* ... to the partial sums */
+  uint64_t result_offset;   /* ... to the factor of the last clip */
+  uint64_t ntiles;
+} rar_grad_plan;
+
+/* Workspace for rar_grad_prepare; 0 on bad args. */
+size_t rar_grad_workspace_bytes(const size_t* counts, size_t ntensors);
+
+/* grads: ntensors device pointers to counts[t] elements of dtypes[t] (types
+ * may differ between tensors, counts may be 0).  outs: where a clip writes
+ * tensor t, counts[t] elements of out_dtypes[t]; NULL (with out_dtypes NULL)
+ * clips in place.  An output may be its own input in the same type; all
+ * other overlaps are refused (RAR_EOVERLAP).  The checks are made here, and
+ * the descriptors are written into the workspace by work enqueued on
+ * `stream`; the tensors' values are not read.  For as long as the plan is
+ * used the tensors must keep their addresses and nothing else may write the
+ * workspace; calls on one plan must be ordered after its preparation and
+ * after one another. */
+int rar_grad_prepare(void* const* grads, void* const* outs, const size_t* counts, const int* dtypes,
+                     const int* out_dtypes, size_t ntensors, void* workspace, size_t ws_bytes,
+                     rar_grad_plan* plan, void* stream);
+
+/* *norm (device, binary32) <- |scale| * the norm of all elements of the set;
+ * 0 for a set without elements.  scale = 1/N makes a ring's sum over N ranks
+ * their mean.  An L2 norm is summed in binary64, so no finite gradient
+ * overflows or vanishes in it.  A NaN anywhere gives NaN, else an infinity
+ * gives infinity. */
+int rar_grad_norm(const rar_grad_plan* plan, int norm_type, double scale, float* norm, void* stream);
+
+/* The same norm, then every output <- round(gradient * f) with
+ * f = scale * min(1, max_norm / (norm + 1e-6)) rounded to binary32.  An
+ * infinite norm makes f zero, a NaN norm makes every output NaN.
+ * max_norm >= 0 (infinity scales without clipping), scale finite. */
+int rar_grad_clip(const rar_grad_plan* plan, int norm_type, double scale, double max_norm,
+                  float* norm, void* stream);
+
+/* out[t] <- round(scale * weight[ids[t]]) for t < tokens: rows of dim
+ * elements, weight rows weight_stride and out rows out_stride elements
+ * apart.  An id outside [0, vocab) gives a row of zeros. */
+int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_dtype, size_t vocab,
+                          size_t dim, const void* ids, int id_type, size_t tokens, float scale,
+                          void* out, size_t out_stride, int out_dtype, void* stream);
+
+/* Workspace for rar_embedding_backward; 0 on bad args. */
+size_t rar_embedding_workspace_bytes(size_t tokens, size_t vocab, size_t dim);
+
+/* dweight[v] <- round(scale * S_v), or round(dweight[v] + scale * S_v) with
+ * accumulate, for every v < vocab: S_v is the sum of dout[t] over the tokens
+ * t with ids[t] == v, in binary32.  Ids outside [0, vocab) and the id
+ * padding_id (-1: none) contribute nothing.  Rows without tokens become zero,
+ * or stay untouched with accumulate.  dout_stride may be 0 (one row for all
+ * tokens).  tokens, vocab and dim below 2^31. */
+int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype, const void* ids,
+                           int id_type, size_t tokens, size_t vocab, size_t dim, float scale,
+                           int64_t padding_id, int accumulate, void* dweight, size_t dweight_stride,
+                           int dweight_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* y <- round((x - mu) * r * weight + bias) for each of `rows` rows of dim
+ * elements: mu the row's mean, r = 1 / sqrt(mean((x - mu)^2) + eps).  weight
+ * and bias (dim elements of weight_dtype each) may be NULL (1 and 0).
+ * mean and rstd (rows binary32 each, NULL if not wanted) receive mu and r.
+ * y may be x with the same stride; x_stride may be 0. */
+int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, const void* bias,
+                          size_t rows, size_t dim, int dtype, int weight_dtype, float eps, void* y,
+                          size_t y_stride, float* mean, float* rstd, void* stream);
+
+/* Workspace for rar_layernorm_backward; 0 on bad args. */
+size_t rar_layernorm_workspace_bytes(size_t rows, size_t dim);
+
+/* From dy, x and the forward pass's mean and rstd, with h = (x - mean)*rstd
+ * and g = dy * weight:
+ *   dx      <- round(rstd * (g - mean(g) - h * mean(g * h)))
+ *   dweight <- round(sum over rows of dy * h), dbias <- round(sum of dy),
+ * with accumulate added to what they hold.  dx, dweight and dbias may each
+ * be NULL; the workspace is needed for dweight or dbias only.  dx may be dy
+ * or x with the same stride; dy_stride and x_stride may be 0.  rows == 0
+ * makes dweight and dbias zero (untouched with accumulate). */
+int rar_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size_t x_stride,
+                           const void* weight, const float* mean, const float* rstd, size_t rows,
+                           size_t dim, int dtype, int weight_dtype, void* dx, size_t dx_stride,
+                           void* dweight, void* dbias, int accumulate, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 
 /* Static description of a status code. */
 const char* rar_status_string(int status);

@@ -16,3 +16,7 @@ from ._binding import (  # noqa: F401
     rank_hashes, ring_allreduce_ft, shared_state_sync, BucketedAllreduce, rank_tensors, TRAFFIC_BYTES,
     ring_allreduce_compressed_noalloc, NOALLOC_SCRATCH_BYTES,
 )
+from ._operators import (  # noqa: F401
+    NORM_L2, NORM_MAX, GradClip, clip_grad_norm, embedding_backward, embedding_forward, embedding_workspace_bytes,
+    grad_clip_workspace_bytes, grad_norm, layernorm_backward, layernorm_forward, layernorm_workspace_bytes,
+)

@@ -51,6 +51,13 @@ class BucketedPlan(ctypes.Structure):
                 ("sent", ctypes.c_uint64 * 64), ("recv", ctypes.c_uint64 * 64)]
 
 
+class GradPlan(ctypes.Structure):
+    """Mirror of rar_grad_plan: a prepared set of gradient tensors."""
+    _fields_ = [("workspace", ctypes.c_void_p), ("desc_offset", ctypes.c_uint64),
+                ("partial_offset", ctypes.c_uint64), ("result_offset", ctypes.c_uint64),
+                ("ntiles", ctypes.c_uint64)]
+
+
 class CompressCfg(ctypes.Structure):
     """Mirror of rar_compress_cfg."""
     _fields_ = [
@@ -117,6 +124,23 @@ _SIGS = {
     "rar_bucketed_prepare": (_c_int, [_c_vp, _c_vp, _c_size, _c_int, _c_int, _c_size, _c_vp, _c_size,
                                       ctypes.POINTER(BucketedPlan), _c_vp]),
     "rar_bucketed_launch": (_c_int, [ctypes.POINTER(BucketedPlan), _c_vp]),
+    "rar_grad_workspace_bytes": (_c_size, [_c_vp, _c_size]),
+    "rar_grad_prepare": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_size, _c_vp, _c_size,
+                                  ctypes.POINTER(GradPlan), _c_vp]),
+    "rar_grad_norm": (_c_int, [ctypes.POINTER(GradPlan), _c_int, ctypes.c_double, _c_vp, _c_vp]),
+    "rar_grad_clip": (_c_int, [ctypes.POINTER(GradPlan), _c_int, ctypes.c_double, ctypes.c_double, _c_vp, _c_vp]),
+    "rar_embedding_forward": (_c_int, [_c_vp, _c_size, _c_int, _c_size, _c_size, _c_vp, _c_int, _c_size,
+                                       ctypes.c_float, _c_vp, _c_size, _c_int, _c_vp]),
+    "rar_embedding_workspace_bytes": (_c_size, [_c_size, _c_size, _c_size]),
+    "rar_embedding_backward": (_c_int, [_c_vp, _c_size, _c_int, _c_vp, _c_int, _c_size, _c_size, _c_size,
+                                        ctypes.c_float, ctypes.c_int64, _c_int, _c_vp, _c_size, _c_int, _c_vp,
+                                        _c_size, _c_vp]),
+    "rar_layernorm_forward": (_c_int, [_c_vp, _c_size, _c_vp, _c_vp, _c_size, _c_size, _c_int, _c_int,
+                                       ctypes.c_float, _c_vp, _c_size, _c_vp, _c_vp, _c_vp]),
+    "rar_layernorm_workspace_bytes": (_c_size, [_c_size, _c_size]),
+    "rar_layernorm_backward": (_c_int, [_c_vp, _c_size, _c_vp, _c_size, _c_vp, _c_vp, _c_vp, _c_size, _c_size,
+                                        _c_int, _c_int, _c_vp, _c_size, _c_vp, _c_vp, _c_int, _c_vp, _c_size,
+                                        _c_vp]),
     "rar_status_string": (ctypes.c_char_p, [_c_int]),
     "rar_version": (ctypes.c_char_p, []),
 }
