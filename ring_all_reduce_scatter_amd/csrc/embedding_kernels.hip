@@ -155,35 +155,38 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __
     if (in) {
       const uint32_t at = cnt[w * R + r];
       const uint64_t below = peers & ((1ull << lane) - 1ull);
-      sort.order[at + (uint32_t)__popcll(below)] = (uint32_t)t;
+      sort.entries[at + (uint32_t)__popcll(below)] = TokenEntry{(uint32_t)t, (uint32_t)id};
       if (below == 0) cnt[w * R + r] = at + (uint32_t)__popcll(peers);
     }
   }
 }
 
 // ------------------------------------------------------------------ gradient
-// A wavefront per table row and kSeg columns: the row's tokens in order.
+// The sorted tokens are cut into pieces of CH entries whatever rows they
+// belong to, so that a row with very many tokens (a few tokens make up most
+// of any text) is shared by many wavefronts.  A wavefront takes one piece
+// and kSeg columns, adds the gradients of each run of equal rows, and stores
+// a run that lies inside its piece straight to the table's gradient.  A run
+// cut by the piece's beginning goes to the piece's head partial, one that
+// begins here and is cut by its end to its tail partial (binary32); after
+// the launch the tail and the heads that follow it are added in order.
+// Rows without tokens are zeroed by further wavefronts of the same launch.
 
-template <int DI, int DO>
-__global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uint64_t dim, TokenSort sort,
-                                                                   uint64_t units, uint32_t segs, float scale,
-                                                                   bool accumulate, Rows dw) {
-  const uint64_t u = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
-  if (u >= units) return;
-  const uint64_t v = u / segs, c = (u - v * segs) * kSeg + (threadIdx.x & 63) * 8;
-  if (c >= dim) return;
-  const int n = dim - c < 8 ? (int)(dim - c) : 8;
-  const uint32_t s = sort.start[v], e = sort.start[v + 1];
-  if (s == e && accumulate) return;
-  G8 acc = {};
-  for (uint32_t i = s; i < e; ++i) {
-    const G8 g = load8_upto<DI>(dout.p, (uint64_t)sort.order[i] * dout.stride + c, n);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc.v[k] += g.v[k];
-  }
+struct Pieces {
+  uint32_t ch;      // entries per piece (a power of two)
+  uint32_t n;       // pieces
+  uint32_t segs;    // column segments of kSeg
+  uint64_t dim;
+  float* partials;  // [n][2][dim]: head, tail
+};
+
+// Rounds a finished sum into the table's gradient.
+template <int DO>
+__device__ __forceinline__ void store_row(const Rows& dw, uint64_t row, uint64_t c, int n, float scale,
+                                          bool accumulate, G8 acc) {
+  const uint64_t at = row * dw.stride + c;
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc.v[k] *= scale;
-  const uint64_t at = v * dw.stride + c;
   if (accumulate) {
     const G8 old = load8_upto<DO>(dw.p, at, n);
 #pragma unroll
@@ -192,26 +195,122 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   store8_upto<DO, true>(dw.p, at, n, acc);
 }
 
-template <int DI>
-hipError_t embedding_grad_to(const Rows& dout, uint64_t vocab, uint64_t dim, const TokenSort& sort, float scale,
-                             bool accumulate, const Rows& dw, hipStream_t stream) {
-  const uint32_t segs = (uint32_t)((dim + kSeg - 1) / kSeg);
-  const uint64_t units = vocab * segs;
-  const dim3 grid((unsigned)((units + kThreads / 64 - 1) / (kThreads / 64))), block(kThreads);
-  switch (dw.dt) {
-    case DT_F32:
-      hipLaunchKernelGGL((embedding_grad_kernel<DI, DT_F32>), grid, block, 0, stream, dout, dim, sort, units, segs,
-                         scale, accumulate, dw);
-      break;
-    case DT_F16:
-      hipLaunchKernelGGL((embedding_grad_kernel<DI, DT_F16>), grid, block, 0, stream, dout, dim, sort, units, segs,
-                         scale, accumulate, dw);
-      break;
-    default:
-      hipLaunchKernelGGL((embedding_grad_kernel<DI, DT_BF16>), grid, block, 0, stream, dout, dim, sort, units, segs,
-                         scale, accumulate, dw);
+constexpr int kBatch = 8;  // rows of dout in flight per wavefront
+
+template <int DI, int DO>
+__global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uint64_t vocab, TokenSort sort,
+                                                                   Pieces pc, float scale, bool accumulate, Rows dw) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t u = (uint64_t)blockIdx.x * (kThreads / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint64_t units = (uint64_t)pc.n * pc.segs;
+  if (u >= units) {  // zero the rows without tokens
+    const uint64_t v = u - units;
+    if (accumulate || v >= vocab || sort.start[v] != sort.start[v + 1]) return;
+    for (uint64_t c = lane * 8; c < pc.dim; c += kSeg)
+      store8_upto<DO, true>(dw.p, v * dw.stride + c, pc.dim - c < 8 ? (int)(pc.dim - c) : 8, G8{});
+    return;
   }
+  const uint32_t p = (uint32_t)(u / pc.segs);
+  const uint64_t c = (u - (uint64_t)p * pc.segs) * kSeg + lane * 8;
+  const uint32_t total = sort.start[vocab];
+  const uint32_t i0 = p * pc.ch;
+  if (i0 >= total) return;
+  const uint32_t i1 = i0 + pc.ch < total ? i0 + pc.ch : total;
+  const int n = c >= pc.dim ? 0 : (pc.dim - c < 8 ? (int)(pc.dim - c) : 8);
+  uint32_t row = sort.entries[i0].row;
+  bool head = i0 > 0 && sort.entries[i0 - 1].row == row;  // the run began in an earlier piece
+  const bool cut = i1 < total && sort.entries[i1].row == sort.entries[i1 - 1].row;
+  float* part = pc.partials + (uint64_t)p * 2 * pc.dim;
+  G8 acc = {};
+  for (uint32_t b = i0; b < i1; b += kBatch) {
+    const int m = i1 - b < (uint32_t)kBatch ? (int)(i1 - b) : kBatch;
+    TokenEntry e[kBatch];
+    G8 g[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) e[k] = sort.entries[b + (k < m ? k : 0)];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) g[k] = load8_upto<DI>(dout.p, (uint64_t)e[k].token * dout.stride + c, n);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (k >= m) break;
+      if (e[k].row != row) {  // uniform
+        if (head) store8_upto<DT_F32, false>((char*)part, c, n, acc);
+        else store_row<DO>(dw, row, c, n, scale, accumulate, acc);
+        head = false;
+        row = e[k].row;
+        acc = G8{};
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc.v[i] += g[k].v[i];
+    }
+  }
+  if (head) store8_upto<DT_F32, false>((char*)part, c, n, acc);
+  else if (cut) store8_upto<DT_F32, false>((char*)part, pc.dim + c, n, acc);
+  else store_row<DO>(dw, row, c, n, scale, accumulate, acc);
+}
+
+// Adds up the runs that were cut: the workgroup of the piece in which such a
+// run begins (and of kSeg columns) adds the piece's tail and the heads of
+// the pieces up to the run's end, each wavefront a consecutive share of
+// them, the shares in order.
+constexpr int kJoinWaves = 8;
+
+template <int DO>
+__global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab, TokenSort sort, Pieces pc,
+                                                                          float scale, bool accumulate, Rows dw) {
+  extern __shared__ float share[];  // [kJoinWaves][kSeg]
+  const uint32_t p = blockIdx.x / pc.segs;
+  const uint32_t total = sort.start[vocab];
+  const uint32_t i0 = p * pc.ch, i1 = i0 + pc.ch;
+  if (i1 >= total) return;
+  const uint32_t row = sort.entries[i1].row;
+  if (sort.entries[i1 - 1].row != row || sort.start[row] < i0) return;
+  const uint32_t q = (sort.start[row + 1] - 1) / pc.ch;  // the run's last piece, after p
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint64_t c = (uint64_t)(blockIdx.x - p * pc.segs) * kSeg + lane * 8;
+  const int n = c >= pc.dim ? 0 : (pc.dim - c < 8 ? (int)(pc.dim - c) : 8);
+  const uint32_t count = q - p + 1, per = (count + kJoinWaves - 1) / kJoinWaves;
+  const uint32_t a = p + w * per, z = a + per < q + 1 ? a + per : q + 1;
+  G8 acc = {};
+  for (uint32_t k = a; k < z; ++k) {
+    const G8 g = load8_upto<DT_F32>((const char*)pc.partials, ((uint64_t)k * 2 + (k == p)) * pc.dim + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc.v[i] += g.v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) share[w * kSeg + lane * 8 + i] = acc.v[i];
+  __syncthreads();
+  if (w != 0) return;
+  for (int k = 1; k < kJoinWaves; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc.v[i] += share[k * kSeg + lane * 8 + i];
+  store_row<DO>(dw, row, c, n, scale, accumulate, acc);
+}
+
+template <int DI, int DO>
+hipError_t embedding_grad_typed(const Rows& dout, uint64_t vocab, const TokenSort& sort, const Pieces& pc, float scale,
+                                bool accumulate, const Rows& dw, hipStream_t stream) {
+  const uint64_t units = (uint64_t)pc.n * pc.segs + (accumulate ? 0 : vocab);
+  constexpr int waves = kThreads / 64;
+  if (units) {
+    hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads),
+                       0, stream, dout, vocab, sort, pc, scale, accumulate, dw);
+    const hipError_t e = launch_status(stream);
+    if (e != hipSuccess || pc.n < 2) return e;
+  }
+  hipLaunchKernelGGL((embedding_join_kernel<DO>), dim3((pc.n - 1) * pc.segs), dim3(kJoinWaves * 64),
+                     kJoinWaves * kSeg * sizeof(float), stream, vocab, sort, pc, scale, accumulate, dw);
   return launch_status(stream);
+}
+
+template <int DI>
+hipError_t embedding_grad_to(const Rows& dout, uint64_t vocab, const TokenSort& sort, const Pieces& pc, float scale,
+                             bool accumulate, const Rows& dw, hipStream_t stream) {
+  switch (dw.dt) {
+    case DT_F32: return embedding_grad_typed<DI, DT_F32>(dout, vocab, sort, pc, scale, accumulate, dw, stream);
+    case DT_F16: return embedding_grad_typed<DI, DT_F16>(dout, vocab, sort, pc, scale, accumulate, dw, stream);
+    default: return embedding_grad_typed<DI, DT_BF16>(dout, vocab, sort, pc, scale, accumulate, dw, stream);
+  }
 }
 
 }  // namespace
@@ -240,12 +339,25 @@ hipError_t launch_token_sort(const void* ids, bool ids64, uint64_t tokens, uint6
   return launch_status(stream);
 }
 
-hipError_t launch_embedding_grad(const Rows& dout, uint64_t vocab, uint64_t dim, const TokenSort& sort, float scale,
-                                 bool accumulate, const Rows& dweight, hipStream_t stream) {
+uint64_t embedding_piece(uint64_t tokens, uint64_t dim) {
+  // short pieces while that gives wavefronts to fill the chip (16 per CU),
+  // longer ones for long batches: fewer partials
+  const uint64_t segs = (dim + kSeg - 1) / kSeg;
+  uint64_t ch = kBatch;
+  while (ch < 64 && (tokens + ch - 1) / ch * segs > 4096) ch *= 2;
+  return ch;
+}
+
+hipError_t launch_embedding_grad(const Rows& dout, uint64_t tokens, uint64_t vocab, uint64_t dim,
+                                 const TokenSort& sort, float* partials, float scale, bool accumulate,
+                                 const Rows& dweight, hipStream_t stream) {
+  const uint64_t ch = embedding_piece(tokens, dim);
+  const Pieces pc{(uint32_t)ch, (uint32_t)((tokens + ch - 1) / ch), (uint32_t)((dim + kSeg - 1) / kSeg), dim, partials};
+  if (accumulate && tokens == 0) return hipSuccess;
   switch (dout.dt) {
-    case DT_F32: return embedding_grad_to<DT_F32>(dout, vocab, dim, sort, scale, accumulate, dweight, stream);
-    case DT_F16: return embedding_grad_to<DT_F16>(dout, vocab, dim, sort, scale, accumulate, dweight, stream);
-    default: return embedding_grad_to<DT_BF16>(dout, vocab, dim, sort, scale, accumulate, dweight, stream);
+    case DT_F32: return embedding_grad_to<DT_F32>(dout, vocab, sort, pc, scale, accumulate, dweight, stream);
+    case DT_F16: return embedding_grad_to<DT_F16>(dout, vocab, sort, pc, scale, accumulate, dweight, stream);
+    default: return embedding_grad_to<DT_BF16>(dout, vocab, sort, pc, scale, accumulate, dweight, stream);
   }
 }
 

@@ -207,6 +207,19 @@ int embedding_sizes(size_t tokens, size_t vocab, size_t dim) {
   return RAR_OK;
 }
 
+// Workspace: row starts, sorted tokens, partial sums.
+struct EmbeddingLayout {
+  size_t entries, partials, bytes;
+};
+EmbeddingLayout embedding_layout(size_t tokens, size_t vocab, size_t dim) {
+  EmbeddingLayout l;
+  const size_t ch = embedding_piece(tokens, dim);
+  l.entries = round_up((vocab + 1) * sizeof(uint32_t), kAlign);
+  l.partials = l.entries + round_up(tokens * sizeof(TokenEntry), kAlign);
+  l.bytes = l.partials + round_up((tokens + ch - 1) / ch * 2 * dim * sizeof(float), kAlign);
+  return l;
+}
+
 }  // namespace
 
 int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_dtype, size_t vocab, size_t dim,
@@ -235,7 +248,7 @@ int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_d
 
 size_t rar_embedding_workspace_bytes(size_t tokens, size_t vocab, size_t dim) {
   if (embedding_sizes(tokens, vocab, dim)) return 0;
-  return round_up((vocab + 1) * sizeof(uint32_t), kAlign) + round_up(tokens * sizeof(uint32_t), kAlign);
+  return embedding_layout(tokens, vocab, dim).bytes;
 }
 
 int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype, const void* ids, int id_type,
@@ -258,13 +271,16 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   const Range r[] = {{(uintptr_t)dweight, wb, true, 0}, {(uintptr_t)workspace, need, true, 0},
                      {(uintptr_t)dout, db, false, 0}, {(uintptr_t)ids, ib * tokens, false, 0}};
   if ((rc = check_ranges(r, 4))) return rc;
-  if (vocab * ((dim + 511) / 512) / 4 >= kMaxGrid) return RAR_ENOTSUP;
-  const TokenSort sort{(uint32_t*)workspace,
-                       (uint32_t*)((char*)workspace + round_up((vocab + 1) * sizeof(uint32_t), kAlign))};
+  const EmbeddingLayout l = embedding_layout(tokens, vocab, dim);
+  const size_t pieces = (tokens + embedding_piece(tokens, dim) - 1) / embedding_piece(tokens, dim);
+  if (pieces * ((dim + 511) / 512) + vocab >= kMaxGrid) return RAR_ENOTSUP;
+  char* base = (char*)workspace;
+  const TokenSort sort{(uint32_t*)base, (TokenEntry*)(base + l.entries)};
   hipStream_t st = (hipStream_t)stream;
   if ((rc = hip_rc(launch_token_sort(ids, id_type == RAR_I64, tokens, vocab, padding_id, sort, st)))) return rc;
-  return hip_rc(launch_embedding_grad(Rows{(char*)dout, dout_stride, dout_dtype}, vocab, dim, sort, scale,
-                                      accumulate != 0, Rows{(char*)dweight, dweight_stride, dweight_dtype}, st));
+  return hip_rc(launch_embedding_grad(Rows{(char*)dout, dout_stride, dout_dtype}, tokens, vocab, dim, sort,
+                                      (float*)(base + l.partials), scale, accumulate != 0,
+                                      Rows{(char*)dweight, dweight_stride, dweight_dtype}, st));
 }
 
 // ------------------------------------------------------------------ layer norm

@@ -40,16 +40,23 @@ struct Rows {  // rows of `dim` elements, `stride` elements apart
 hipError_t launch_embedding(const Rows& weight, uint64_t vocab, uint64_t dim, const void* ids, bool ids64,
                             uint64_t tokens, float scale, const Rows& out, hipStream_t stream);
 
-// The tokens of each table row in ascending order: row v's are
-// order[start[v] .. start[v+1]) (u32 each; start holds vocab + 1 words).
+// The tokens sorted by table row, ascending within a row: row v's are
+// entries[start[v] .. start[v+1]) (start holds vocab + 1 words).
+struct TokenEntry {
+  uint32_t token, row;
+};
 struct TokenSort {
   uint32_t* start;
-  uint32_t* order;
+  TokenEntry* entries;
 };
 hipError_t launch_token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t vocab, int64_t padding,
                              const TokenSort& sort, hipStream_t stream);
-hipError_t launch_embedding_grad(const Rows& dout, uint64_t vocab, uint64_t dim, const TokenSort& sort, float scale,
-                                 bool accumulate, const Rows& dweight, hipStream_t stream);
+// Entries that one wavefront of the gradient takes; partials holds two rows
+// of dim floats for each such piece.
+uint64_t embedding_piece(uint64_t tokens, uint64_t dim);
+hipError_t launch_embedding_grad(const Rows& dout, uint64_t tokens, uint64_t vocab, uint64_t dim,
+                                 const TokenSort& sort, float* partials, float scale, bool accumulate,
+                                 const Rows& dweight, hipStream_t stream);
 
 // -------------------------------------------------------------- layer norm (layernorm_kernels.hip)
 
