@@ -92,11 +92,11 @@ __device__ __forceinline__ Acc<KIND> block_join(Acc<KIND> a, double* lds) {
 
 template <int DT, int KIND>
 __device__ __forceinline__ void norm_tile(const char* in, uint32_t n, Acc<KIND>& acc) {
-  for (uint32_t e = threadIdx.x * 8; e < n; e += kThreads * 8) {
-    const int k = n - e < 8 ? (int)(n - e) : 8;
-    const G8 g = load8_upto<DT>(in, e, k);
+  constexpr int E = vec_elems<DT, DT>();
+  for (uint32_t e = threadIdx.x * E; e < n; e += kThreads * E) {
+    const VecF<E> g = load_vec_upto<DT, E>(in, e, vec_count<E>(n, e));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc.add(g.v[i]);
+    for (int i = 0; i < E; ++i) acc.add(g.v[i]);
   }
 }
 
@@ -143,12 +143,13 @@ __global__ __launch_bounds__(kThreads) void norm_finish_kernel(const double* __r
 
 template <int DI, int DO>
 __device__ __forceinline__ void clip_tile(const char* in, char* out, uint32_t n, float f) {
-  for (uint32_t e = threadIdx.x * 8; e < n; e += kThreads * 8) {
-    const int k = n - e < 8 ? (int)(n - e) : 8;
-    G8 g = load8_upto<DI>(in, e, k);
+  constexpr int E = vec_elems<DI, DO>();
+  for (uint32_t e = threadIdx.x * E; e < n; e += kThreads * E) {
+    const int k = vec_count<E>(n, e);
+    VecF<E> g = load_vec_upto<DI, E>(in, e, k);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g.v[i] *= f;
-    store8_upto<DO, true>(out, e, k, g);
+    for (int i = 0; i < E; ++i) g.v[i] *= f;
+    store_vec_upto<DO, E>(out, e, k, g);
   }
 }
 

@@ -19,25 +19,61 @@ __device__ __forceinline__ int64_t load_id(const void* ids, bool ids64, uint64_t
   return ids64 ? ((const int64_t*)ids)[t] : (int64_t)((const int32_t*)ids)[t];
 }
 
+// A lane's share of kSeg columns from c0 on: V vectors, 64 * E columns apart.
+template <int E>
+struct SegCols {
+  static constexpr int V = 8 / E;
+  VecF<E> x[V];
+  __device__ __forceinline__ void add(const SegCols& o) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[j].v[i] += o.x[j].v[i];
+  }
+};
+template <int E>
+__device__ __forceinline__ uint64_t seg_col(uint64_t c0, int j) {
+  return c0 + (uint32_t)(j * 64 + (int)(threadIdx.x & 63)) * E;
+}
+template <int DT, int E>
+__device__ __forceinline__ SegCols<E> load_seg(const char* base, uint64_t row, uint64_t c0, uint64_t dim) {
+  SegCols<E> s;
+#pragma unroll
+  for (int j = 0; j < SegCols<E>::V; ++j) {
+    const uint64_t c = seg_col<E>(c0, j);
+    s.x[j] = load_vec_upto<DT, E>(base, row + c, vec_count<E>(dim, c));
+  }
+  return s;
+}
+template <int DT, int E>
+__device__ __forceinline__ void store_seg(char* base, uint64_t row, uint64_t c0, uint64_t dim, const SegCols<E>& s) {
+#pragma unroll
+  for (int j = 0; j < SegCols<E>::V; ++j) {
+    const uint64_t c = seg_col<E>(c0, j);
+    store_vec_upto<DT, E>(base, row + c, vec_count<E>(dim, c), s.x[j]);
+  }
+}
+
 // ------------------------------------------------------------------ lookup
 
 template <int DW, int DO>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(Rows weight, uint64_t vocab, uint64_t dim,
                                                               const void* __restrict__ ids, bool ids64,
                                                               uint64_t units, uint32_t segs, float scale, Rows out) {
+  constexpr int E = vec_elems<DW, DO>();
   const uint64_t u = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
   if (u >= units) return;
-  const uint64_t t = u / segs, c = (u - t * segs) * kSeg + (threadIdx.x & 63) * 8;
-  if (c >= dim) return;
-  const int n = dim - c < 8 ? (int)(dim - c) : 8;
+  const uint64_t t = u / segs, c = (u - t * segs) * kSeg;
   const int64_t id = load_id(ids, ids64, t);
-  G8 g = {};
+  SegCols<E> g = {};
   if ((uint64_t)id < vocab) {
-    g = load8_upto<DW>(weight.p, (uint64_t)id * weight.stride + c, n);
+    g = load_seg<DW, E>(weight.p, (uint64_t)id * weight.stride, c, dim);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g.v[i] *= scale;
+    for (int j = 0; j < SegCols<E>::V; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) g.x[j].v[i] *= scale;
   }
-  store8_upto<DO, true>(out.p, t * out.stride + c, n, g);
+  store_seg<DO, E>(out.p, t * out.stride, c, dim, g);
 }
 
 template <int DW>
@@ -76,6 +112,24 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSortMaxRows = 2048;  // 16 x 2048 counters: 128 of the 160 KiB of LDS
 
+constexpr int kSortAhead = 8;            // ids in flight per lane
+
+// Table rows of the tokens t, t + 64, ... below end; kNoRow for a token that
+// counts for none.
+constexpr uint32_t kNoRow = 0xffffffffu;
+__device__ __forceinline__ void load_rows(const void* ids, bool ids64, uint64_t t, uint64_t end, uint32_t vocab,
+                                          int64_t padding, uint32_t* row) {
+  int64_t id[kSortAhead];
+#pragma unroll
+  for (int k = 0; k < kSortAhead; ++k) {
+    id[k] = -1;
+    if (t + 64 * k < end) id[k] = load_id(ids, ids64, t + 64 * k);
+  }
+#pragma unroll
+  for (int k = 0; k < kSortAhead; ++k)
+    row[k] = (uint64_t)id[k] < vocab && id[k] != padding ? (uint32_t)id[k] : kNoRow;
+}
+
 __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __restrict__ ids, bool ids64,
                                                                    uint32_t tokens, uint32_t vocab, int64_t padding,
                                                                    uint32_t R, int rbits, TokenSort sort) {
@@ -91,13 +145,14 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __
   const uint64_t t0 = (uint64_t)w * part;
   const uint64_t t1 = t0 + part < tokens ? t0 + part : tokens;
   uint32_t before = 0;
-  for (uint64_t b = t0; b < t1; b += 64) {
-    const uint64_t t = b + lane;
-    int64_t id = -1;
-    if (t < t1) id = load_id(ids, ids64, t);
-    const bool ok = (uint64_t)id < vocab && id != padding;
-    if (ok && (uint32_t)id < lo) ++before;
-    if (ok && (uint32_t)id >= lo && (uint32_t)id - lo < rows) atomicAdd(&cnt[w * R + ((uint32_t)id - lo)], 1u);
+  for (uint64_t b = t0; b < t1; b += 64 * kSortAhead) {
+    uint32_t id[kSortAhead];
+    load_rows(ids, ids64, b + lane, t1, vocab, padding, id);
+#pragma unroll
+    for (int k = 0; k < kSortAhead; ++k) {
+      if (id[k] < lo) ++before;
+      else if (id[k] - lo < rows) atomicAdd(&cnt[w * R + (id[k] - lo)], 1u);
+    }
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) before += (uint32_t)__shfl_xor((int)before, d, 64);
@@ -139,24 +194,26 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __
     if (lo + r + 1 == vocab) sort.start[vocab] = pos;
   }
   __syncthreads();
-  for (uint64_t b = t0; b < t1; b += 64) {
-    const uint64_t t = b + lane;
-    int64_t id = -1;
-    if (t < t1) id = load_id(ids, ids64, t);
-    const bool in = (uint64_t)id < vocab && id != padding && (uint32_t)id >= lo && (uint32_t)id - lo < rows;
-    uint64_t peers = __ballot(in);
-    if (peers == 0) continue;  // uniform over the wavefront
-    const uint32_t r = in ? (uint32_t)id - lo : 0;
-    for (int k = 0; k < rbits; ++k) {
-      const bool bit = (r >> k) & 1u;
-      const uint64_t set = __ballot(bit);
-      peers &= bit ? set : ~set;
-    }
-    if (in) {
-      const uint32_t at = cnt[w * R + r];
-      const uint64_t below = peers & ((1ull << lane) - 1ull);
-      sort.entries[at + (uint32_t)__popcll(below)] = TokenEntry{(uint32_t)t, (uint32_t)id};
-      if (below == 0) cnt[w * R + r] = at + (uint32_t)__popcll(peers);
+  for (uint64_t b = t0; b < t1; b += 64 * kSortAhead) {
+    uint32_t id[kSortAhead];
+    load_rows(ids, ids64, b + lane, t1, vocab, padding, id);
+#pragma unroll
+    for (int k = 0; k < kSortAhead; ++k) {
+      const uint32_t r = id[k] - lo;
+      const bool in = id[k] >= lo && r < rows;
+      uint64_t peers = __ballot(in);
+      if (peers == 0) continue;  // uniform over the wavefront
+      for (int j = 0; j < rbits; ++j) {
+        const bool bit = (r >> j) & 1u;
+        const uint64_t set = __ballot(bit);
+        peers &= bit ? set : ~set;
+      }
+      if (in) {
+        const uint32_t at = cnt[w * R + r];
+        const uint64_t below = peers & ((1ull << lane) - 1ull);
+        sort.entries[at + (uint32_t)__popcll(below)] = TokenEntry{(uint32_t)(b + 64 * k + lane), id[k]};
+        if (below == 0) cnt[w * R + r] = at + (uint32_t)__popcll(peers);
+      }
     }
   }
 }
@@ -177,114 +234,136 @@ struct Pieces {
   uint32_t n;       // pieces
   uint32_t segs;    // column segments of kSeg
   uint64_t dim;
-  float* partials;  // [n][2][dim]: head, tail
+  float* partials;  // [n][2][segs * kSeg]: head, tail
 };
 
 // Rounds a finished sum into the table's gradient.
-template <int DO>
-__device__ __forceinline__ void store_row(const Rows& dw, uint64_t row, uint64_t c, int n, float scale,
-                                          bool accumulate, G8 acc) {
-  const uint64_t at = row * dw.stride + c;
+template <int DO, int E>
+__device__ __forceinline__ void finish_row(const Rows& dw, uint64_t row, uint64_t c0, uint64_t dim, float scale,
+                                           bool accumulate, SegCols<E> acc) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) acc.v[k] *= scale;
-  if (accumulate) {
-    const G8 old = load8_upto<DO>(dw.p, at, n);
+  for (int j = 0; j < SegCols<E>::V; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc.v[k] += old.v[k];
+    for (int i = 0; i < E; ++i) acc.x[j].v[i] *= scale;
+  if (accumulate) acc.add(load_seg<DO, E>(dw.p, row * dw.stride, c0, dim));
+  store_seg<DO, E>(dw.p, row * dw.stride, c0, dim, acc);
+}
+
+// Partial sums: a lane's eight values side by side in one workspace row of
+// segs * kSeg floats, so no column is missing.
+template <int E>
+__device__ __forceinline__ float* partial_at(const Pieces& pc, uint32_t piece, int tail, uint64_t c0) {
+  return pc.partials + ((uint64_t)piece * 2 + tail) * pc.segs * kSeg + c0 + (threadIdx.x & 63) * 4;
+}
+template <int E>
+__device__ __forceinline__ void store_partial(float* p, const SegCols<E>& s) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    u32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(s.x[(4 * h) / E].v[(4 * h) % E + i]);
+    *(u32x4*)(p + h * 256) = x;
   }
-  store8_upto<DO, true>(dw.p, at, n, acc);
+}
+template <int E>
+__device__ __forceinline__ SegCols<E> load_partial(const float* p) {
+  SegCols<E> s;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const u32x4 x = *(const u32x4*)(p + h * 256);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.x[(4 * h) / E].v[(4 * h) % E + i] = __uint_as_float(x[i]);
+  }
+  return s;
 }
 
 constexpr int kBatch = 8;  // rows of dout in flight per wavefront
 
 template <int DI, int DO>
-__global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uint64_t vocab, TokenSort sort,
-                                                                   Pieces pc, float scale, bool accumulate, Rows dw) {
-  const int lane = threadIdx.x & 63;
+__global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uint64_t vocab,
+                                                                   const uint32_t* __restrict__ start,
+                                                                   const TokenEntry* __restrict__ entries, Pieces pc,
+                                                                   float scale, bool accumulate, Rows dw) {
+  constexpr int E = vec_elems<DI, DO>();
   const uint64_t u = (uint64_t)blockIdx.x * (kThreads / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t units = (uint64_t)pc.n * pc.segs;
   if (u >= units) {  // zero the rows without tokens
     const uint64_t v = u - units;
-    if (accumulate || v >= vocab || sort.start[v] != sort.start[v + 1]) return;
-    for (uint64_t c = lane * 8; c < pc.dim; c += kSeg)
-      store8_upto<DO, true>(dw.p, v * dw.stride + c, pc.dim - c < 8 ? (int)(pc.dim - c) : 8, G8{});
+    if (accumulate || v >= vocab || start[v] != start[v + 1]) return;
+    constexpr int Z = DO == DT_F32 ? 4 : 8;
+    for (uint64_t c = (threadIdx.x & 63) * Z; c < pc.dim; c += 64 * Z)
+      store_vec_upto<DO, Z>(dw.p, v * dw.stride + c, vec_count<Z>(pc.dim, c), VecF<Z>{});
     return;
   }
   const uint32_t p = (uint32_t)(u / pc.segs);
-  const uint64_t c = (u - (uint64_t)p * pc.segs) * kSeg + lane * 8;
-  const uint32_t total = sort.start[vocab];
+  const uint64_t c0 = (u - (uint64_t)p * pc.segs) * kSeg;
+  const uint32_t total = start[vocab];
   const uint32_t i0 = p * pc.ch;
   if (i0 >= total) return;
   const uint32_t i1 = i0 + pc.ch < total ? i0 + pc.ch : total;
-  const int n = c >= pc.dim ? 0 : (pc.dim - c < 8 ? (int)(pc.dim - c) : 8);
-  uint32_t row = sort.entries[i0].row;
-  bool head = i0 > 0 && sort.entries[i0 - 1].row == row;  // the run began in an earlier piece
-  const bool cut = i1 < total && sort.entries[i1].row == sort.entries[i1 - 1].row;
-  float* part = pc.partials + (uint64_t)p * 2 * pc.dim;
-  G8 acc = {};
+  uint32_t row = entries[i0].row;
+  bool head = i0 > 0 && entries[i0 - 1].row == row;  // the run began in an earlier piece
+  const bool cut = i1 < total && entries[i1].row == entries[i1 - 1].row;
+  SegCols<E> acc = {};
   for (uint32_t b = i0; b < i1; b += kBatch) {
     const int m = i1 - b < (uint32_t)kBatch ? (int)(i1 - b) : kBatch;
     TokenEntry e[kBatch];
-    G8 g[kBatch];
+    SegCols<E> g[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) e[k] = sort.entries[b + (k < m ? k : 0)];
+    for (int k = 0; k < kBatch; ++k) e[k] = entries[b + (k < m ? k : 0)];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) g[k] = load8_upto<DI>(dout.p, (uint64_t)e[k].token * dout.stride + c, n);
+    for (int k = 0; k < kBatch; ++k) g[k] = load_seg<DI, E>(dout.p, (uint64_t)e[k].token * dout.stride, c0, pc.dim);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (k >= m) break;
       if (e[k].row != row) {  // uniform
-        if (head) store8_upto<DT_F32, false>((char*)part, c, n, acc);
-        else store_row<DO>(dw, row, c, n, scale, accumulate, acc);
+        if (head) store_partial(partial_at<E>(pc, p, 0, c0), acc);
+        else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
         head = false;
         row = e[k].row;
-        acc = G8{};
+        acc = SegCols<E>{};
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc.v[i] += g[k].v[i];
+      acc.add(g[k]);
     }
   }
-  if (head) store8_upto<DT_F32, false>((char*)part, c, n, acc);
-  else if (cut) store8_upto<DT_F32, false>((char*)part, pc.dim + c, n, acc);
-  else store_row<DO>(dw, row, c, n, scale, accumulate, acc);
+  if (head) store_partial(partial_at<E>(pc, p, 0, c0), acc);
+  else if (cut) store_partial(partial_at<E>(pc, p, 1, c0), acc);
+  else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
 }
 
 // Adds up the runs that were cut: the workgroup of the piece in which such a
 // run begins (and of kSeg columns) adds the piece's tail and the heads of
 // the pieces up to the run's end, each wavefront a consecutive share of
-// them, the shares in order.
+// them, the shares in order.  E is the gradient kernel's: it fixes which
+// columns a lane's partial sums are.
 constexpr int kJoinWaves = 8;
 
-template <int DO>
-__global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab, TokenSort sort, Pieces pc,
-                                                                          float scale, bool accumulate, Rows dw) {
+template <int DO, int E>
+__global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab,
+                                                                          const uint32_t* __restrict__ start,
+                                                                          const TokenEntry* __restrict__ entries,
+                                                                          Pieces pc, float scale, bool accumulate,
+                                                                          Rows dw) {
   extern __shared__ float share[];  // [kJoinWaves][kSeg]
   const uint32_t p = blockIdx.x / pc.segs;
-  const uint32_t total = sort.start[vocab];
+  const uint32_t total = start[vocab];
   const uint32_t i0 = p * pc.ch, i1 = i0 + pc.ch;
   if (i1 >= total) return;
-  const uint32_t row = sort.entries[i1].row;
-  if (sort.entries[i1 - 1].row != row || sort.start[row] < i0) return;
-  const uint32_t q = (sort.start[row + 1] - 1) / pc.ch;  // the run's last piece, after p
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const uint64_t c = (uint64_t)(blockIdx.x - p * pc.segs) * kSeg + lane * 8;
-  const int n = c >= pc.dim ? 0 : (pc.dim - c < 8 ? (int)(pc.dim - c) : 8);
+  const uint32_t row = entries[i1].row;
+  if (entries[i1 - 1].row != row || start[row] < i0) return;
+  const uint32_t q = (start[row + 1] - 1) / pc.ch;  // the run's last piece, after p
+  const int w = threadIdx.x >> 6;
+  const uint64_t c0 = (uint64_t)(blockIdx.x - p * pc.segs) * kSeg;
   const uint32_t count = q - p + 1, per = (count + kJoinWaves - 1) / kJoinWaves;
   const uint32_t a = p + w * per, z = a + per < q + 1 ? a + per : q + 1;
-  G8 acc = {};
-  for (uint32_t k = a; k < z; ++k) {
-    const G8 g = load8_upto<DT_F32>((const char*)pc.partials, ((uint64_t)k * 2 + (k == p)) * pc.dim + c, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc.v[i] += g.v[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) share[w * kSeg + lane * 8 + i] = acc.v[i];
+  SegCols<E> acc = {};
+  for (uint32_t k = a; k < z; ++k) acc.add(load_partial<E>(partial_at<E>(pc, k, k == p, c0)));
+  float* mine = share + (threadIdx.x & 63) * 4;
+  store_partial(mine + w * kSeg, acc);
   __syncthreads();
   if (w != 0) return;
-  for (int k = 1; k < kJoinWaves; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc.v[i] += share[k * kSeg + lane * 8 + i];
-  store_row<DO>(dw, row, c, n, scale, accumulate, acc);
+  for (int k = 1; k < kJoinWaves; ++k) acc.add(load_partial<E>(mine + k * kSeg));
+  finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
 }
 
 template <int DI, int DO>
@@ -294,12 +373,13 @@ hipError_t embedding_grad_typed(const Rows& dout, uint64_t vocab, const TokenSor
   constexpr int waves = kThreads / 64;
   if (units) {
     hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads),
-                       0, stream, dout, vocab, sort, pc, scale, accumulate, dw);
+                       0, stream, dout, vocab, sort.start, sort.entries, pc, scale, accumulate, dw);
     const hipError_t e = launch_status(stream);
     if (e != hipSuccess || pc.n < 2) return e;
   }
-  hipLaunchKernelGGL((embedding_join_kernel<DO>), dim3((pc.n - 1) * pc.segs), dim3(kJoinWaves * 64),
-                     kJoinWaves * kSeg * sizeof(float), stream, vocab, sort, pc, scale, accumulate, dw);
+  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3((pc.n - 1) * pc.segs),
+                     dim3(kJoinWaves * 64), kJoinWaves * kSeg * sizeof(float), stream, vocab, sort.start, sort.entries,
+                     pc, scale, accumulate, dw);
   return launch_status(stream);
 }
 

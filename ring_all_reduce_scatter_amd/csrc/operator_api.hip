@@ -216,7 +216,7 @@ EmbeddingLayout embedding_layout(size_t tokens, size_t vocab, size_t dim) {
   const size_t ch = embedding_piece(tokens, dim);
   l.entries = round_up((vocab + 1) * sizeof(uint32_t), kAlign);
   l.partials = l.entries + round_up(tokens * sizeof(TokenEntry), kAlign);
-  l.bytes = l.partials + round_up((tokens + ch - 1) / ch * 2 * dim * sizeof(float), kAlign);
+  l.bytes = l.partials + round_up((tokens + ch - 1) / ch * 2 * round_up(dim, 512) * sizeof(float), kAlign);
   return l;
 }
 

@@ -1,7 +1,13 @@
 // Typed access to rows that may start on any element: rows of an odd number
-// of 16-bit elements do.  gfx950 serves 16-byte global accesses at any
-// address, so a lane always moves whole vectors and only the last, partial
-// vector of a row goes element by element.
+// of 16-bit elements do.  gfx950 serves 8- and 16-byte global accesses at
+// any address, so a lane always moves whole vectors and only the last,
+// partial vector of a row goes element by element.
+//
+// A lane's vector is E consecutive elements: 8 when every type involved has
+// 16 bits, 4 as soon as one is binary32, so that each load or store
+// instruction of a wavefront covers one contiguous range in both types.
+// (Eight binary32 elements a lane would be two instructions that each touch
+// every other 16 bytes: streaming stores then reach memory as half lines.)
 #pragma once
 
 #include "common.hpp"
@@ -9,40 +15,117 @@
 namespace rar {
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
-__device__ __forceinline__ u32x4 ld16_any(const char* p) { return *(const u32x4_any*)p; }
-template <bool NT>
-__device__ __forceinline__ void st16_any(char* p, u32x4 v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, (u32x4_any*)p);
-  else *(u32x4_any*)p = v;
+template <int A, int B>
+constexpr int vec_elems() {
+  return A == DT_F32 || B == DT_F32 ? 4 : 8;
 }
 
-// Eight consecutive elements as binary32.
-template <int DT>
-__device__ __forceinline__ G8 load8_any(const char* base, uint64_t elem) {
+template <int E>
+struct VecF {
+  float v[E];
+};
+
+// A vector as stored: E elements of type DT.
+template <int DT, int E>
+struct VecRaw {
+  static constexpr int W = E * DtypeSize<DT>::value / 4;
+  static_assert(W == 2 || W == 4, "8 or 16 bytes");
+  uint32_t w[W];
+};
+
+template <int DT, int E>
+__device__ __forceinline__ VecRaw<DT, E> load_raw(const char* base, uint64_t elem) {
   const char* p = base + elem * DtypeSize<DT>::value;
-  Raw8<DT> r;
-  r.w[0] = ld16_any(p);
-  if constexpr (DT == DT_F32) r.w[1] = ld16_any(p + 16);
-  return unpack8<DT>(r);
-}
-template <int DT, bool NT>
-__device__ __forceinline__ void store8_any(char* base, uint64_t elem, const G8& g) {
-  char* p = base + elem * DtypeSize<DT>::value;
-  const Raw8<DT> r = pack8<DT>(g);
-  st16_any<NT>(p, r.w[0]);
-  if constexpr (DT == DT_F32) st16_any<NT>(p + 16, r.w[1]);
+  VecRaw<DT, E> r;
+  if constexpr (VecRaw<DT, E>::W == 4) {
+    const u32x4 x = *(const u32x4_any*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = x[i];
+  } else {
+    const u32x2 x = *(const u32x2_any*)p;
+    r.w[0] = x[0];
+    r.w[1] = x[1];
+  }
+  return r;
 }
 
-// The same for the first n <= 8 elements (missing ones read as +0).
-template <int DT>
-__device__ __forceinline__ G8 load8_upto(const char* base, uint64_t elem, int n) {
-  return n >= 8 ? load8_any<DT>(base, elem) : load_part8<DT>(base, elem, n);
+template <int DT, int E>
+__device__ __forceinline__ VecF<E> unpack(const VecRaw<DT, E>& r) {
+  VecF<E> f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if constexpr (DT == DT_F32) f.v[i] = __uint_as_float(r.w[i]);
+    else f.v[i] = widen16<DT>(i & 1 ? r.w[i / 2] >> 16 : r.w[i / 2] & 0xffffu);
+  }
+  return f;
 }
-template <int DT, bool NT>
-__device__ __forceinline__ void store8_upto(char* base, uint64_t elem, int n, const G8& g) {
-  if (n >= 8) store8_any<DT, NT>(base, elem, g);
-  else store_part8<DT>(base, elem, n, g);
+
+template <int DT, int E>
+__device__ __forceinline__ VecF<E> load_vec(const char* base, uint64_t elem) {
+  return unpack<DT, E>(load_raw<DT, E>(base, elem));
+}
+
+// Streaming stores (nontemporal): an output that is not read back soon.
+template <int DT, int E>
+__device__ __forceinline__ void store_vec(char* base, uint64_t elem, const VecF<E>& f) {
+  char* p = base + elem * DtypeSize<DT>::value;
+  if constexpr (DT == DT_F32) {
+    u32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(f.v[i]);
+    __builtin_nontemporal_store(x, (u32x4_any*)p);
+  } else if constexpr (E == 8) {
+    u32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pack_pair<DT>(f.v[2 * i], f.v[2 * i + 1]);
+    __builtin_nontemporal_store(x, (u32x4_any*)p);
+  } else {
+    const u32x2 x = {pack_pair<DT>(f.v[0], f.v[1]), pack_pair<DT>(f.v[2], f.v[3])};
+    __builtin_nontemporal_store(x, (u32x2_any*)p);
+  }
+}
+
+// The same for the first n elements; missing ones read as +0.
+template <int DT, int E>
+__device__ __forceinline__ VecF<E> load_vec_upto(const char* base, uint64_t elem, int n) {
+  if (n >= E) return load_vec<DT, E>(base, elem);
+  VecF<E> f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) f.v[i] = i < n ? load_elem<DT>(base, elem + i) : 0.0f;
+  return f;
+}
+template <int DT, int E>
+__device__ __forceinline__ VecRaw<DT, E> load_raw_upto(const char* base, uint64_t elem, int n) {
+  if (n >= E) return load_raw<DT, E>(base, elem);
+  VecRaw<DT, E> r;
+#pragma unroll
+  for (int i = 0; i < VecRaw<DT, E>::W; ++i) {
+    if constexpr (DT == DT_F32) {
+      r.w[i] = i < n ? ((const uint32_t*)base)[elem + i] : 0u;
+    } else {
+      const uint16_t* p = (const uint16_t*)base + elem;
+      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+  }
+  return r;
+}
+template <int DT, int E>
+__device__ __forceinline__ void store_vec_upto(char* base, uint64_t elem, int n, const VecF<E>& f) {
+  if (n >= E) {
+    store_vec<DT, E>(base, elem, f);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (i < n) store_elem<DT>(base, elem + i, f.v[i]);
+}
+
+// Elements of [col, dim) in a vector of E, for any col.
+template <int E>
+__device__ __forceinline__ int vec_count(uint64_t dim, uint64_t col) {
+  return col >= dim ? 0 : (dim - col < (uint64_t)E ? (int)(dim - col) : E);
 }
 
 // One element of a type known at run time (uniform over the launch).
@@ -56,11 +139,21 @@ __device__ __forceinline__ void store_elem_dt(char* base, uint64_t i, int dt, fl
   else store_elem<DT_BF16>(base, i, x);
 }
 
-// Sums over the 64 lanes of a wavefront; every lane receives the result.
+// Sum over the 64 lanes of a wavefront (all active); every lane receives it.
+// Inside a row of 16 lanes by DPP moves, then the four rows by scalar reads.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float lane_f32(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  v += dpp_f32<kDppQuad1032>(v);
+  v += dpp_f32<kDppQuad2301>(v);
+  v += dpp_f32<kDppRowHalfMirror>(v);
+  v += dpp_f32<kDppRowMirror>(v);
+  return (lane_f32(v, 0) + lane_f32(v, 16)) + (lane_f32(v, 32) + lane_f32(v, 48));
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
