@@ -180,12 +180,17 @@ def _check(rc: int, what: str) -> None:
 
 # ------------------------------------------------------------------ marshalling
 
+_dtype_codes: dict = {}  # filled by the first call, so importing needs no torch
+
+
 def dtype_code(t) -> int:
-    import torch
-    m = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    if t.dtype not in m:
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _stream(stream, t):

@@ -13,7 +13,13 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import F32, GradPlan, _check, _dptr, _sizes, _stream, dtype_code, lib
+from . import _binding
+from ._binding import F32, GradPlan, RarError, _sizes, dtype_code, lib
+
+# These calls can take less time on the GPU than their Python does on the
+# host (a layer norm of one row: 3 us), so the way to the library is kept
+# short: types and functions are looked up once, the current stream is read
+# as an address, and shapes are read once per tensor.
 
 NORM_L2, NORM_MAX = 0, 1
 _I32, _I64 = 0, 1
@@ -68,17 +74,51 @@ def _floats(t, n: int, what: str):
         raise ValueError(f"{what} must be float32, got {t.dtype}")
 
 
+def _dptr(t) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"expected a GPU tensor, got one on {t.device}")
+    return t.data_ptr()
+
+
 def _ptr(t):
     return None if t is None else _dptr(t)
 
 
+_id_codes: dict = {}  # filled by the first call, so importing needs no torch
+
+
 def _ids(ids):
-    code = {"torch.int32": _I32, "torch.int64": _I64}.get(str(ids.dtype))
+    if not _id_codes:
+        import torch
+        _id_codes.update({torch.int32: _I32, torch.int64: _I64})
+    code = _id_codes.get(ids.dtype)
     if code is None:
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     return code
+
+
+_current_stream = None
+
+
+def _stream(stream, t):
+    """Address of the given stream, or of the current one on t's device."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        # the address without a Stream object around it, where torch offers that
+        _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _current_stream(t.get_device())
+
+
+def _call(name: str, *args):
+    rc = getattr(_binding._lib or lib(), name)(*args)
+    if rc:
+        raise RarError(rc, name)
 
 
 def _workspace(ws):
@@ -145,21 +185,19 @@ class GradClip:
         self._keep = (grads, outs, workspace)
         self._ws = workspace
         self._plan = GradPlan()
-        _check(lib().rar_grad_prepare(ptrs, optrs, _sizes([g.numel() for g in grads]), dts, odts, n, ws, nbytes,
-                                      ctypes.byref(self._plan), _stream(stream, workspace)), "rar_grad_prepare")
+        _call("rar_grad_prepare", ptrs, optrs, _sizes([g.numel() for g in grads]), dts, odts, n, ws, nbytes,
+              ctypes.byref(self._plan), _stream(stream, workspace))
         self._ref = ctypes.byref(self._plan)
 
     def norm(self, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
         """norm (one float32 on the device) <- |scale| * the norm of all gradients."""
         _floats(norm, 1, "norm")
-        _check(lib().rar_grad_norm(self._ref, norm_type, scale, _ptr(norm), _stream(stream, self._ws)),
-               "rar_grad_norm")
+        _call("rar_grad_norm", self._ref, norm_type, scale, _ptr(norm), _stream(stream, self._ws))
 
     def clip(self, max_norm: float, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
         """The same norm, and every gradient times scale * min(1, max_norm / (norm + 1e-6))."""
         _floats(norm, 1, "norm")
-        _check(lib().rar_grad_clip(self._ref, norm_type, scale, max_norm, _ptr(norm), _stream(stream, self._ws)),
-               "rar_grad_clip")
+        _call("rar_grad_clip", self._ref, norm_type, scale, max_norm, _ptr(norm), _stream(stream, self._ws))
 
 
 def grad_norm(grads, workspace, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
@@ -184,9 +222,8 @@ def embedding_forward(weight, ids, out, scale: float = 1.0, stream=None):
     tokens = ids.numel()
     ostride = _out_rows(out, dim, tokens, "out")
     wstride = _out_rows(weight, dim, vocab, "weight")
-    _check(lib().rar_embedding_forward(_dptr(weight), wstride, dtype_code(weight), vocab, dim, _dptr(ids), code, tokens,
-                                       scale, _dptr(out), ostride, dtype_code(out), _stream(stream, out)),
-           "rar_embedding_forward")
+    _call("rar_embedding_forward", _dptr(weight), wstride, dtype_code(weight), vocab, dim, _dptr(ids), code, tokens,
+          scale, _dptr(out), ostride, dtype_code(out), _stream(stream, out))
 
 
 def embedding_workspace_bytes(tokens: int, vocab: int, dim: int) -> int:
@@ -208,10 +245,9 @@ def embedding_backward(dout, ids, dweight, workspace, scale: float = 1.0, paddin
         raise ValueError(f"dout has {n} rows for {tokens} ids")
     wstride = _out_rows(dweight, dim, vocab, "dweight")
     ws, nbytes = _workspace(workspace)
-    _check(lib().rar_embedding_backward(_dptr(dout), dstride, dtype_code(dout), _dptr(ids), code, tokens, vocab, dim,
-                                        scale, -1 if padding_id is None else padding_id, int(accumulate),
-                                        _dptr(dweight), wstride, dtype_code(dweight), ws, nbytes,
-                                        _stream(stream, dweight)), "rar_embedding_backward")
+    _call("rar_embedding_backward", _dptr(dout), dstride, dtype_code(dout), _dptr(ids), code, tokens, vocab, dim,
+          scale, -1 if padding_id is None else padding_id, int(accumulate), _dptr(dweight), wstride,
+          dtype_code(dweight), ws, nbytes, _stream(stream, dweight))
 
 
 # ------------------------------------------------------------------ layer norm
@@ -238,9 +274,8 @@ def layernorm_forward(x, weight, bias, out, eps: float = 1e-5, mean=None, rstd=N
     _floats(rstd, rows, "rstd")
     dt = dtype_code(x)
     wdt = _weight_type(dt, weight, bias)
-    _check(lib().rar_layernorm_forward(_dptr(x), xstride, _ptr(weight), _ptr(bias), rows, dim, dt, wdt, eps,
-                                       _dptr(out), ystride, _ptr(mean), _ptr(rstd), _stream(stream, x)),
-           "rar_layernorm_forward")
+    _call("rar_layernorm_forward", _dptr(x), xstride, _ptr(weight), _ptr(bias), rows, dim, dt, wdt, eps, _dptr(out),
+          ystride, _ptr(mean), _ptr(rstd), _stream(stream, x))
 
 
 def layernorm_workspace_bytes(rows: int, dim: int) -> int:
@@ -266,6 +301,6 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias, workspac
     dt = dtype_code(x)
     wdt = _weight_type(dt, weight, dweight, dbias)
     ws, nbytes = _workspace(workspace)
-    _check(lib().rar_layernorm_backward(_dptr(dout), dstride, _dptr(x), xstride, _ptr(weight), _ptr(mean), _ptr(rstd),
-                                        rows, dim, dt, wdt, _ptr(dx), gstride, _ptr(dweight), _ptr(dbias),
-                                        int(accumulate), ws, nbytes, _stream(stream, x)), "rar_layernorm_backward")
+    _call("rar_layernorm_backward", _dptr(dout), dstride, _dptr(x), xstride, _ptr(weight), _ptr(mean), _ptr(rstd),
+          rows, dim, dt, wdt, _ptr(dx), gstride, _ptr(dweight), _ptr(dbias), int(accumulate), ws, nbytes,
+          _stream(stream, x))

@@ -15,8 +15,9 @@ namespace {
 
 constexpr int kSeg = 64 * 8;  // columns of a row that a wavefront takes
 
-__device__ __forceinline__ int64_t load_id(const void* ids, bool ids64, uint64_t t) {
-  return ids64 ? ((const int64_t*)ids)[t] : (int64_t)((const int32_t*)ids)[t];
+// A wavefront's number in the grid, the same register for all its lanes.
+__device__ __forceinline__ uint32_t grid_wave() {
+  return blockIdx.x * (blockDim.x / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
 // A lane's share of kSeg columns from c0 on: V vectors, 64 * E columns apart.
@@ -56,15 +57,15 @@ __device__ __forceinline__ void store_seg(char* base, uint64_t row, uint64_t c0,
 
 // ------------------------------------------------------------------ lookup
 
-template <int DW, int DO>
+template <int DW, int DO, typename ID>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(Rows weight, uint64_t vocab, uint64_t dim,
-                                                              const void* __restrict__ ids, bool ids64,
-                                                              uint64_t units, uint32_t segs, float scale, Rows out) {
+                                                              const ID* __restrict__ ids, uint32_t units,
+                                                              uint32_t segs, float scale, Rows out) {
   constexpr int E = vec_elems<DW, DO>();
-  const uint64_t u = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
+  const uint32_t u = grid_wave();
   if (u >= units) return;
-  const uint64_t t = u / segs, c = (u - t * segs) * kSeg;
-  const int64_t id = load_id(ids, ids64, t);
+  const uint64_t t = u / segs, c = (uint64_t)(u - (uint32_t)t * segs) * kSeg;
+  const int64_t id = ids[t];
   SegCols<E> g = {};
   if ((uint64_t)id < vocab) {
     g = load_seg<DW, E>(weight.p, (uint64_t)id * weight.stride, c, dim);
@@ -76,26 +77,35 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(Rows weight, uint64
   store_seg<DO, E>(out.p, t * out.stride, c, dim, g);
 }
 
-template <int DW>
-hipError_t embedding_to(const Rows& w, uint64_t vocab, uint64_t dim, const void* ids, bool ids64, uint64_t tokens,
-                        float scale, const Rows& out, hipStream_t stream) {
+template <int DW, int DO, typename ID>
+hipError_t embedding_typed(const Rows& w, uint64_t vocab, uint64_t dim, const void* ids, uint64_t tokens, float scale,
+                           const Rows& out, hipStream_t stream) {
   const uint32_t segs = (uint32_t)((dim + kSeg - 1) / kSeg);
-  const uint64_t units = tokens * segs;
-  const dim3 grid((unsigned)((units + kThreads / 64 - 1) / (kThreads / 64))), block(kThreads);
-  switch (out.dt) {
-    case DT_F32:
-      hipLaunchKernelGGL((embedding_kernel<DW, DT_F32>), grid, block, 0, stream, w, vocab, dim, ids, ids64, units,
-                         segs, scale, out);
-      break;
-    case DT_F16:
-      hipLaunchKernelGGL((embedding_kernel<DW, DT_F16>), grid, block, 0, stream, w, vocab, dim, ids, ids64, units,
-                         segs, scale, out);
-      break;
-    default:
-      hipLaunchKernelGGL((embedding_kernel<DW, DT_BF16>), grid, block, 0, stream, w, vocab, dim, ids, ids64, units,
-                         segs, scale, out);
-  }
+  const uint32_t units = (uint32_t)(tokens * segs);
+  constexpr uint32_t waves = kThreads / 64;
+  hipLaunchKernelGGL((embedding_kernel<DW, DO, ID>), dim3(units / waves + (units % waves != 0)), dim3(kThreads), 0,
+                     stream, w, vocab, dim, (const ID*)ids, units, segs, scale, out);
   return launch_status(stream);
+}
+
+template <int DW, typename ID>
+hipError_t embedding_to(const Rows& w, uint64_t vocab, uint64_t dim, const void* ids, uint64_t tokens, float scale,
+                        const Rows& out, hipStream_t stream) {
+  switch (out.dt) {
+    case DT_F32: return embedding_typed<DW, DT_F32, ID>(w, vocab, dim, ids, tokens, scale, out, stream);
+    case DT_F16: return embedding_typed<DW, DT_F16, ID>(w, vocab, dim, ids, tokens, scale, out, stream);
+    default: return embedding_typed<DW, DT_BF16, ID>(w, vocab, dim, ids, tokens, scale, out, stream);
+  }
+}
+
+template <typename ID>
+hipError_t embedding_ids(const Rows& w, uint64_t vocab, uint64_t dim, const void* ids, uint64_t tokens, float scale,
+                         const Rows& out, hipStream_t stream) {
+  switch (w.dt) {
+    case DT_F32: return embedding_to<DT_F32, ID>(w, vocab, dim, ids, tokens, scale, out, stream);
+    case DT_F16: return embedding_to<DT_F16, ID>(w, vocab, dim, ids, tokens, scale, out, stream);
+    default: return embedding_to<DT_BF16, ID>(w, vocab, dim, ids, tokens, scale, out, stream);
+  }
 }
 
 // ------------------------------------------------------------------ token sort
@@ -117,22 +127,26 @@ constexpr int kSortAhead = 8;            // ids in flight per lane
 // Table rows of the tokens t, t + 64, ... below end; kNoRow for a token that
 // counts for none.
 constexpr uint32_t kNoRow = 0xffffffffu;
-__device__ __forceinline__ void load_rows(const void* ids, bool ids64, uint64_t t, uint64_t end, uint32_t vocab,
-                                          int64_t padding, uint32_t* row) {
-  int64_t id[kSortAhead];
+template <typename ID>
+__device__ __forceinline__ void load_rows(const ID* ids, uint32_t t, uint32_t end, uint32_t vocab, int64_t padding,
+                                          uint32_t* row) {
+  ID id[kSortAhead];
 #pragma unroll
   for (int k = 0; k < kSortAhead; ++k) {
-    id[k] = -1;
-    if (t + 64 * k < end) id[k] = load_id(ids, ids64, t + 64 * k);
+    const uint32_t i = t + 64 * k;
+    id[k] = ids[i < end ? i : end - 1];
   }
 #pragma unroll
-  for (int k = 0; k < kSortAhead; ++k)
-    row[k] = (uint64_t)id[k] < vocab && id[k] != padding ? (uint32_t)id[k] : kNoRow;
+  for (int k = 0; k < kSortAhead; ++k) {
+    const int64_t v = id[k];
+    row[k] = t + 64 * k < end && (uint64_t)v < vocab && v != padding ? (uint32_t)v : kNoRow;
+  }
 }
 
-__global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __restrict__ ids, bool ids64,
-                                                                   uint32_t tokens, uint32_t vocab, int64_t padding,
-                                                                   uint32_t R, int rbits, TokenSort sort) {
+template <typename ID>
+__global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __restrict__ ids, uint32_t tokens,
+                                                                   uint32_t vocab, int64_t padding, uint32_t R,
+                                                                   int rbits, TokenSort sort) {
   extern __shared__ uint32_t sm[];
   uint32_t* cnt = sm;                          // [kSortWaves][R]
   uint32_t* wsum = sm + kSortWaves * R;        // [kSortWaves]
@@ -142,12 +156,12 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __
   for (uint32_t i = tid; i < kSortWaves * R; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
   const uint32_t part = ((tokens + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
-  const uint64_t t0 = (uint64_t)w * part;
-  const uint64_t t1 = t0 + part < tokens ? t0 + part : tokens;
+  const uint32_t t0 = (uint32_t)w * part;  // at most tokens + 1024: below 2^32
+  const uint32_t t1 = t0 + part < tokens ? t0 + part : tokens;
   uint32_t before = 0;
-  for (uint64_t b = t0; b < t1; b += 64 * kSortAhead) {
+  for (uint32_t b = t0; b < t1; b += 64 * kSortAhead) {
     uint32_t id[kSortAhead];
-    load_rows(ids, ids64, b + lane, t1, vocab, padding, id);
+    load_rows(ids, b + lane, t1, vocab, padding, id);
 #pragma unroll
     for (int k = 0; k < kSortAhead; ++k) {
       if (id[k] < lo) ++before;
@@ -167,8 +181,9 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __
   uint32_t mine = 0;
   for (uint32_t j = 0; j < per; ++j) {
     const uint32_t r = (uint32_t)tid * per + j;
-    if (r < rows)
-      for (int k = 0; k < kSortWaves; ++k) mine += cnt[k * R + r];
+    if (r >= rows) break;
+#pragma unroll
+    for (int k = 0; k < kSortWaves; ++k) mine += cnt[k * R + r];
   }
   uint32_t incl = mine;
 #pragma unroll
@@ -186,17 +201,20 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const void* __
     const uint32_t r = (uint32_t)tid * per + j;
     if (r >= rows) break;
     sort.start[lo + r] = pos;
+    uint32_t c[kSortWaves];
+#pragma unroll
+    for (int k = 0; k < kSortWaves; ++k) c[k] = cnt[k * R + r];
+#pragma unroll
     for (int k = 0; k < kSortWaves; ++k) {
-      const uint32_t c = cnt[k * R + r];
       cnt[k * R + r] = pos;
-      pos += c;
+      pos += c[k];
     }
     if (lo + r + 1 == vocab) sort.start[vocab] = pos;
   }
   __syncthreads();
-  for (uint64_t b = t0; b < t1; b += 64 * kSortAhead) {
+  for (uint32_t b = t0; b < t1; b += 64 * kSortAhead) {
     uint32_t id[kSortAhead];
-    load_rows(ids, ids64, b + lane, t1, vocab, padding, id);
+    load_rows(ids, b + lane, t1, vocab, padding, id);
 #pragma unroll
     for (int k = 0; k < kSortAhead; ++k) {
       const uint32_t r = id[k] - lo;
@@ -285,8 +303,8 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
                                                                    const TokenEntry* __restrict__ entries, Pieces pc,
                                                                    float scale, bool accumulate, Rows dw) {
   constexpr int E = vec_elems<DI, DO>();
-  const uint64_t u = (uint64_t)blockIdx.x * (kThreads / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint64_t units = (uint64_t)pc.n * pc.segs;
+  const uint32_t u = grid_wave();
+  const uint32_t units = pc.n * pc.segs;
   if (u >= units) {  // zero the rows without tokens
     const uint64_t v = u - units;
     if (accumulate || v >= vocab || start[v] != start[v + 1]) return;
@@ -295,8 +313,8 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
       store_vec_upto<DO, Z>(dw.p, v * dw.stride + c, vec_count<Z>(pc.dim, c), VecF<Z>{});
     return;
   }
-  const uint32_t p = (uint32_t)(u / pc.segs);
-  const uint64_t c0 = (u - (uint64_t)p * pc.segs) * kSeg;
+  const uint32_t p = u / pc.segs;
+  const uint64_t c0 = (uint64_t)(u - p * pc.segs) * kSeg;
   const uint32_t total = start[vocab];
   const uint32_t i0 = p * pc.ch;
   if (i0 >= total) return;
@@ -398,11 +416,8 @@ hipError_t embedding_grad_to(const Rows& dout, uint64_t vocab, const TokenSort& 
 hipError_t launch_embedding(const Rows& weight, uint64_t vocab, uint64_t dim, const void* ids, bool ids64,
                             uint64_t tokens, float scale, const Rows& out, hipStream_t stream) {
   if (tokens == 0) return hipSuccess;
-  switch (weight.dt) {
-    case DT_F32: return embedding_to<DT_F32>(weight, vocab, dim, ids, ids64, tokens, scale, out, stream);
-    case DT_F16: return embedding_to<DT_F16>(weight, vocab, dim, ids, ids64, tokens, scale, out, stream);
-    default: return embedding_to<DT_BF16>(weight, vocab, dim, ids, ids64, tokens, scale, out, stream);
-  }
+  return ids64 ? embedding_ids<int64_t>(weight, vocab, dim, ids, tokens, scale, out, stream)
+               : embedding_ids<int32_t>(weight, vocab, dim, ids, tokens, scale, out, stream);
 }
 
 hipError_t launch_token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t vocab, int64_t padding,
@@ -414,8 +429,12 @@ hipError_t launch_token_sort(const void* ids, bool ids64, uint64_t tokens, uint6
   while ((1u << rbits) < R) ++rbits;
   const uint32_t grid = (uint32_t)((vocab + R - 1) / R);
   const size_t lds = ((size_t)kSortWaves * R + kSortWaves) * sizeof(uint32_t);
-  hipLaunchKernelGGL(token_sort_kernel, dim3(grid), dim3(kSortThreads), lds, stream, ids, ids64, (uint32_t)tokens,
-                     (uint32_t)vocab, padding, R, rbits, sort);
+  if (ids64)
+    hipLaunchKernelGGL(token_sort_kernel<int64_t>, dim3(grid), dim3(kSortThreads), lds, stream, (const int64_t*)ids,
+                       (uint32_t)tokens, (uint32_t)vocab, padding, R, rbits, sort);
+  else
+    hipLaunchKernelGGL(token_sort_kernel<int32_t>, dim3(grid), dim3(kSortThreads), lds, stream, (const int32_t*)ids,
+                       (uint32_t)tokens, (uint32_t)vocab, padding, R, rbits, sort);
   return launch_status(stream);
 }
 

@@ -16,6 +16,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr uint64_t kMaxGrid = 0x7fffffffull;
+constexpr uint64_t kMaxUnits = 0xfffffff0ull;  // wavefronts of one launch (32-bit numbers)
 
 size_t es_of(int dt) { return dt == RAR_F32 ? 4 : 2; }
 bool dt_ok(int dt) { return dt == RAR_F32 || dt == RAR_F16 || dt == RAR_BF16; }
@@ -240,7 +241,7 @@ int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_d
   const Range r[] = {{(uintptr_t)out, ob, true, 0}, {(uintptr_t)weight, wb, false, 0},
                      {(uintptr_t)ids, ib * tokens, false, 0}};
   if ((rc = check_ranges(r, 3))) return rc;
-  if (tokens * ((dim + 511) / 512) / 4 >= kMaxGrid) return RAR_ENOTSUP;
+  if (tokens * ((dim + 511) / 512) > kMaxUnits) return RAR_ENOTSUP;
   return hip_rc(launch_embedding(Rows{(char*)weight, weight_stride, weight_dtype}, vocab, dim, ids,
                                  id_type == RAR_I64, tokens, scale, Rows{(char*)out, out_stride, out_dtype},
                                  (hipStream_t)stream));
@@ -273,7 +274,7 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   if ((rc = check_ranges(r, 4))) return rc;
   const EmbeddingLayout l = embedding_layout(tokens, vocab, dim);
   const size_t pieces = (tokens + embedding_piece(tokens, dim) - 1) / embedding_piece(tokens, dim);
-  if (pieces * ((dim + 511) / 512) + vocab >= kMaxGrid) return RAR_ENOTSUP;
+  if (pieces * ((dim + 511) / 512) + vocab > kMaxUnits) return RAR_ENOTSUP;
   char* base = (char*)workspace;
   const TokenSort sort{(uint32_t*)base, (TokenEntry*)(base + l.entries)};
   hipStream_t st = (hipStream_t)stream;

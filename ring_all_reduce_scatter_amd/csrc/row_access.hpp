@@ -35,16 +35,21 @@ struct VecRaw {
   uint32_t w[W];
 };
 
-template <int DT, int E>
+// NT: a streaming (nontemporal) load, for data that the launch reads once.
+template <int DT, int E, bool NT = false>
 __device__ __forceinline__ VecRaw<DT, E> load_raw(const char* base, uint64_t elem) {
   const char* p = base + elem * DtypeSize<DT>::value;
   VecRaw<DT, E> r;
   if constexpr (VecRaw<DT, E>::W == 4) {
-    const u32x4 x = *(const u32x4_any*)p;
+    u32x4 x;
+    if constexpr (NT) x = __builtin_nontemporal_load((const u32x4_any*)p);
+    else x = *(const u32x4_any*)p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.w[i] = x[i];
   } else {
-    const u32x2 x = *(const u32x2_any*)p;
+    u32x2 x;
+    if constexpr (NT) x = __builtin_nontemporal_load((const u32x2_any*)p);
+    else x = *(const u32x2_any*)p;
     r.w[0] = x[0];
     r.w[1] = x[1];
   }
@@ -67,20 +72,25 @@ __device__ __forceinline__ VecF<E> load_vec(const char* base, uint64_t elem) {
   return unpack<DT, E>(load_raw<DT, E>(base, elem));
 }
 
+// Four binary32 or eight 16-bit elements as stored.
+template <int DT, int E>
+__device__ __forceinline__ u32x4 pack_vec(const VecF<E>& f) {
+  static_assert(E * DtypeSize<DT>::value == 16, "16 bytes");
+  u32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == DT_F32) x[i] = __float_as_uint(f.v[i]);
+    else x[i] = pack_pair<DT>(f.v[2 * i], f.v[2 * i + 1]);
+  }
+  return x;
+}
+
 // Streaming stores (nontemporal): an output that is not read back soon.
 template <int DT, int E>
 __device__ __forceinline__ void store_vec(char* base, uint64_t elem, const VecF<E>& f) {
   char* p = base + elem * DtypeSize<DT>::value;
-  if constexpr (DT == DT_F32) {
-    u32x4 x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(f.v[i]);
-    __builtin_nontemporal_store(x, (u32x4_any*)p);
-  } else if constexpr (E == 8) {
-    u32x4 x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = pack_pair<DT>(f.v[2 * i], f.v[2 * i + 1]);
-    __builtin_nontemporal_store(x, (u32x4_any*)p);
+  if constexpr (VecRaw<DT, E>::W == 4) {
+    __builtin_nontemporal_store(pack_vec<DT, E>(f), (u32x4_any*)p);
   } else {
     const u32x2 x = {pack_pair<DT>(f.v[0], f.v[1]), pack_pair<DT>(f.v[2], f.v[3])};
     __builtin_nontemporal_store(x, (u32x2_any*)p);
