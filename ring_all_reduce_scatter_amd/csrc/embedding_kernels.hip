@@ -110,17 +110,19 @@ hipError_t embedding_ids(const Rows& w, uint64_t vocab, uint64_t dim, const void
 
 // ------------------------------------------------------------------ token sort
 // Workgroup b owns the R table rows from lo = b*R.  Its 16 wavefronts each
-// walk one sixteenth of the tokens twice: first they count the tokens of
-// every owned row (and those of rows before lo, which is where the
-// workgroup's part of the order begins), then, with the counts turned into
-// positions (row by row, within a row wavefront by wavefront), they place
-// them.  Tokens that share a row and a wavefront iteration are ranked by
-// their lanes.  Every workgroup reads all ids: 256 workgroups read them
-// from the L2, and no pass over memory or launch is added.
+// walk one sixteenth of the tokens: they count the tokens of every owned row
+// (and those of rows before lo, which is where the workgroup's part of the
+// order begins) and keep the owned tokens in LDS.  With the counts turned
+// into positions (row by row, within a row wavefront by wavefront) they
+// place the kept tokens, or, where a wavefront met more than it can keep,
+// walk the ids again.  Tokens that share a row and a wavefront iteration are
+// ranked by their lanes.  Every workgroup reads all ids: 256 workgroups read
+// them from the L2, and no pass over memory or launch is added.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr uint32_t kSortMaxRows = 2048;  // 16 x 2048 counters: 128 of the 160 KiB of LDS
+constexpr uint32_t kSortKeep = 256;      // owned tokens that a wavefront keeps from the first walk
+constexpr uint32_t kSortMaxRows = 1792;  // counters of 112 KiB, kept tokens of 32: of the CU's 160
 
 constexpr int kSortAhead = 8;            // ids in flight per lane
 
@@ -143,14 +145,28 @@ __device__ __forceinline__ void load_rows(const ID* ids, uint32_t t, uint32_t en
   }
 }
 
+// Lanes with the same r (below 2^rbits) as this one, among those of `in`.
+__device__ __forceinline__ uint64_t lanes_alike(bool in, uint32_t r, int rbits) {
+  uint64_t alike = __ballot(in);
+  for (int j = 0; j < rbits; ++j) {
+    const bool bit = (r >> j) & 1u;
+    const uint64_t set = __ballot(bit);
+    alike &= bit ? set : ~set;
+  }
+  return alike;
+}
+// Bits of the lanes before this one.
+__device__ __forceinline__ uint64_t lanes_before() { return (1ull << (threadIdx.x & 63)) - 1ull; }
+
 template <typename ID>
 __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __restrict__ ids, uint32_t tokens,
                                                                    uint32_t vocab, int64_t padding, uint32_t R,
                                                                    int rbits, TokenSort sort) {
   extern __shared__ uint32_t sm[];
-  uint32_t* cnt = sm;                          // [kSortWaves][R]
-  uint32_t* wsum = sm + kSortWaves * R;        // [kSortWaves]
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  uint32_t* wsum = sm;                                               // [kSortWaves]
+  TokenEntry* keep = (TokenEntry*)(sm + kSortWaves) + w * kSortKeep;  // [kSortWaves][kSortKeep]
+  uint32_t* cnt = sm + kSortWaves + 2 * kSortWaves * kSortKeep;      // [kSortWaves][R]
   const uint32_t lo = blockIdx.x * R;
   const uint32_t rows = vocab - lo < R ? vocab - lo : R;
   for (uint32_t i = tid; i < kSortWaves * R; i += kSortThreads) cnt[i] = 0;
@@ -158,14 +174,23 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __re
   const uint32_t part = ((tokens + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   const uint32_t t0 = (uint32_t)w * part;  // at most tokens + 1024: below 2^32
   const uint32_t t1 = t0 + part < tokens ? t0 + part : tokens;
-  uint32_t before = 0;
+  uint32_t before = 0, kept = 0;
   for (uint32_t b = t0; b < t1; b += 64 * kSortAhead) {
     uint32_t id[kSortAhead];
     load_rows(ids, b + lane, t1, vocab, padding, id);
 #pragma unroll
     for (int k = 0; k < kSortAhead; ++k) {
       if (id[k] < lo) ++before;
-      else if (id[k] - lo < rows) atomicAdd(&cnt[w * R + (id[k] - lo)], 1u);
+      const uint32_t r = id[k] - lo;
+      const bool in = id[k] >= lo && r < rows;
+      const uint64_t owned = __ballot(in);
+      if (owned == 0) continue;  // uniform over the wavefront
+      if (in) {
+        atomicAdd(&cnt[w * R + r], 1u);
+        const uint32_t at = kept + (uint32_t)__popcll(owned & lanes_before());
+        if (at < kSortKeep) keep[at] = TokenEntry{b + 64 * k + lane, r};
+      }
+      kept += (uint32_t)__popcll(owned);
     }
   }
 #pragma unroll
@@ -212,6 +237,23 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __re
     if (lo + r + 1 == vocab) sort.start[vocab] = pos;
   }
   __syncthreads();
+  auto place = [&](bool in, uint32_t r, uint32_t token) {
+    const uint64_t alike = lanes_alike(in, r, rbits);
+    if (in) {
+      const uint32_t at = cnt[w * R + r];
+      const uint64_t below = alike & lanes_before();
+      sort.entries[at + (uint32_t)__popcll(below)] = TokenEntry{token, lo + r};
+      if (below == 0) cnt[w * R + r] = at + (uint32_t)__popcll(alike);
+    }
+  };
+  if (kept <= kSortKeep) {  // uniform over the wavefront
+    for (uint32_t i = 0; i < kept; i += 64) {
+      const bool in = i + lane < kept;
+      const TokenEntry e = keep[in ? i + lane : i];
+      place(in, in ? e.row : 0, e.token);
+    }
+    return;
+  }
   for (uint32_t b = t0; b < t1; b += 64 * kSortAhead) {
     uint32_t id[kSortAhead];
     load_rows(ids, b + lane, t1, vocab, padding, id);
@@ -219,21 +261,27 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __re
     for (int k = 0; k < kSortAhead; ++k) {
       const uint32_t r = id[k] - lo;
       const bool in = id[k] >= lo && r < rows;
-      uint64_t peers = __ballot(in);
-      if (peers == 0) continue;  // uniform over the wavefront
-      for (int j = 0; j < rbits; ++j) {
-        const bool bit = (r >> j) & 1u;
-        const uint64_t set = __ballot(bit);
-        peers &= bit ? set : ~set;
-      }
-      if (in) {
-        const uint32_t at = cnt[w * R + r];
-        const uint64_t below = peers & ((1ull << lane) - 1ull);
-        sort.entries[at + (uint32_t)__popcll(below)] = TokenEntry{(uint32_t)(b + 64 * k + lane), id[k]};
-        if (below == 0) cnt[w * R + r] = at + (uint32_t)__popcll(peers);
-      }
+      if (__ballot(in) != 0) place(in, in ? r : 0, b + 64 * k + lane);
     }
   }
+}
+
+hipError_t token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t vocab, int64_t padding,
+                             const TokenSort& sort, hipStream_t stream) {
+  uint32_t R = (uint32_t)((vocab + 255) / 256);
+  if (R < 16) R = 16;
+  if (R > kSortMaxRows) R = kSortMaxRows;
+  int rbits = 1;
+  while ((1u << rbits) < R) ++rbits;
+  const uint32_t grid = (uint32_t)((vocab + R - 1) / R);
+  const size_t lds = ((size_t)kSortWaves * R + kSortWaves + 2 * kSortWaves * kSortKeep) * sizeof(uint32_t);
+  if (ids64)
+    hipLaunchKernelGGL(token_sort_kernel<int64_t>, dim3(grid), dim3(kSortThreads), lds, stream, (const int64_t*)ids,
+                       (uint32_t)tokens, (uint32_t)vocab, padding, R, rbits, sort);
+  else
+    hipLaunchKernelGGL(token_sort_kernel<int32_t>, dim3(grid), dim3(kSortThreads), lds, stream, (const int32_t*)ids,
+                       (uint32_t)tokens, (uint32_t)vocab, padding, R, rbits, sort);
+  return launch_status(stream);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -350,11 +398,22 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
 }
 
 // Adds up the runs that were cut: the workgroup of the piece in which such a
-// run begins (and of kSeg columns) adds the piece's tail and the heads of
-// the pieces up to the run's end, each wavefront a consecutive share of
-// them, the shares in order.  E is the gradient kernel's: it fixes which
-// columns a lane's partial sums are.
-constexpr int kJoinWaves = 8;
+// run begins adds the piece's tail and the heads of the pieces up to the
+// run's end.  Up to kJoinAlone of them a wavefront adds alone, each
+// wavefront its own column segments; of more, all wavefronts of the
+// workgroup add consecutive shares, segment by segment, and the shares are
+// added in order.  E is the gradient kernel's: it fixes which columns a
+// lane's partial sums are.
+constexpr uint32_t kJoinWaves = 8, kJoinAlone = 16;
+
+template <int E>
+__device__ __forceinline__ SegCols<E> join_partials(const Pieces& pc, uint32_t first, uint32_t a, uint32_t z,
+                                                    uint64_t c0) {
+  SegCols<E> acc = {};
+#pragma unroll 4
+  for (uint32_t k = a; k < z; ++k) acc.add(load_partial<E>(partial_at<E>(pc, k, k == first, c0)));
+  return acc;
+}
 
 template <int DO, int E>
 __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab,
@@ -363,51 +422,188 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
                                                                           Pieces pc, float scale, bool accumulate,
                                                                           Rows dw) {
   extern __shared__ float share[];  // [kJoinWaves][kSeg]
-  const uint32_t p = blockIdx.x / pc.segs;
-  const uint32_t total = start[vocab];
+  const uint32_t p = blockIdx.x;
   const uint32_t i0 = p * pc.ch, i1 = i0 + pc.ch;
-  if (i1 >= total) return;
-  const uint32_t row = entries[i1].row;
-  if (entries[i1 - 1].row != row || start[row] < i0) return;
-  const uint32_t q = (start[row + 1] - 1) / pc.ch;  // the run's last piece, after p
-  const int w = threadIdx.x >> 6;
-  const uint64_t c0 = (uint64_t)(blockIdx.x - p * pc.segs) * kSeg;
-  const uint32_t count = q - p + 1, per = (count + kJoinWaves - 1) / kJoinWaves;
-  const uint32_t a = p + w * per, z = a + per < q + 1 ? a + per : q + 1;
-  SegCols<E> acc = {};
-  for (uint32_t k = a; k < z; ++k) acc.add(load_partial<E>(partial_at<E>(pc, k, k == p, c0)));
+  const uint32_t total = start[vocab];
+  const uint32_t before = entries[i1 - 1].row, row = entries[i1].row;  // both inside the buffer, in use or not
+  if (i1 >= total || before != row || start[row] < i0) return;
+  const uint32_t z = (start[row + 1] - 1) / pc.ch + 1;  // past the run's last piece
+  const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (z - p <= kJoinAlone) {
+    for (uint32_t g = w; g < pc.segs; g += kJoinWaves) {
+      const uint64_t c0 = (uint64_t)g * kSeg;
+      finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, join_partials<E>(pc, p, p, z, c0));
+    }
+    return;
+  }
+  const uint32_t per = (z - p + kJoinWaves - 1) / kJoinWaves;
+  const uint32_t a = p + w * per < z ? p + w * per : z, b = a + per < z ? a + per : z;
   float* mine = share + (threadIdx.x & 63) * 4;
-  store_partial(mine + w * kSeg, acc);
+  for (uint32_t g = 0; g < pc.segs; ++g) {
+    const uint64_t c0 = (uint64_t)g * kSeg;
+    SegCols<E> acc = join_partials<E>(pc, p, a, b, c0);
+    store_partial(mine + w * kSeg, acc);
+    __syncthreads();
+    if (w == 0) {
+      for (uint32_t k = 1; k < kJoinWaves; ++k) acc.add(load_partial<E>(mine + k * kSeg));
+      finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ gradient of few tokens
+// Up to kFewTokens tokens are sorted, added and stored by one launch.  A
+// workgroup takes R table rows and kSeg columns: it picks its rows' tokens
+// out of all ids (one a thread), zeroes the rows that have none, sorts the
+// others in LDS by counting for each how many come before it (an entry is
+// row << 10 | token, so they are ordered as numbers), and adds them in
+// sixteen pieces as above, with the partial sums in LDS.
+
+constexpr uint32_t kFewTokens = 1024, kFewWaves = kFewTokens / 64, kFewRows = 1024;
+
+template <int DI, int DO, typename ID>
+__global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dout, const ID* __restrict__ ids,
+                                                                         uint32_t tokens, uint32_t vocab, uint64_t dim,
+                                                                         int64_t padding, uint32_t R, float scale,
+                                                                         bool accumulate, Rows dw) {
+  constexpr int E = vec_elems<DI, DO>();
+  extern __shared__ uint32_t sm[];
+  uint32_t* count = sm;                                            // [kFewWaves]
+  uint32_t* used = sm + kFewWaves;                                 // [kFewRows / 32] bits
+  uint32_t* list = used + kFewRows / 32;                           // [kFewTokens]
+  uint32_t* sorted = list + kFewTokens;                            // [kFewTokens]
+  float* part = (float*)(sorted + kFewTokens);                     // [kFewWaves][2][kSeg]
+  const uint32_t tid = threadIdx.x, lane = tid & 63;
+  const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t lo = blockIdx.x * R, rows = vocab - lo < R ? vocab - lo : R;
+  const uint64_t c0 = (uint64_t)blockIdx.y * kSeg;
+  const int64_t id = ids[tid < tokens ? tid : 0];
+  const bool in = tid < tokens && id != padding && id >= (int64_t)lo && id < (int64_t)lo + rows;
+  const uint64_t mask = __ballot(in);
+  if (tid < kFewRows / 32) used[tid] = 0;
+  if (lane == 0) count[w] = (uint32_t)__popcll(mask);
   __syncthreads();
-  if (w != 0) return;
-  for (int k = 1; k < kJoinWaves; ++k) acc.add(load_partial<E>(mine + k * kSeg));
-  finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
+  uint32_t at = (uint32_t)__popcll(mask & lanes_before()), total = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < kFewWaves; ++k) {
+    if (k < w) at += count[k];
+    total += count[k];
+  }
+  total = (uint32_t)__builtin_amdgcn_readfirstlane(total);
+  if (in) {
+    const uint32_t r = (uint32_t)id - lo;
+    list[at] = r << 10 | tid;
+    atomicOr(&used[r >> 5], 1u << (r & 31));
+  }
+  __syncthreads();
+  if (tid < total) {
+    const uint32_t e = list[tid];
+    uint32_t rank = 0;
+#pragma unroll 4
+    for (uint32_t k = 0; k < total; ++k) rank += list[k] < e;
+    sorted[rank] = e;
+  }
+  if (!accumulate)
+    for (uint32_t r = w; r < rows; r += kFewWaves)
+      if (!(used[r >> 5] >> (r & 31) & 1u)) store_seg<DO, E>(dw.p, (uint64_t)(lo + r) * dw.stride, c0, dim, SegCols<E>{});
+  if (total == 0) return;
+  __syncthreads();
+  // pieces of ch entries, the w-th this wavefront's
+  const uint32_t ch = (total + kFewWaves - 1) / kFewWaves;
+  const uint32_t i0 = w * ch, i1 = i0 + ch < total ? i0 + ch : total;
+  float* mine = part + lane * 4;
+  bool begins = false;  // a run begins in this piece and goes on in the next
+  uint32_t row = 0;
+  if (i0 < i1) {
+    row = sorted[i0] >> 10;
+    bool head = i0 > 0 && sorted[i0 - 1] >> 10 == row;
+    const bool cut = i1 < total && sorted[i1] >> 10 == sorted[i1 - 1] >> 10;
+    SegCols<E> acc = {};
+    for (uint32_t b = i0; b < i1; b += kBatch) {
+      const int m = i1 - b < (uint32_t)kBatch ? (int)(i1 - b) : kBatch;
+      uint32_t e[kBatch];
+      SegCols<E> g[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) e[k] = (uint32_t)__builtin_amdgcn_readfirstlane(sorted[b + (k < m ? k : 0)]);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k < m) g[k] = load_seg<DI, E>(dout.p, (uint64_t)(e[k] & 1023u) * dout.stride, c0, dim);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (k >= m) break;
+        if (e[k] >> 10 != row) {  // uniform
+          if (head) store_partial(mine + w * 2 * kSeg, acc);
+          else finish_row<DO, E>(dw, lo + row, c0, dim, scale, accumulate, acc);
+          head = false;
+          row = e[k] >> 10;
+          acc = SegCols<E>{};
+        }
+        acc.add(g[k]);
+      }
+    }
+    begins = cut && !head;
+    if (head) store_partial(mine + w * 2 * kSeg, acc);
+    else if (cut) store_partial(mine + (w * 2 + 1) * kSeg, acc);
+    else finish_row<DO, E>(dw, lo + row, c0, dim, scale, accumulate, acc);
+  }
+  __syncthreads();
+  if (!begins) return;
+  SegCols<E> acc = load_partial<E>(mine + (w * 2 + 1) * kSeg);
+  for (uint32_t k = w + 1; k * ch < total && sorted[k * ch] >> 10 == row; ++k)
+    acc.add(load_partial<E>(mine + k * 2 * kSeg));
+  finish_row<DO, E>(dw, lo + row, c0, dim, scale, accumulate, acc);
 }
 
 template <int DI, int DO>
-hipError_t embedding_grad_typed(const Rows& dout, uint64_t vocab, const TokenSort& sort, const Pieces& pc, float scale,
-                                bool accumulate, const Rows& dw, hipStream_t stream) {
-  const uint64_t units = (uint64_t)pc.n * pc.segs + (accumulate ? 0 : vocab);
+hipError_t embedding_grad_few(const Rows& dout, const void* ids, bool ids64, uint64_t tokens, uint64_t vocab,
+                              uint64_t dim, int64_t padding, float scale, bool accumulate, const Rows& dw,
+                              hipStream_t stream) {
+  const uint64_t segs = (dim + kSeg - 1) / kSeg;
+  // two workgroups per CU, each of at least a row per wavefront
+  uint64_t R = (vocab * segs + 511) / 512;
+  R = R < kFewWaves ? kFewWaves : (R > kFewRows ? kFewRows : R);
+  const dim3 grid((unsigned)((vocab + R - 1) / R), (unsigned)segs), block(kFewTokens);
+  const size_t lds = (kFewWaves + kFewRows / 32 + 2 * kFewTokens + kFewWaves * 2 * kSeg) * sizeof(uint32_t);
+  if (ids64)
+    hipLaunchKernelGGL((embedding_grad_few_kernel<DI, DO, int64_t>), grid, block, lds, stream, dout,
+                       (const int64_t*)ids, (uint32_t)tokens, (uint32_t)vocab, dim, padding, (uint32_t)R, scale,
+                       accumulate, dw);
+  else
+    hipLaunchKernelGGL((embedding_grad_few_kernel<DI, DO, int32_t>), grid, block, lds, stream, dout,
+                       (const int32_t*)ids, (uint32_t)tokens, (uint32_t)vocab, dim, padding, (uint32_t)R, scale,
+                       accumulate, dw);
+  return launch_status(stream);
+}
+
+template <int DI, int DO>
+hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
+  if (a.tokens == 0 && a.accumulate) return hipSuccess;
+  if (a.tokens > 0 && a.tokens <= kFewTokens && a.dim <= (uint64_t)kSeg * 65535)
+    return embedding_grad_few<DI, DO>(a.dout, a.ids, a.ids64, a.tokens, a.vocab, a.dim, a.padding, a.scale,
+                                      a.accumulate, a.dweight, stream);
+  hipError_t e = token_sort(a.ids, a.ids64, a.tokens, a.vocab, a.padding, a.sort, stream);
+  if (e != hipSuccess) return e;
+  const uint64_t ch = embedding_piece(a.tokens, a.dim);
+  const Pieces pc{(uint32_t)ch, (uint32_t)((a.tokens + ch - 1) / ch), (uint32_t)((a.dim + kSeg - 1) / kSeg), a.dim,
+                  a.partials};
+  const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : a.vocab);
   constexpr int waves = kThreads / 64;
-  if (units) {
-    hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads),
-                       0, stream, dout, vocab, sort.start, sort.entries, pc, scale, accumulate, dw);
-    const hipError_t e = launch_status(stream);
-    if (e != hipSuccess || pc.n < 2) return e;
-  }
-  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3((pc.n - 1) * pc.segs),
-                     dim3(kJoinWaves * 64), kJoinWaves * kSeg * sizeof(float), stream, vocab, sort.start, sort.entries,
-                     pc, scale, accumulate, dw);
+  hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads), 0,
+                     stream, a.dout, a.vocab, a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
+  if ((e = launch_status(stream)) != hipSuccess || pc.n < 2) return e;
+  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3(pc.n - 1), dim3(kJoinWaves * 64),
+                     kJoinWaves * kSeg * sizeof(float), stream, a.vocab, a.sort.start, a.sort.entries, pc, a.scale,
+                     a.accumulate, a.dweight);
   return launch_status(stream);
 }
 
 template <int DI>
-hipError_t embedding_grad_to(const Rows& dout, uint64_t vocab, const TokenSort& sort, const Pieces& pc, float scale,
-                             bool accumulate, const Rows& dw, hipStream_t stream) {
-  switch (dw.dt) {
-    case DT_F32: return embedding_grad_typed<DI, DT_F32>(dout, vocab, sort, pc, scale, accumulate, dw, stream);
-    case DT_F16: return embedding_grad_typed<DI, DT_F16>(dout, vocab, sort, pc, scale, accumulate, dw, stream);
-    default: return embedding_grad_typed<DI, DT_BF16>(dout, vocab, sort, pc, scale, accumulate, dw, stream);
+hipError_t embedding_grad_to(const EmbeddingGrad& a, hipStream_t stream) {
+  switch (a.dweight.dt) {
+    case DT_F32: return embedding_grad_typed<DI, DT_F32>(a, stream);
+    case DT_F16: return embedding_grad_typed<DI, DT_F16>(a, stream);
+    default: return embedding_grad_typed<DI, DT_BF16>(a, stream);
   }
 }
 
@@ -420,24 +616,6 @@ hipError_t launch_embedding(const Rows& weight, uint64_t vocab, uint64_t dim, co
                : embedding_ids<int32_t>(weight, vocab, dim, ids, tokens, scale, out, stream);
 }
 
-hipError_t launch_token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t vocab, int64_t padding,
-                             const TokenSort& sort, hipStream_t stream) {
-  uint32_t R = (uint32_t)((vocab + 255) / 256);
-  if (R < 16) R = 16;
-  if (R > kSortMaxRows) R = kSortMaxRows;
-  int rbits = 1;
-  while ((1u << rbits) < R) ++rbits;
-  const uint32_t grid = (uint32_t)((vocab + R - 1) / R);
-  const size_t lds = ((size_t)kSortWaves * R + kSortWaves) * sizeof(uint32_t);
-  if (ids64)
-    hipLaunchKernelGGL(token_sort_kernel<int64_t>, dim3(grid), dim3(kSortThreads), lds, stream, (const int64_t*)ids,
-                       (uint32_t)tokens, (uint32_t)vocab, padding, R, rbits, sort);
-  else
-    hipLaunchKernelGGL(token_sort_kernel<int32_t>, dim3(grid), dim3(kSortThreads), lds, stream, (const int32_t*)ids,
-                       (uint32_t)tokens, (uint32_t)vocab, padding, R, rbits, sort);
-  return launch_status(stream);
-}
-
 uint64_t embedding_piece(uint64_t tokens, uint64_t dim) {
   // short pieces while that gives wavefronts to fill the chip (16 per CU),
   // longer ones for long batches: fewer partials
@@ -447,16 +625,11 @@ uint64_t embedding_piece(uint64_t tokens, uint64_t dim) {
   return ch;
 }
 
-hipError_t launch_embedding_grad(const Rows& dout, uint64_t tokens, uint64_t vocab, uint64_t dim,
-                                 const TokenSort& sort, float* partials, float scale, bool accumulate,
-                                 const Rows& dweight, hipStream_t stream) {
-  const uint64_t ch = embedding_piece(tokens, dim);
-  const Pieces pc{(uint32_t)ch, (uint32_t)((tokens + ch - 1) / ch), (uint32_t)((dim + kSeg - 1) / kSeg), dim, partials};
-  if (accumulate && tokens == 0) return hipSuccess;
-  switch (dout.dt) {
-    case DT_F32: return embedding_grad_to<DT_F32>(dout, vocab, sort, pc, scale, accumulate, dweight, stream);
-    case DT_F16: return embedding_grad_to<DT_F16>(dout, vocab, sort, pc, scale, accumulate, dweight, stream);
-    default: return embedding_grad_to<DT_BF16>(dout, vocab, sort, pc, scale, accumulate, dweight, stream);
+hipError_t launch_embedding_grad(const EmbeddingGrad& a, hipStream_t stream) {
+  switch (a.dout.dt) {
+    case DT_F32: return embedding_grad_to<DT_F32>(a, stream);
+    case DT_F16: return embedding_grad_to<DT_F16>(a, stream);
+    default: return embedding_grad_to<DT_BF16>(a, stream);
   }
 }
 

@@ -276,12 +276,20 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   const size_t pieces = (tokens + embedding_piece(tokens, dim) - 1) / embedding_piece(tokens, dim);
   if (pieces * ((dim + 511) / 512) + vocab > kMaxUnits) return RAR_ENOTSUP;
   char* base = (char*)workspace;
-  const TokenSort sort{(uint32_t*)base, (TokenEntry*)(base + l.entries)};
-  hipStream_t st = (hipStream_t)stream;
-  if ((rc = hip_rc(launch_token_sort(ids, id_type == RAR_I64, tokens, vocab, padding_id, sort, st)))) return rc;
-  return hip_rc(launch_embedding_grad(Rows{(char*)dout, dout_stride, dout_dtype}, tokens, vocab, dim, sort,
-                                      (float*)(base + l.partials), scale, accumulate != 0,
-                                      Rows{(char*)dweight, dweight_stride, dweight_dtype}, st));
+  EmbeddingGrad a{};
+  a.dout = Rows{(char*)dout, dout_stride, dout_dtype};
+  a.dweight = Rows{(char*)dweight, dweight_stride, dweight_dtype};
+  a.ids = ids;
+  a.tokens = tokens;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.padding = padding_id;
+  a.sort = TokenSort{(uint32_t*)base, (TokenEntry*)(base + l.entries)};
+  a.partials = (float*)(base + l.partials);
+  a.scale = scale;
+  a.ids64 = id_type == RAR_I64;
+  a.accumulate = accumulate != 0;
+  return hip_rc(launch_embedding_grad(a, (hipStream_t)stream));
 }
 
 // ------------------------------------------------------------------ layer norm

@@ -49,14 +49,20 @@ struct TokenSort {
   uint32_t* start;
   TokenEntry* entries;
 };
-hipError_t launch_token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t vocab, int64_t padding,
-                             const TokenSort& sort, hipStream_t stream);
 // Entries that one wavefront of the gradient takes; partials holds two rows
 // of dim floats, rounded up to 512, for each such piece.
 uint64_t embedding_piece(uint64_t tokens, uint64_t dim);
-hipError_t launch_embedding_grad(const Rows& dout, uint64_t tokens, uint64_t vocab, uint64_t dim,
-                                 const TokenSort& sort, float* partials, float scale, bool accumulate,
-                                 const Rows& dweight, hipStream_t stream);
+struct EmbeddingGrad {
+  Rows dout, dweight;
+  const void* ids;
+  uint64_t tokens, vocab, dim;
+  int64_t padding;
+  TokenSort sort;
+  float* partials;
+  float scale;
+  bool ids64, accumulate;
+};
+hipError_t launch_embedding_grad(const EmbeddingGrad& a, hipStream_t stream);
 
 // -------------------------------------------------------------- layer norm (layernorm_kernels.hip)
 
