@@ -46,8 +46,22 @@ __device__ __forceinline__ SegCols<E> load_seg(const char* base, uint64_t row, u
   }
   return s;
 }
-template <int DT, int E>
+// WT: segments on 16-byte boundaries are stored write-through.
+template <int DT, int E, bool WT>
 __device__ __forceinline__ void store_seg(char* base, uint64_t row, uint64_t c0, uint64_t dim, const SegCols<E>& s) {
+  constexpr int ES = DtypeSize<DT>::value;
+  const char* seg = base + (row + c0) * ES;  // the same in all lanes
+  if (WT && ((uint64_t)seg & 15) == 0) {
+    const WtRange range = wt_range(seg, kSeg * ES);
+#pragma unroll
+    for (int j = 0; j < SegCols<E>::V; ++j) {
+      const uint64_t c = seg_col<E>(c0, j);
+      const int n = vec_count<E>(dim, c);
+      if (n == E) store_vec_wt<DT, E>(range, (uint32_t)(c - c0) * ES, s.x[j]);
+      else store_vec_upto<DT, E>(base, row + c, n, s.x[j]);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < SegCols<E>::V; ++j) {
     const uint64_t c = seg_col<E>(c0, j);
@@ -74,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(Rows weight, uint64
 #pragma unroll
       for (int i = 0; i < E; ++i) g.x[j].v[i] *= scale;
   }
-  store_seg<DO, E>(out.p, t * out.stride, c, dim, g);
+  store_seg<DO, E, false>(out.p, t * out.stride, c, dim, g);
 }
 
 template <int DW, int DO, typename ID>
@@ -124,7 +138,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSortKeep = 256;      // owned tokens that a wavefront keeps from the first walk
 constexpr uint32_t kSortMaxRows = 1792;  // counters of 112 KiB, kept tokens of 32: of the CU's 160
 
-constexpr int kSortAhead = 8;            // ids in flight per lane
+constexpr int kSortAhead = 16;           // ids in flight per lane
 
 // Table rows of the tokens t, t + 64, ... below end; kNoRow for a token that
 // counts for none.
@@ -304,7 +318,7 @@ struct Pieces {
 };
 
 // Rounds a finished sum into the table's gradient.
-template <int DO, int E>
+template <int DO, int E, bool WT = true>
 __device__ __forceinline__ void finish_row(const Rows& dw, uint64_t row, uint64_t c0, uint64_t dim, float scale,
                                            bool accumulate, SegCols<E> acc) {
 #pragma unroll
@@ -312,7 +326,7 @@ __device__ __forceinline__ void finish_row(const Rows& dw, uint64_t row, uint64_
 #pragma unroll
     for (int i = 0; i < E; ++i) acc.x[j].v[i] *= scale;
   if (accumulate) acc.add(load_seg<DO, E>(dw.p, row * dw.stride, c0, dim));
-  store_seg<DO, E>(dw.p, row * dw.stride, c0, dim, acc);
+  store_seg<DO, E, WT>(dw.p, row * dw.stride, c0, dim, acc);
 }
 
 // Partial sums: a lane's eight values side by side in one workspace row of
@@ -356,9 +370,8 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   if (u >= units) {  // zero the rows without tokens
     const uint64_t v = u - units;
     if (accumulate || v >= vocab || start[v] != start[v + 1]) return;
-    constexpr int Z = DO == DT_F32 ? 4 : 8;
-    for (uint64_t c = (threadIdx.x & 63) * Z; c < pc.dim; c += 64 * Z)
-      store_vec_upto<DO, Z>(dw.p, v * dw.stride + c, vec_count<Z>(pc.dim, c), VecF<Z>{});
+    for (uint32_t k = 0; k < pc.segs; ++k)
+      store_seg<DO, vec_elems<DO, DO>(), true>(dw.p, v * dw.stride, (uint64_t)k * kSeg, pc.dim, {});
     return;
   }
   const uint32_t p = u / pc.segs;
@@ -397,23 +410,12 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
 }
 
-// Adds up the runs that were cut: the workgroup of the piece in which such a
-// run begins adds the piece's tail and the heads of the pieces up to the
-// run's end.  Up to kJoinAlone of them a wavefront adds alone, each
-// wavefront its own column segments; of more, all wavefronts of the
-// workgroup add consecutive shares, segment by segment, and the shares are
-// added in order.  E is the gradient kernel's: it fixes which columns a
-// lane's partial sums are.
-constexpr uint32_t kJoinWaves = 8, kJoinAlone = 16;
-
-template <int E>
-__device__ __forceinline__ SegCols<E> join_partials(const Pieces& pc, uint32_t first, uint32_t a, uint32_t z,
-                                                    uint64_t c0) {
-  SegCols<E> acc = {};
-#pragma unroll 4
-  for (uint32_t k = a; k < z; ++k) acc.add(load_partial<E>(partial_at<E>(pc, k, k == first, c0)));
-  return acc;
-}
+// Adds up the runs that were cut.  The workgroup of the piece in which such
+// a run begins (and of kJoinSegs column segments) adds the piece's tail and
+// the heads of the pieces up to the run's end: kJoinShares wavefronts per
+// segment each a consecutive share of them, then the shares in order.  E is
+// the gradient kernel's: it fixes which columns a lane's partial sums are.
+constexpr uint32_t kJoinSegs = 4, kJoinShares = 4, kJoinWaves = kJoinSegs * kJoinShares;
 
 template <int DO, int E>
 __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab,
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
                                                                           const TokenEntry* __restrict__ entries,
                                                                           Pieces pc, float scale, bool accumulate,
                                                                           Rows dw) {
-  extern __shared__ float share[];  // [kJoinWaves][kSeg]
+  extern __shared__ float lds[];  // [kJoinWaves][kSeg]
   const uint32_t p = blockIdx.x;
   const uint32_t i0 = p * pc.ch, i1 = i0 + pc.ch;
   const uint32_t total = start[vocab];
@@ -429,27 +431,22 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
   if (i1 >= total || before != row || start[row] < i0) return;
   const uint32_t z = (start[row + 1] - 1) / pc.ch + 1;  // past the run's last piece
   const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (z - p <= kJoinAlone) {
-    for (uint32_t g = w; g < pc.segs; g += kJoinWaves) {
-      const uint64_t c0 = (uint64_t)g * kSeg;
-      finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, join_partials<E>(pc, p, p, z, c0));
-    }
-    return;
+  const uint32_t seg = blockIdx.y * kJoinSegs + w % kJoinSegs, share = w / kJoinSegs;
+  const uint64_t c0 = (uint64_t)seg * kSeg;
+  const uint32_t per = (z - p + kJoinShares - 1) / kJoinShares;
+  const uint32_t a = p + share * per < z ? p + share * per : z, b = a + per < z ? a + per : z;
+  float* mine = lds + w * kSeg + (threadIdx.x & 63) * 4;
+  SegCols<E> acc = {};
+  if (seg < pc.segs) {
+#pragma unroll 8
+    for (uint32_t k = a; k < b; ++k) acc.add(load_partial<E>(partial_at<E>(pc, k, k == p, c0)));
   }
-  const uint32_t per = (z - p + kJoinWaves - 1) / kJoinWaves;
-  const uint32_t a = p + w * per < z ? p + w * per : z, b = a + per < z ? a + per : z;
-  float* mine = share + (threadIdx.x & 63) * 4;
-  for (uint32_t g = 0; g < pc.segs; ++g) {
-    const uint64_t c0 = (uint64_t)g * kSeg;
-    SegCols<E> acc = join_partials<E>(pc, p, a, b, c0);
-    store_partial(mine + w * kSeg, acc);
-    __syncthreads();
-    if (w == 0) {
-      for (uint32_t k = 1; k < kJoinWaves; ++k) acc.add(load_partial<E>(mine + k * kSeg));
-      finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
-    }
-    __syncthreads();
-  }
+  store_partial(mine, acc);
+  __syncthreads();
+  if (share != 0 || seg >= pc.segs) return;
+#pragma unroll
+  for (uint32_t k = 1; k < kJoinShares; ++k) acc.add(load_partial<E>(mine + k * kJoinSegs * kSeg));
+  finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
 }
 
 // ------------------------------------------------------------------ gradient of few tokens
@@ -506,7 +503,7 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
   }
   if (!accumulate)
     for (uint32_t r = w; r < rows; r += kFewWaves)
-      if (!(used[r >> 5] >> (r & 31) & 1u)) store_seg<DO, E>(dw.p, (uint64_t)(lo + r) * dw.stride, c0, dim, SegCols<E>{});
+      if (!(used[r >> 5] >> (r & 31) & 1u)) store_seg<DO, E, false>(dw.p, (uint64_t)(lo + r) * dw.stride, c0, dim, SegCols<E>{});
   if (total == 0) return;
   __syncthreads();
   // pieces of ch entries, the w-th this wavefront's
@@ -534,7 +531,7 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
         if (k >= m) break;
         if (e[k] >> 10 != row) {  // uniform
           if (head) store_partial(mine + w * 2 * kSeg, acc);
-          else finish_row<DO, E>(dw, lo + row, c0, dim, scale, accumulate, acc);
+          else finish_row<DO, E, false>(dw, lo + row, c0, dim, scale, accumulate, acc);
           head = false;
           row = e[k] >> 10;
           acc = SegCols<E>{};
@@ -545,14 +542,14 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
     begins = cut && !head;
     if (head) store_partial(mine + w * 2 * kSeg, acc);
     else if (cut) store_partial(mine + (w * 2 + 1) * kSeg, acc);
-    else finish_row<DO, E>(dw, lo + row, c0, dim, scale, accumulate, acc);
+    else finish_row<DO, E, false>(dw, lo + row, c0, dim, scale, accumulate, acc);
   }
   __syncthreads();
   if (!begins) return;
   SegCols<E> acc = load_partial<E>(mine + (w * 2 + 1) * kSeg);
   for (uint32_t k = w + 1; k * ch < total && sorted[k * ch] >> 10 == row; ++k)
     acc.add(load_partial<E>(mine + k * 2 * kSeg));
-  finish_row<DO, E>(dw, lo + row, c0, dim, scale, accumulate, acc);
+  finish_row<DO, E, false>(dw, lo + row, c0, dim, scale, accumulate, acc);
 }
 
 template <int DI, int DO>
@@ -592,7 +589,7 @@ hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads), 0,
                      stream, a.dout, a.vocab, a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
   if ((e = launch_status(stream)) != hipSuccess || pc.n < 2) return e;
-  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3(pc.n - 1), dim3(kJoinWaves * 64),
+  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3(pc.n - 1, (pc.segs + kJoinSegs - 1) / kJoinSegs), dim3(kJoinWaves * 64),
                      kJoinWaves * kSeg * sizeof(float), stream, a.vocab, a.sort.start, a.sort.entries, pc, a.scale,
                      a.accumulate, a.dweight);
   return launch_status(stream);

@@ -155,7 +155,9 @@ int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, co
   p.result_offset = l.result;
   p.ntiles = l.ntiles;
   if (l.ntiles) {
-    int rc = hip_rc(launch_fill_u64((uint64_t*)workspace, tab.data(), (int)tab.size(), st));
+    const uint64_t none = 0;  // no workgroup has arrived
+    int rc = hip_rc(launch_fill_u64((uint64_t*)((char*)workspace + l.result), &none, 1, st));
+    if (!rc) rc = hip_rc(launch_fill_u64((uint64_t*)workspace, tab.data(), (int)tab.size(), st));
     if (!rc) rc = hip_rc(launch_clip_desc((const uint64_t*)workspace, (char*)workspace + l.descs, nt, l.ntiles, st));
     if (rc) return rc;
   }

@@ -13,11 +13,11 @@ namespace rar {
 struct ClipSet {
   const void* descs;   // one 32-byte descriptor per tile
   void* partials;      // kClipMaxBlocks doubles
-  void* result;        // two floats: the norm and the factor
+  void* result;        // the last clip's factor (binary32) and a count of arrived workgroups, 0 between launches
   uint64_t ntiles;
 };
 constexpr uint32_t kClipTile = 8192;      // elements per tile
-constexpr uint32_t kClipMaxBlocks = 2048;  // workgroups of the norm launch
+constexpr uint32_t kClipMaxBlocks = 256;   // workgroups of the norm launch
 constexpr uint32_t kClipDescBytes = 32;
 // Words of the table that launch_clip_desc reads: per tensor its first tile
 // (and, after the last, the tile count), then per tensor the input address,

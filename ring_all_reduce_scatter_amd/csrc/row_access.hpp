@@ -85,16 +85,24 @@ __device__ __forceinline__ u32x4 pack_vec(const VecF<E>& f) {
   return x;
 }
 
+template <int DT>
+__device__ __forceinline__ u32x2 pack_vec_half(const VecF<4>& f) {
+  return (u32x2){pack_pair<DT>(f.v[0], f.v[1]), pack_pair<DT>(f.v[2], f.v[3])};
+}
+
 // Streaming stores (nontemporal): an output that is not read back soon.
 template <int DT, int E>
 __device__ __forceinline__ void store_vec(char* base, uint64_t elem, const VecF<E>& f) {
   char* p = base + elem * DtypeSize<DT>::value;
-  if constexpr (VecRaw<DT, E>::W == 4) {
-    __builtin_nontemporal_store(pack_vec<DT, E>(f), (u32x4_any*)p);
-  } else {
-    const u32x2 x = {pack_pair<DT>(f.v[0], f.v[1]), pack_pair<DT>(f.v[2], f.v[3])};
-    __builtin_nontemporal_store(x, (u32x2_any*)p);
-  }
+  if constexpr (VecRaw<DT, E>::W == 4) __builtin_nontemporal_store(pack_vec<DT, E>(f), (u32x4_any*)p);
+  else __builtin_nontemporal_store(pack_vec_half<DT>(f), (u32x2_any*)p);
+}
+// The same write-through (st16_wt), off bytes into a range; both must be
+// multiples of the vector's size.
+template <int DT, int E>
+__device__ __forceinline__ void store_vec_wt(WtRange range, uint32_t off, const VecF<E>& f) {
+  if constexpr (VecRaw<DT, E>::W == 4) st16_wt(range, off, pack_vec<DT, E>(f));
+  else st8_wt(range, off, pack_vec_half<DT>(f));
 }
 
 // The same for the first n elements; missing ones read as +0.
