@@ -524,7 +524,7 @@ typedef struct {
   void* workspace;          /* the prepared workspace */
   uint64_t desc_offset;     /* bytes from workspace to the tile descriptors */
   uint64_t partial_offset;  /* ... to the partial sums */
-  uint64_t result_offset;   /* ... to the factor of the last clip */
+  uint64_t result_offset;   /* ... to the counts of arrived workgroups and the last factor */
   uint64_t ntiles;
 } rar_grad_plan;
 

@@ -65,28 +65,30 @@ int check_ptr(const void* p, size_t align) {
 
 // ------------------------------------------------------------------ norm and clip
 
-// Workspace: table, descriptors, partial sums, result.
+// Workspace: table, descriptors, partial sums, then the counts of arrived
+// workgroups and the factor.
+uint64_t clip_tiles(size_t count, int dt) { return (count + clip_tile_elems(dt) - 1) / clip_tile_elems(dt); }
 struct ClipLayout {
-  uint64_t ntiles;
   size_t descs, partials, result, bytes;
 };
 bool clip_layout(const size_t* counts, size_t nt, ClipLayout* l) {
-  l->ntiles = 0;
+  uint64_t ntiles = 0;  // at most: as if every tensor were binary32
   for (size_t t = 0; t < nt; ++t) {
-    if (counts[t] >= (size_t)1 << 46) return false;
-    l->ntiles += (counts[t] + kClipTile - 1) / kClipTile;
+    if (counts[t] >= (size_t)1 << 43) return false;
+    ntiles += clip_tiles(counts[t], RAR_F32);
   }
-  if (nt >= (size_t)1 << 24 || l->ntiles > kMaxGrid) return false;
+  if (nt >= (size_t)1 << 24 || ntiles > kMaxGrid) return false;
   l->descs = round_up((5 * nt + 1) * sizeof(uint64_t), kAlign);
-  l->partials = l->descs + round_up((size_t)l->ntiles * kClipDescBytes, kAlign);
+  l->partials = l->descs + round_up((size_t)ntiles * kClipDescBytes, kAlign);
   l->result = l->partials + kClipMaxBlocks * sizeof(double);
-  l->bytes = l->result + kAlign;
+  l->bytes = l->result + kClipCountBytes + kAlign;
   return true;
 }
 
 ClipSet clip_set(const rar_grad_plan* p) {
   char* ws = (char*)p->workspace;
-  return ClipSet{ws + p->desc_offset, ws + p->partial_offset, ws + p->result_offset, p->ntiles};
+  char* result = ws + p->result_offset;
+  return ClipSet{ws + p->desc_offset, ws + p->partial_offset, result, result + kClipCountBytes, p->ntiles};
 }
 
 int check_plan(const rar_grad_plan* p, int norm_type, double scale, const float* norm) {
@@ -141,7 +143,7 @@ int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, co
   uint64_t tiles = 0;
   for (size_t t = 0; t < nt; ++t) {
     tab[t] = tiles;
-    tiles += (counts[t] + kClipTile - 1) / kClipTile;
+    tiles += clip_tiles(counts[t], dtypes[t]);
     tab[nt + 1 + t] = (uint64_t)(uintptr_t)grads[t];
     tab[2 * nt + 1 + t] = (uint64_t)(uintptr_t)(outs ? outs[t] : grads[t]);
     tab[3 * nt + 1 + t] = counts[t];
@@ -153,12 +155,13 @@ int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, co
   p.desc_offset = l.descs;
   p.partial_offset = l.partials;
   p.result_offset = l.result;
-  p.ntiles = l.ntiles;
-  if (l.ntiles) {
-    const uint64_t none = 0;  // no workgroup has arrived
-    int rc = hip_rc(launch_fill_u64((uint64_t*)((char*)workspace + l.result), &none, 1, st));
+  p.ntiles = tiles;
+  if (tiles) {
+    const uint64_t none[kClipCountBytes / sizeof(uint64_t)] = {};  // no workgroup has arrived
+    int rc = hip_rc(launch_fill_u64((uint64_t*)((char*)workspace + l.result), none,
+                                    (int)(kClipCountBytes / sizeof(uint64_t)), st));
     if (!rc) rc = hip_rc(launch_fill_u64((uint64_t*)workspace, tab.data(), (int)tab.size(), st));
-    if (!rc) rc = hip_rc(launch_clip_desc((const uint64_t*)workspace, (char*)workspace + l.descs, nt, l.ntiles, st));
+    if (!rc) rc = hip_rc(launch_clip_desc((const uint64_t*)workspace, (char*)workspace + l.descs, nt, tiles, st));
     if (rc) return rc;
   }
   *plan = p;

@@ -13,12 +13,15 @@ namespace rar {
 struct ClipSet {
   const void* descs;   // one 32-byte descriptor per tile
   void* partials;      // kClipMaxBlocks doubles
-  void* result;        // the last clip's factor (binary32) and a count of arrived workgroups, 0 between launches
+  void* counts;        // kClipCountBytes: arrived workgroups, zero between launches
+  void* factor;        // the last clip's factor (binary32)
   uint64_t ntiles;
 };
-constexpr uint32_t kClipTile = 8192;      // elements per tile
+constexpr uint32_t kClipTileBytes = 16384;  // of input per tile
+__host__ __device__ constexpr uint32_t clip_tile_elems(int dt) { return kClipTileBytes / (dt == DT_F32 ? 4 : 2); }
 constexpr uint32_t kClipMaxBlocks = 256;   // workgroups of the norm launch
 constexpr uint32_t kClipDescBytes = 32;
+constexpr uint32_t kClipCountBytes = 2048;
 // Words of the table that launch_clip_desc reads: per tensor its first tile
 // (and, after the last, the tile count), then per tensor the input address,
 // the output address, the count and the types (input | output << 8).
