@@ -7,6 +7,8 @@
 // sorted by row first (token_sort_kernel), keeping their order within a
 // row, so that every row's sum is formed in ascending token order in
 // binary32, without atomics: the same inputs give the same bits.
+#include <algorithm>
+
 #include "operator_launch.hpp"
 #include "row_access.hpp"
 
@@ -314,6 +316,7 @@ struct Pieces {
   uint32_t n;       // pieces
   uint32_t segs;    // column segments of kSeg
   uint64_t dim;
+  uint32_t zrows;   // rows that one wavefront looks through for empty ones (at most 64)
   float* partials;  // [n][2][segs * kSeg]: head, tail
 };
 
@@ -367,11 +370,17 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   constexpr int E = vec_elems<DI, DO>();
   const uint32_t u = grid_wave();
   const uint32_t units = pc.n * pc.segs;
-  if (u >= units) {  // zero the rows without tokens
-    const uint64_t v = u - units;
-    if (accumulate || v >= vocab || start[v] != start[v + 1]) return;
-    for (uint32_t k = 0; k < pc.segs; ++k)
-      store_seg<DO, vec_elems<DO, DO>(), true>(dw.p, v * dw.stride, (uint64_t)k * kSeg, pc.dim, {});
+  if (u >= units) {  // zero those of pc.zrows rows that have no tokens
+    const uint32_t lane = threadIdx.x & 63;
+    const uint64_t v0 = (uint64_t)(u - units) * pc.zrows;
+    if (accumulate || v0 >= vocab) return;
+    const uint64_t mine = v0 + lane;
+    const bool empty = lane < pc.zrows && mine < vocab && start[mine] == start[mine + 1];
+    for (uint64_t left = __ballot(empty); left != 0; left &= left - 1) {
+      const uint64_t v = v0 + (uint32_t)__builtin_ctzll(left);
+      for (uint32_t k = 0; k < pc.segs; ++k)
+        store_seg<DO, vec_elems<DO, DO>(), true>(dw.p, v * dw.stride, (uint64_t)k * kSeg, pc.dim, {});
+    }
     return;
   }
   const uint32_t p = u / pc.segs;
@@ -410,12 +419,32 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
 }
 
-// Adds up the runs that were cut.  The workgroup of the piece in which such
-// a run begins (and of kJoinSegs column segments) adds the piece's tail and
-// the heads of the pieces up to the run's end: kJoinShares wavefronts per
-// segment each a consecutive share of them, then the shares in order.  E is
-// the gradient kernel's: it fixes which columns a lane's partial sums are.
-constexpr uint32_t kJoinSegs = 4, kJoinShares = 4, kJoinWaves = kJoinSegs * kJoinShares;
+// Adds up the runs that were cut.  A run belongs to the piece it begins in,
+// whose tail and the heads of the pieces up to the run's end are its parts.
+// A workgroup looks at kJoinPieces pieces, kJoinEach wavefronts each.  Runs
+// of up to kJoinShort parts are added there and then, each wavefront taking
+// every kJoinEach-th column segment; for longer ones all wavefronts of the
+// workgroup come together, kJoinEach for a segment's consecutive shares,
+// which are then added in order.  E is the gradient kernel's: it fixes which
+// columns a lane's partial sums are.
+constexpr uint32_t kJoinWaves = 16, kJoinPieces = 4, kJoinEach = kJoinWaves / kJoinPieces, kJoinShort = 16;
+
+template <int E>
+__device__ __forceinline__ SegCols<E> add_parts(const Pieces& pc, uint32_t p, uint32_t a, uint32_t z, uint64_t c0) {
+  SegCols<E> acc = {};
+  for (uint32_t k0 = a; k0 < z; k0 += kBatch) {  // all loads of a batch in flight, the last one repeated at its end
+    SegCols<E> part[kBatch];
+#pragma unroll
+    for (uint32_t i = 0; i < kBatch; ++i) {
+      const uint32_t k = k0 + i < z ? k0 + i : z - 1;
+      part[i] = load_partial<E>(partial_at<E>(pc, k, k == p, c0));
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kBatch; ++i)
+      if (k0 + i < z) acc.add(part[i]);
+  }
+  return acc;
+}
 
 template <int DO, int E>
 __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab,
@@ -423,30 +452,53 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
                                                                           const TokenEntry* __restrict__ entries,
                                                                           Pieces pc, float scale, bool accumulate,
                                                                           Rows dw) {
-  extern __shared__ float lds[];  // [kJoinWaves][kSeg]
-  const uint32_t p = blockIdx.x;
-  const uint32_t i0 = p * pc.ch, i1 = i0 + pc.ch;
-  const uint32_t total = start[vocab];
-  const uint32_t before = entries[i1 - 1].row, row = entries[i1].row;  // both inside the buffer, in use or not
-  if (i1 >= total || before != row || start[row] < i0) return;
-  const uint32_t z = (start[row + 1] - 1) / pc.ch + 1;  // past the run's last piece
+  extern __shared__ float lds[];                       // [kJoinWaves][kSeg], then per piece its run's end and row
+  uint32_t* run_end = (uint32_t*)(lds + kJoinWaves * kSeg);  // 0: nothing left to add
+  uint32_t* run_row = run_end + kJoinPieces;
   const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t seg = blockIdx.y * kJoinSegs + w % kJoinSegs, share = w / kJoinSegs;
-  const uint64_t c0 = (uint64_t)seg * kSeg;
-  const uint32_t per = (z - p + kJoinShares - 1) / kJoinShares;
-  const uint32_t a = p + share * per < z ? p + share * per : z, b = a + per < z ? a + per : z;
-  float* mine = lds + w * kSeg + (threadIdx.x & 63) * 4;
-  SegCols<E> acc = {};
-  if (seg < pc.segs) {
-#pragma unroll 8
-    for (uint32_t k = a; k < b; ++k) acc.add(load_partial<E>(partial_at<E>(pc, k, k == p, c0)));
+  const uint32_t mine = w / kJoinEach, p = blockIdx.x * kJoinPieces + mine;
+  const uint32_t total = start[vocab];
+  uint32_t row = 0, z = 0;  // z: past the last piece of the run that begins in p and is cut
+  if (p + 1 < pc.n && (p + 1) * pc.ch < total) {
+    const uint32_t i1 = (p + 1) * pc.ch;
+    row = entries[i1].row;
+    if (entries[i1 - 1].row == row && start[row] >= p * pc.ch) z = (start[row + 1] - 1) / pc.ch + 1;
   }
-  store_partial(mine, acc);
+  const bool alone = z != 0 && z - p <= kJoinShort;
+  if (w % kJoinEach == 0) {
+    run_end[mine] = alone ? 0 : z;
+    run_row[mine] = row;
+  }
+  if (alone)
+    for (uint32_t seg = w % kJoinEach; seg < pc.segs; seg += kJoinEach) {
+      const uint64_t c0 = (uint64_t)seg * kSeg;
+      finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, add_parts<E>(pc, p, p, z, c0));
+    }
   __syncthreads();
-  if (share != 0 || seg >= pc.segs) return;
-#pragma unroll
-  for (uint32_t k = 1; k < kJoinShares; ++k) acc.add(load_partial<E>(mine + k * kJoinSegs * kSeg));
-  finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
+  for (uint32_t q = 0; q < kJoinPieces; ++q) {
+    const uint32_t end = (uint32_t)__builtin_amdgcn_readfirstlane(run_end[q]);
+    if (end == 0) continue;
+    const uint32_t first = blockIdx.x * kJoinPieces + q;
+    const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane(run_row[q]);
+    // S segments at a time, 16 / S wavefronts each
+    const uint32_t S = pc.segs < 3 ? pc.segs : 4, shares = kJoinWaves / S;
+    const uint32_t per = (end - first + shares - 1) / shares, share = w / S;
+    const uint32_t a = first + share * per < end ? first + share * per : end, b = a + per < end ? a + per : end;
+    float* at = lds + w * kSeg + (threadIdx.x & 63) * 4;
+    for (uint32_t s0 = 0; s0 < pc.segs; s0 += S) {
+      const uint32_t seg = s0 + w % S;
+      const uint64_t c0 = (uint64_t)seg * kSeg;
+      SegCols<E> acc = {};
+      if (seg < pc.segs) acc = add_parts<E>(pc, first, a, b, c0);
+      store_partial(at, acc);
+      __syncthreads();
+      if (share == 0 && seg < pc.segs) {
+        for (uint32_t k = 1; k < shares; ++k) acc.add(load_partial<E>(at + k * S * kSeg));
+        finish_row<DO, E>(dw, to, c0, pc.dim, scale, accumulate, acc);
+      }
+      __syncthreads();
+    }
+  }
 }
 
 // ------------------------------------------------------------------ gradient of few tokens
@@ -502,8 +554,11 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
     sorted[rank] = e;
   }
   if (!accumulate)
-    for (uint32_t r = w; r < rows; r += kFewWaves)
-      if (!(used[r >> 5] >> (r & 31) & 1u)) store_seg<DO, E, false>(dw.p, (uint64_t)(lo + r) * dw.stride, c0, dim, SegCols<E>{});
+    // whole rows, shared out among the workgroups of these rows
+    for (uint32_t r = w * gridDim.y + blockIdx.y; r < rows; r += kFewWaves * gridDim.y)
+      if (!(used[r >> 5] >> (r & 31) & 1u))
+        for (uint32_t k = 0; k < gridDim.y; ++k)
+          store_seg<DO, vec_elems<DO, DO>(), false>(dw.p, (uint64_t)(lo + r) * dw.stride, (uint64_t)k * kSeg, dim, {});
   if (total == 0) return;
   __syncthreads();
   // pieces of ch entries, the w-th this wavefront's
@@ -582,16 +637,21 @@ hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   hipError_t e = token_sort(a.ids, a.ids64, a.tokens, a.vocab, a.padding, a.sort, stream);
   if (e != hipSuccess) return e;
   const uint64_t ch = embedding_piece(a.tokens, a.dim);
+  // a wavefront zeroes about 8 KiB: one row of 2048 f32 (the whole call takes
+  // 134 us so, 143 with 16 rows), 16 rows of 128 bf16 (44 us; with one, each
+  // wavefront waits for its row's starts for a store of 256 bytes)
+  const uint64_t row_bytes = a.dim * DtypeSize<DO>::value;
+  const uint32_t zrows = row_bytes >= 8192 ? 1 : (uint32_t)std::min<uint64_t>(8192 / row_bytes, 16);
   const Pieces pc{(uint32_t)ch, (uint32_t)((a.tokens + ch - 1) / ch), (uint32_t)((a.dim + kSeg - 1) / kSeg), a.dim,
-                  a.partials};
-  const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : a.vocab);
+                  zrows, a.partials};
+  const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : (a.vocab + zrows - 1) / zrows);
   constexpr int waves = kThreads / 64;
   hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads), 0,
                      stream, a.dout, a.vocab, a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
   if ((e = launch_status(stream)) != hipSuccess || pc.n < 2) return e;
-  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3(pc.n - 1, (pc.segs + kJoinSegs - 1) / kJoinSegs), dim3(kJoinWaves * 64),
-                     kJoinWaves * kSeg * sizeof(float), stream, a.vocab, a.sort.start, a.sort.entries, pc, a.scale,
-                     a.accumulate, a.dweight);
+  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3((pc.n - 1 + kJoinPieces - 1) / kJoinPieces),
+                     dim3(kJoinWaves * 64), (kJoinWaves * kSeg + 2 * kJoinPieces) * sizeof(float), stream, a.vocab,
+                     a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
   return launch_status(stream);
 }
 
