@@ -48,12 +48,14 @@ __device__ __forceinline__ SegCols<E> load_seg(const char* base, uint64_t row, u
   }
   return s;
 }
-// WT: segments on 16-byte boundaries are stored write-through.
+// WT: segments on cache-line boundaries are stored write-through.  (Elsewhere
+// that costs: 32,768 x 1000 f32 tokens into 65,536 rows took 113.6 us with
+// all segments on 16-byte boundaries so, 105.3 us this way.)
 template <int DT, int E, bool WT>
 __device__ __forceinline__ void store_seg(char* base, uint64_t row, uint64_t c0, uint64_t dim, const SegCols<E>& s) {
   constexpr int ES = DtypeSize<DT>::value;
   const char* seg = base + (row + c0) * ES;  // the same in all lanes
-  if (WT && ((uint64_t)seg & 15) == 0) {
+  if (WT && ((uint64_t)seg & 127) == 0) {
     const WtRange range = wt_range(seg, kSeg * ES);
 #pragma unroll
     for (int j = 0; j < SegCols<E>::V; ++j) {

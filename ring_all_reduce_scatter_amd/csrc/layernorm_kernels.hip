@@ -8,10 +8,10 @@
 // mean, not as a difference of moments.  The sums over rows are formed in a
 // fixed order: each of the row groups on its own, then the groups in order.
 //
-// A row stays in the registers of NW wavefronts, V vectors a lane, from its
-// load to its store, so memory is read and written once.  Rows too long for
-// that go through the loops at the end of this file, which read a row once
-// per pass.
+// A row stays in the registers of NT lanes, V vectors a lane, from its load
+// to its store, so memory is read and written once: 16 lanes for short rows,
+// a wavefront, or four or eight of them.  Rows too long for that go through
+// the loops at the end of this file, which read a row once per pass.
 #include <algorithm>
 
 #include "operator_launch.hpp"
@@ -24,16 +24,17 @@ constexpr int kWaves = kThreads / 64;
 
 // ------------------------------------------------------------------ rows in registers
 
-// K sums over the NW wavefronts of a row; every lane receives them.  lds
-// holds 2 * NW * K floats of the row's own; consecutive calls alternate
-// between its halves (turn), so one barrier a call is enough: a wavefront
-// writes a half again only after a barrier that all readers of its last
-// contents have passed.  With one wavefront there is no barrier at all.
-template <int NW, int K>
+// K sums over the NT lanes of a row; every lane receives them.  16 lanes are
+// a DPP row, 64 a wavefront.  Of more, lds holds 2 * (NT / 64) * K floats of
+// the row's own; consecutive calls alternate between its halves (turn), so
+// one barrier a call is enough: a wavefront writes a half again only after a
+// barrier that all readers of its last contents have passed.
+template <int NT, int K>
 __device__ __forceinline__ void row_sums(float* v, float* lds, int& turn) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
-  if constexpr (NW > 1) {
+  for (int k = 0; k < K; ++k) v[k] = NT == 16 ? dpp_row_sum(v[k]) : wave_sum(v[k]);
+  if constexpr (NT > 64) {
+    constexpr int NW = NT / 64;
     float* half = lds + (turn & 1) * NW * K;
     ++turn;
     const int lane = threadIdx.x & 63, w = (int)(threadIdx.x >> 6) % NW;
@@ -51,14 +52,21 @@ __device__ __forceinline__ void row_sums(float* v, float* lds, int& turn) {
   }
 }
 
-// A lane's share of a row of dim elements: V vectors of E, NW * 64 vectors
+// A row's number in its workgroup: the same register for all lanes of a
+// wavefront, unless the wavefront carries several rows.
+template <int NT>
+__device__ __forceinline__ uint32_t row_slot() {
+  const uint32_t slot = threadIdx.x / NT;
+  return NT < 64 ? slot : (uint32_t)__builtin_amdgcn_readfirstlane(slot);
+}
+
+// A lane's share of a row of dim elements: V vectors of E, NT vectors
 // apart, as far as the row has whole vectors, and one of the dim % E
 // elements after them.  A lane without a vector (or element) holds zeros in
 // its place; valid() and tail() tell.
-template <int DT, int NW, int V>
+template <int DT, int NT, int V>
 struct RowShape {
   static constexpr int E = vec_elems<DT, DT>();
-  static constexpr int NT = NW * 64;
   uint32_t lane;  // among the row's NT
   uint32_t nvec, ntail;
   __device__ __forceinline__ RowShape(uint32_t l, uint64_t dim)
@@ -81,9 +89,9 @@ struct RowF {
   float t;
 };
 
-template <int DT, int NW, int V>
-__device__ __forceinline__ void load_row(const RowShape<DT, NW, V>& sh, const char* row, RowRaw<DT, V>& x) {
-  constexpr int E = RowShape<DT, NW, V>::E;
+template <int DT, int NT, int V>
+__device__ __forceinline__ void load_row(const RowShape<DT, NT, V>& sh, const char* row, RowRaw<DT, V>& x) {
+  constexpr int E = RowShape<DT, NT, V>::E;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     if (sh.valid(j)) x.v[j] = load_raw<DT, E, true>(row, sh.col(j));
@@ -92,15 +100,20 @@ __device__ __forceinline__ void load_row(const RowShape<DT, NW, V>& sh, const ch
   x.t = 0.0f;
   if (sh.tail()) x.t = load_elem<DT>(row, sh.tail_col());
 }
-// Rows on 16-byte boundaries are stored write-through (st16_wt): on 16,384
-// rows the forward pass of 4096 columns takes 47.8 us with it against 48.8
-// with nontemporal stores, the backward pass of 8192 columns 140.5 against
-// 145.9.
-template <int DT, int NW, int V>
-__device__ __forceinline__ void store_row(const RowShape<DT, NW, V>& sh, char* row,
+// Whether every row begins on a cache line.  Such rows are stored
+// write-through (st16_wt), others with nontemporal stores: on 65,536 rows
+// the forward pass of 1000 f32 columns takes 97 us so, 108 with all rows on
+// 16-byte boundaries write-through; on 16,384 rows the backward pass of 8192
+// bf16 columns 140 against 146 with nontemporal stores alone.
+template <int DT>
+__device__ __forceinline__ bool rows_on_lines(const Rows& r) {
+  return (((uint64_t)r.p | r.stride * DtypeSize<DT>::value) & 127) == 0;
+}
+template <int DT, int NT, int V>
+__device__ __forceinline__ void store_row(const RowShape<DT, NT, V>& sh, char* row, bool lines,
                                           const RowF<vec_elems<DT, DT>(), V>& x) {
-  constexpr int E = RowShape<DT, NW, V>::E;
-  if (((uint64_t)row & 15) == 0) {  // uniform: a row's first element
+  constexpr int E = RowShape<DT, NT, V>::E;
+  if (NT >= 64 && lines) {  // uniform, as is the row
     const WtRange range = wt_range(row, sh.nvec * 16);
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -122,10 +135,10 @@ __device__ __forceinline__ RowF<vec_elems<DT, DT>(), V> unpack_row(const RowRaw<
 }
 
 // A weight or bias vector of type WT in a row's shape.
-template <int WT, int DT, int NW, int V>
-__device__ __forceinline__ void load_weight_as(const RowShape<DT, NW, V>& sh, const char* w,
+template <int WT, int DT, int NT, int V>
+__device__ __forceinline__ void load_weight_as(const RowShape<DT, NT, V>& sh, const char* w,
                                                RowF<vec_elems<DT, DT>(), V>& f) {
-  constexpr int E = RowShape<DT, NW, V>::E;
+  constexpr int E = RowShape<DT, NT, V>::E;
 #pragma unroll
   for (int j = 0; j < V; ++j)
     if (sh.valid(j))
@@ -137,15 +150,15 @@ __device__ __forceinline__ void load_weight_as(const RowShape<DT, NW, V>& sh, co
       }
   if (sh.tail()) f.t = load_elem<WT>(w, sh.tail_col());
 }
-template <int DT, int NW, int V>
-__device__ __forceinline__ void load_weight(const RowShape<DT, NW, V>& sh, const void* w, int wdt, float missing,
+template <int DT, int NT, int V>
+__device__ __forceinline__ void load_weight(const RowShape<DT, NT, V>& sh, const void* w, int wdt, float missing,
                                             RowF<vec_elems<DT, DT>(), V>& f) {
   f = {};
   if (w == nullptr) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int i = 0; i < RowShape<DT, NW, V>::E; ++i) f.v[j].v[i] = missing;
+      for (int i = 0; i < RowShape<DT, NT, V>::E; ++i) f.v[j].v[i] = missing;
     f.t = missing;
   } else if (wdt == DT_F32) {
     load_weight_as<DT_F32>(sh, (const char*)w, f);
@@ -156,22 +169,23 @@ __device__ __forceinline__ void load_weight(const RowShape<DT, NW, V>& sh, const
   }
 }
 
-// Forward: a workgroup of NW * RB wavefronts carries RB rows at a time and
+// Forward: a workgroup of NT * RB lanes carries RB rows at a time and
 // strides over the rows; the next row's loads are issued before this one's
 // sums.
-template <int DT, int NW, int V, int RB>
-__global__ __launch_bounds__(NW * RB * 64) void layernorm_row_kernel(Rows x, const void* __restrict__ weight,
+template <int DT, int NT, int V, int RB>
+__global__ __launch_bounds__(NT * RB) void layernorm_row_kernel(Rows x, const void* __restrict__ weight,
                                                                       const void* __restrict__ bias, int wdt,
                                                                       uint64_t rows, uint64_t dim, float eps, Rows y,
                                                                       float* __restrict__ mean,
                                                                       float* __restrict__ rstd) {
   extern __shared__ float lds[];
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
-  const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / (NW * 64));
-  const RowShape<DT, NW, V> sh(threadIdx.x % (NW * 64), dim);
-  float* red = lds + slot * 2 * NW;
+  const uint32_t slot = row_slot<NT>();
+  const RowShape<DT, NT, V> sh(threadIdx.x % NT, dim);
+  float* red = lds + slot * (2 * NT / 64);
   int turn = 0;
   const uint64_t step = (uint64_t)gridDim.x * RB;
+  const bool lines = rows_on_lines<DT>(y);
   uint64_t r = (uint64_t)blockIdx.x * RB + slot;
   RowRaw<DT, V> raw;
   load_row(sh, x.p + (r < rows ? r : rows - 1) * x.stride * ES, raw);
@@ -187,7 +201,7 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_row_kernel(Rows x, con
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int i = 0; i < E; ++i) s += v.v[j].v[i];
-    row_sums<NW, 1>(&s, red, turn);
+    row_sums<NT, 1>(&s, red, turn);
     const float mu = s / (float)dim;
     v.t -= mu;
     float q = sh.tail() ? v.t * v.t : 0.0f;
@@ -199,7 +213,7 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_row_kernel(Rows x, con
 #pragma unroll
         for (int i = 0; i < E; ++i) q = __builtin_fmaf(v.v[j].v[i], v.v[j].v[i], q);
     }
-    row_sums<NW, 1>(&q, red, turn);
+    row_sums<NT, 1>(&q, red, turn);
     const float rs = 1.0f / __builtin_sqrtf(q / (float)dim + eps);
     if (r < rows) {
 #pragma unroll
@@ -207,7 +221,7 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_row_kernel(Rows x, con
 #pragma unroll
         for (int i = 0; i < E; ++i) v.v[j].v[i] = __builtin_fmaf(v.v[j].v[i] * rs, w.v[j].v[i], b.v[j].v[i]);
       v.t = __builtin_fmaf(v.t * rs, w.t, b.t);
-      store_row(sh, y.p + r * y.stride * ES, v);
+      store_row(sh, y.p + r * y.stride * ES, lines, v);
       if (sh.lane == 0) {
         if (mean) mean[r] = mu;
         if (rstd) rstd[r] = rs;
@@ -219,16 +233,17 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_row_kernel(Rows x, con
 // Backward: the same walk over the rows with the sums of dy h and dy over
 // the workgroup's rows kept in registers; at the end the RB row slots are
 // added (through LDS) and stored as the workgroup's partial sums.
-template <int DT, int NW, int V, int RB>
-__global__ __launch_bounds__(NW * RB * 64) void layernorm_grad_row_kernel(LayernormGrad a, uint64_t rows,
+template <int DT, int NT, int V, int RB>
+__global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGrad a, uint64_t rows,
                                                                            uint64_t dim) {
   extern __shared__ float lds[];
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
-  const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / (NW * 64));
-  const RowShape<DT, NW, V> sh(threadIdx.x % (NW * 64), dim);
-  float* red = lds + slot * 4 * NW;
+  const uint32_t slot = row_slot<NT>();
+  const RowShape<DT, NT, V> sh(threadIdx.x % NT, dim);
+  float* red = lds + slot * (4 * NT / 64);
   int turn = 0;
   const uint64_t step = (uint64_t)gridDim.x * RB;
+  const bool lines = rows_on_lines<DT>(a.dx);
   uint64_t r = (uint64_t)blockIdx.x * RB + slot;
   RowRaw<DT, V> rx, ry;
   float mu_next, rs_next;
@@ -244,7 +259,7 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_grad_row_kernel(Layern
   load_weight(sh, a.weight, a.wdt, 1.0f, w);
   for (uint64_t r0 = (uint64_t)blockIdx.x * RB; r0 < rows; r0 += step, r += step) {
     const float mu = mu_next, rs = rs_next;
-    const bool live = r < rows;  // uniform over the row's wavefronts
+    const bool live = r < rows;
     // where the row has no element dy is zero, so it adds to no sum
     RowF<E, V> h = unpack_row<DT, V>(rx), g = unpack_row<DT, V>(ry);
 #pragma unroll
@@ -279,7 +294,7 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_grad_row_kernel(Layern
     }
     if (r0 + step < rows) fetch(r + step);
     if (a.dx.p == nullptr) continue;  // uniform
-    row_sums<NW, 2>(s, red, turn);
+    row_sums<NT, 2>(s, red, turn);
     const float mg = s[0] / (float)dim, mgh = s[1] / (float)dim;
     if (live) {
 #pragma unroll
@@ -287,15 +302,15 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_grad_row_kernel(Layern
 #pragma unroll
         for (int i = 0; i < E; ++i) g.v[j].v[i] = rs * (g.v[j].v[i] - mg - h.v[j].v[i] * mgh);
       g.t = rs * (g.t - mg - h.t * mgh);
-      store_row(sh, a.dx.p + r * a.dx.stride * ES, g);
+      store_row(sh, a.dx.p + r * a.dx.stride * ES, lines, g);
     }
   }
   if (!a.dweight && !a.dbias) return;
   // the row slots' sums, halving the slots each time: the upper half hands
   // its sums to the lower through LDS (in a fixed order like any other)
   if constexpr (RB > 1) {
-    constexpr int kCols = NW * 64 * (V * E + 1);
-    float* sum = lds + RB * 4 * NW;  // [RB / 2][2][kCols]
+    constexpr int kCols = NT * (V * E + 1);
+    float* sum = lds + RB * 4 * NT / 64;  // [RB / 2][2][kCols]
 #pragma unroll
     for (int half = RB / 2; half >= 1; half /= 2) {
       const bool gives = slot >= (uint32_t)half && slot < 2u * half;
@@ -306,11 +321,11 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_grad_row_kernel(Layern
         for (int j = 0; j < V; ++j)
 #pragma unroll
           for (int i = 0; i < E; ++i) {
-            at[(j * E + i) * NW * 64] = dw.v[j].v[i];
-            at[(j * E + i) * NW * 64 + kCols] = db.v[j].v[i];
+            at[(j * E + i) * NT] = dw.v[j].v[i];
+            at[(j * E + i) * NT + kCols] = db.v[j].v[i];
           }
-        at[V * E * NW * 64] = dw.t;
-        at[V * E * NW * 64 + kCols] = db.t;
+        at[V * E * NT] = dw.t;
+        at[V * E * NT + kCols] = db.t;
       }
       __syncthreads();
       if (slot < (uint32_t)half) {
@@ -318,11 +333,11 @@ __global__ __launch_bounds__(NW * RB * 64) void layernorm_grad_row_kernel(Layern
         for (int j = 0; j < V; ++j)
 #pragma unroll
           for (int i = 0; i < E; ++i) {
-            dw.v[j].v[i] += at[(j * E + i) * NW * 64];
-            db.v[j].v[i] += at[(j * E + i) * NW * 64 + kCols];
+            dw.v[j].v[i] += at[(j * E + i) * NT];
+            db.v[j].v[i] += at[(j * E + i) * NT + kCols];
           }
-        dw.t += at[V * E * NW * 64];
-        db.t += at[V * E * NW * 64 + kCols];
+        dw.t += at[V * E * NT];
+        db.t += at[V * E * NT + kCols];
       }
       __syncthreads();
     }
@@ -473,15 +488,15 @@ unsigned row_grid(uint64_t rows) { return (unsigned)(rows < 65536 ? rows : 65536
 constexpr uint64_t kGradGroups = 256;
 uint64_t grad_groups(uint64_t rows, int rb) { return std::min<uint64_t>(kGradGroups, (rows + rb - 1) / rb); }
 
-template <int DT, int NW, int V, int RB>
+template <int DT, int NT, int V, int RB>
 hipError_t forward_rows(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
                         float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream) {
   // twelve wavefronts per CU: 46.6 us for 16,384 x 4096 in binary16, against
   // 50.6 with eight and 48.8 with sixteen
-  constexpr uint64_t per_cu = 12 / (NW * RB) > 0 ? 12 / (NW * RB) : 1;
+  constexpr uint64_t waves = NT * RB / 64, per_cu = waves < 12 ? 12 / waves : 1;
   const uint64_t groups = std::min<uint64_t>((rows + RB - 1) / RB, 256 * per_cu);
-  hipLaunchKernelGGL((layernorm_row_kernel<DT, NW, V, RB>), dim3((unsigned)groups), dim3(NW * RB * 64),
-                     RB * 2 * NW * sizeof(float), stream, x, weight, bias, wdt, rows, dim, eps, y, mean, rstd);
+  hipLaunchKernelGGL((layernorm_row_kernel<DT, NT, V, RB>), dim3((unsigned)groups), dim3(NT * RB),
+                     RB * 2 * NT / 64 * sizeof(float), stream, x, weight, bias, wdt, rows, dim, eps, y, mean, rstd);
   return launch_status(stream);
 }
 
@@ -489,16 +504,18 @@ template <int DT>
 hipError_t layernorm_dt(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
                         float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream) {
   const uint64_t vecs = dim / vec_elems<DT, DT>();
-#define RAR_FORWARD(NW, V, RB) \
-  return forward_rows<DT, NW, V, RB>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream)
-  if (vecs <= 64) RAR_FORWARD(1, 1, 4);
-  if (vecs <= 128) RAR_FORWARD(1, 2, 4);
-  if (vecs <= 256) RAR_FORWARD(1, 4, 4);
-  if (vecs <= 512) RAR_FORWARD(4, 2, 1);
-  if (vecs <= 1024) RAR_FORWARD(4, 4, 1);
-  if (vecs <= 2048) RAR_FORWARD(8, 4, 1);
+#define RAR_FORWARD(NT, V, RB) \
+  return forward_rows<DT, NT, V, RB>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream)
+  if (vecs <= 16) RAR_FORWARD(16, 1, 16);
+  if (vecs <= 32) RAR_FORWARD(16, 2, 16);
+  if (vecs <= 64) RAR_FORWARD(64, 1, 4);
+  if (vecs <= 128) RAR_FORWARD(64, 2, 4);
+  if (vecs <= 256) RAR_FORWARD(64, 4, 4);
+  if (vecs <= 512) RAR_FORWARD(256, 2, 1);
+  if (vecs <= 1024) RAR_FORWARD(256, 4, 1);
+  if (vecs <= 2048) RAR_FORWARD(512, 4, 1);
   if constexpr (DT == DT_F32)
-    if (vecs <= 4096) RAR_FORWARD(8, 8, 1);
+    if (vecs <= 4096) RAR_FORWARD(512, 8, 1);
 #undef RAR_FORWARD
   hipLaunchKernelGGL((layernorm_kernel<DT>), dim3(row_grid(rows)), dim3(kThreads), kWaves * sizeof(float), stream, x,
                      weight, bias, wdt, rows, dim, eps, y, mean, rstd);
@@ -512,11 +529,11 @@ hipError_t join_partials(const LayernormGrad& a, uint64_t splits, uint64_t dim, 
   return launch_status(stream);
 }
 
-template <int DT, int NW, int V, int RB>
+template <int DT, int NT, int V, int RB>
 hipError_t backward_rows(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
   const uint64_t groups = grad_groups(rows, RB);
-  const size_t lds = (RB * 4 * NW + RB / 2 * 2 * NW * 64 * (V * vec_elems<DT, DT>() + 1)) * sizeof(float);
-  hipLaunchKernelGGL((layernorm_grad_row_kernel<DT, NW, V, RB>), dim3((unsigned)groups), dim3(NW * RB * 64), lds,
+  const size_t lds = (RB * 4 * NT / 64 + RB / 2 * 2 * NT * (V * vec_elems<DT, DT>() + 1)) * sizeof(float);
+  hipLaunchKernelGGL((layernorm_grad_row_kernel<DT, NT, V, RB>), dim3((unsigned)groups), dim3(NT * RB), lds,
                      stream, a, rows, dim);
   const hipError_t e = launch_status(stream);
   return e != hipSuccess ? e : join_partials(a, groups, dim, stream);
@@ -526,12 +543,14 @@ template <int DT>
 hipError_t layernorm_grad_dt(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
   if (rows == 0) return join_partials(a, 0, dim, stream);
   const uint64_t vecs = dim / vec_elems<DT, DT>();
-  if (vecs <= 64) return backward_rows<DT, 1, 1, 8>(a, rows, dim, stream);
-  if (vecs <= 128) return backward_rows<DT, 1, 2, 8>(a, rows, dim, stream);
-  if (vecs <= 256) return backward_rows<DT, 1, 4, 8>(a, rows, dim, stream);
-  if (vecs <= 512) return backward_rows<DT, 4, 2, 2>(a, rows, dim, stream);
-  if (vecs <= 1024) return backward_rows<DT, 4, 4, 2>(a, rows, dim, stream);
-  if (vecs <= 2048) return backward_rows<DT, 8, 4, 1>(a, rows, dim, stream);
+  if (vecs <= 16) return backward_rows<DT, 16, 1, 32>(a, rows, dim, stream);
+  if (vecs <= 32) return backward_rows<DT, 16, 2, 32>(a, rows, dim, stream);
+  if (vecs <= 64) return backward_rows<DT, 64, 1, 8>(a, rows, dim, stream);
+  if (vecs <= 128) return backward_rows<DT, 64, 2, 8>(a, rows, dim, stream);
+  if (vecs <= 256) return backward_rows<DT, 64, 4, 8>(a, rows, dim, stream);
+  if (vecs <= 512) return backward_rows<DT, 256, 2, 2>(a, rows, dim, stream);
+  if (vecs <= 1024) return backward_rows<DT, 256, 4, 2>(a, rows, dim, stream);
+  if (vecs <= 2048) return backward_rows<DT, 512, 4, 1>(a, rows, dim, stream);
   hipError_t e = hipSuccess;
   // dw and db first: dx may be written over dy or x
   if (a.dweight || a.dbias) {

@@ -157,8 +157,9 @@ __device__ __forceinline__ void store_elem_dt(char* base, uint64_t i, int dt, fl
   else store_elem<DT_BF16>(base, i, x);
 }
 
-// Sum over the 64 lanes of a wavefront (all active); every lane receives it.
-// Inside a row of 16 lanes by DPP moves, then the four rows by scalar reads.
+// Sums over a DPP row of 16 lanes, and over the 64 lanes of a wavefront (all
+// active); every lane receives its own.  The four rows of a wavefront are
+// joined by scalar reads.
 template <int CTRL>
 __device__ __forceinline__ float dpp_f32(float v) {
   return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
@@ -166,11 +167,15 @@ __device__ __forceinline__ float dpp_f32(float v) {
 __device__ __forceinline__ float lane_f32(float v, int lane) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
 }
-__device__ __forceinline__ float wave_sum(float v) {
+__device__ __forceinline__ float dpp_row_sum(float v) {
   v += dpp_f32<kDppQuad1032>(v);
   v += dpp_f32<kDppQuad2301>(v);
   v += dpp_f32<kDppRowHalfMirror>(v);
   v += dpp_f32<kDppRowMirror>(v);
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_row_sum(v);
   return (lane_f32(v, 0) + lane_f32(v, 16)) + (lane_f32(v, 32) + lane_f32(v, 48));
 }
 __device__ __forceinline__ double wave_sum(double v) {
