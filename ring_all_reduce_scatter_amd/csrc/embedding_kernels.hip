@@ -314,7 +314,8 @@ hipError_t token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t voc
 // Rows without tokens are zeroed by further wavefronts of the same launch.
 
 struct Pieces {
-  uint32_t ch;      // entries per piece (a power of two)
+  uint32_t tokens;
+  uint32_t ch;      // entries per piece (a power of two, at most 64)
   uint32_t n;       // pieces
   uint32_t segs;    // column segments of kSeg
   uint64_t dim;
@@ -362,7 +363,7 @@ __device__ __forceinline__ SegCols<E> load_partial(const float* p) {
   return s;
 }
 
-constexpr int kBatch = 8;  // rows of dout in flight per wavefront
+constexpr uint32_t kBatch = 8;  // rows of dout in flight per wavefront
 
 template <int DI, int DO>
 __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uint64_t vocab,
@@ -389,28 +390,34 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   const uint64_t c0 = (uint64_t)(u - p * pc.segs) * kSeg;
   const uint32_t total = start[vocab];
   const uint32_t i0 = p * pc.ch;
+  // the piece's entries, one a lane, and the rows beside it; past the used
+  // entries the buffer holds anything, which is not looked at
+  const uint32_t lane = threadIdx.x & 63, last = pc.tokens - 1;
+  const TokenEntry own = entries[lane < pc.ch && i0 + lane < last ? i0 + lane : last];
+  const uint32_t row_before = entries[i0 > 0 ? i0 - 1 : 0].row;
+  const uint32_t row_after = entries[i0 + pc.ch < last ? i0 + pc.ch : last].row;
   if (i0 >= total) return;
-  const uint32_t i1 = i0 + pc.ch < total ? i0 + pc.ch : total;
-  uint32_t row = entries[i0].row;
-  bool head = i0 > 0 && entries[i0 - 1].row == row;  // the run began in an earlier piece
-  const bool cut = i1 < total && entries[i1].row == entries[i1 - 1].row;
+  const uint32_t m = i0 + pc.ch < total ? pc.ch : total - i0;
+  auto entry_token = [&](uint32_t i) { return (uint32_t)__builtin_amdgcn_readlane(own.token, i); };
+  auto entry_row = [&](uint32_t i) { return (uint32_t)__builtin_amdgcn_readlane(own.row, i); };
+  uint32_t row = entry_row(0);
+  bool head = i0 > 0 && row_before == row;  // the run began in an earlier piece
+  const bool cut = i0 + m < total && row_after == entry_row(m - 1);
   SegCols<E> acc = {};
-  for (uint32_t b = i0; b < i1; b += kBatch) {
-    const int m = i1 - b < (uint32_t)kBatch ? (int)(i1 - b) : kBatch;
-    TokenEntry e[kBatch];
+  for (uint32_t b = 0; b < m; b += kBatch) {
     SegCols<E> g[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) e[k] = entries[b + (k < m ? k : 0)];
+    for (uint32_t k = 0; k < kBatch; ++k)
+      g[k] = load_seg<DI, E>(dout.p, (uint64_t)entry_token(b + k < m ? b + k : b) * dout.stride, c0, pc.dim);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) g[k] = load_seg<DI, E>(dout.p, (uint64_t)e[k].token * dout.stride, c0, pc.dim);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (k >= m) break;
-      if (e[k].row != row) {  // uniform
+    for (uint32_t k = 0; k < kBatch; ++k) {
+      if (b + k >= m) break;
+      const uint32_t r = entry_row(b + k);
+      if (r != row) {  // uniform
         if (head) store_partial(partial_at<E>(pc, p, 0, c0), acc);
         else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
         head = false;
-        row = e[k].row;
+        row = r;
         acc = SegCols<E>{};
       }
       acc.add(g[k]);
@@ -575,16 +582,16 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
     const bool cut = i1 < total && sorted[i1] >> 10 == sorted[i1 - 1] >> 10;
     SegCols<E> acc = {};
     for (uint32_t b = i0; b < i1; b += kBatch) {
-      const int m = i1 - b < (uint32_t)kBatch ? (int)(i1 - b) : kBatch;
+      const uint32_t m = i1 - b < kBatch ? i1 - b : kBatch;
       uint32_t e[kBatch];
       SegCols<E> g[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) e[k] = (uint32_t)__builtin_amdgcn_readfirstlane(sorted[b + (k < m ? k : 0)]);
+      for (uint32_t k = 0; k < kBatch; ++k) e[k] = (uint32_t)__builtin_amdgcn_readfirstlane(sorted[b + (k < m ? k : 0)]);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
+      for (uint32_t k = 0; k < kBatch; ++k)
         if (k < m) g[k] = load_seg<DI, E>(dout.p, (uint64_t)(e[k] & 1023u) * dout.stride, c0, dim);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (uint32_t k = 0; k < kBatch; ++k) {
         if (k >= m) break;
         if (e[k] >> 10 != row) {  // uniform
           if (head) store_partial(mine + w * 2 * kSeg, acc);
@@ -644,7 +651,7 @@ hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   // wavefront waits for its row's starts for a store of 256 bytes)
   const uint64_t row_bytes = a.dim * DtypeSize<DO>::value;
   const uint32_t zrows = row_bytes >= 8192 ? 1 : (uint32_t)std::min<uint64_t>(8192 / row_bytes, 16);
-  const Pieces pc{(uint32_t)ch, (uint32_t)((a.tokens + ch - 1) / ch), (uint32_t)((a.dim + kSeg - 1) / kSeg), a.dim,
+  const Pieces pc{(uint32_t)a.tokens, (uint32_t)ch, (uint32_t)((a.tokens + ch - 1) / ch), (uint32_t)((a.dim + kSeg - 1) / kSeg), a.dim,
                   zrows, a.partials};
   const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : (a.vocab + zrows - 1) / zrows);
   constexpr int waves = kThreads / 64;

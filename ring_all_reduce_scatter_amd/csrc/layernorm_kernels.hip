@@ -508,7 +508,7 @@ hipError_t layernorm_dt(const Rows& x, const void* weight, const void* bias, int
   return forward_rows<DT, NT, V, RB>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream)
   if (vecs <= 16) RAR_FORWARD(16, 1, 16);
   if (vecs <= 32) RAR_FORWARD(16, 2, 16);
-  if (vecs <= 64) RAR_FORWARD(64, 1, 4);
+  if (vecs <= 64) RAR_FORWARD(16, 4, 16);
   if (vecs <= 128) RAR_FORWARD(64, 2, 4);
   if (vecs <= 256) RAR_FORWARD(64, 4, 4);
   if (vecs <= 512) RAR_FORWARD(256, 2, 1);
@@ -543,9 +543,9 @@ template <int DT>
 hipError_t layernorm_grad_dt(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
   if (rows == 0) return join_partials(a, 0, dim, stream);
   const uint64_t vecs = dim / vec_elems<DT, DT>();
-  if (vecs <= 16) return backward_rows<DT, 16, 1, 32>(a, rows, dim, stream);
-  if (vecs <= 32) return backward_rows<DT, 16, 2, 32>(a, rows, dim, stream);
-  if (vecs <= 64) return backward_rows<DT, 64, 1, 8>(a, rows, dim, stream);
+  if (vecs <= 16) return backward_rows<DT, 16, 1, 64>(a, rows, dim, stream);
+  if (vecs <= 32) return backward_rows<DT, 16, 2, 64>(a, rows, dim, stream);
+  if (vecs <= 64) return backward_rows<DT, 16, 4, 32>(a, rows, dim, stream);
   if (vecs <= 128) return backward_rows<DT, 64, 2, 8>(a, rows, dim, stream);
   if (vecs <= 256) return backward_rows<DT, 64, 4, 8>(a, rows, dim, stream);
   if (vecs <= 512) return backward_rows<DT, 256, 2, 2>(a, rows, dim, stream);
