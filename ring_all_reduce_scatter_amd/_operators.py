@@ -26,15 +26,17 @@ _I32, _I64 = 0, 1
 
 
 def _width(t, what: str) -> int:
-    if t.dim() == 0 or t.shape[-1] == 0:
-        raise ValueError(f"{what} must have rows of at least one element, got shape {tuple(t.shape)}")
-    return t.shape[-1]
+    shape = t.shape
+    if not shape or shape[-1] == 0:
+        raise ValueError(f"{what} must have rows of at least one element, got shape {tuple(shape)}")
+    return shape[-1]
 
 
 def _rows(t, dim: int, what: str):
     """(rows, elements between rows) of a tensor (..., dim)."""
-    if t.dim() == 0 or t.shape[-1] != dim:
-        raise ValueError(f"{what} must have rows of {dim} elements, got shape {tuple(t.shape)}")
+    shape = t.shape
+    if not shape or shape[-1] != dim:
+        raise ValueError(f"{what} must have rows of {dim} elements, got shape {tuple(shape)}")
     if t.is_contiguous():
         return t.numel() // dim, dim
     if dim > 1 and t.stride(-1) != 1:
@@ -62,26 +64,25 @@ def _out_rows(t, dim: int, rows: int, what: str):
 
 
 def _vector(t, n: int, what: str):
-    """A contiguous tensor of n elements, or None."""
-    if t is not None and (t.numel() != n or not t.is_contiguous()):
+    """Address of a contiguous tensor of n elements, None for None."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous with {n} elements, got shape {tuple(t.shape)}")
-
-
-def _floats(t, n: int, what: str):
-    """n contiguous float32 values, or None."""
-    _vector(t, n, what)
-    if t is not None and dtype_code(t) != F32:
-        raise ValueError(f"{what} must be float32, got {t.dtype}")
-
-
-def _dptr(t) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"expected a GPU tensor, got one on {t.device}")
     return t.data_ptr()
 
 
-def _ptr(t):
-    return None if t is None else _dptr(t)
+def _floats(t, n: int, what: str):
+    """Address of n contiguous float32 values, None for None."""
+    if t is not None and dtype_code(t) != F32:
+        raise ValueError(f"{what} must be float32, got {t.dtype}")
+    return _vector(t, n, what)
+
+
+def _on_gpu(*ts):
+    for t in ts:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"expected a GPU tensor, got one on {t.device}")
 
 
 _id_codes: dict = {}  # filled by the first call, so importing needs no torch
@@ -115,10 +116,9 @@ def _stream(stream, t):
     return _current_stream(t.get_device())
 
 
-def _call(name: str, *args):
-    rc = getattr(_binding._lib or lib(), name)(*args)
+def _check(rc: int, what: str):
     if rc:
-        raise RarError(rc, name)
+        raise RarError(rc, what)
 
 
 def _workspace(ws):
@@ -126,7 +126,7 @@ def _workspace(ws):
         return None, 0
     if not ws.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return _dptr(ws), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 # ------------------------------------------------------------------ norm and clip
@@ -172,32 +172,40 @@ class GradClip:
             for g, o in zip(grads, outs):
                 if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
                     raise ValueError("an output must have its gradient's shape and strides")
+        if workspace is None:
+            raise ValueError("a workspace is needed")
+        _on_gpu(workspace, *grads, *(outs or ()))
         n = len(grads)
-        ptrs = (ctypes.c_void_p * max(n, 1))(*[_dptr(g) for g in grads])
+        ptrs = (ctypes.c_void_p * max(n, 1))(*[g.data_ptr() for g in grads])
         dts = (ctypes.c_int * max(n, 1))(*[dtype_code(g) for g in grads])
         optrs = odts = None
         if outs is not None:
-            optrs = (ctypes.c_void_p * max(n, 1))(*[_dptr(o) for o in outs])
+            optrs = (ctypes.c_void_p * max(n, 1))(*[o.data_ptr() for o in outs])
             odts = (ctypes.c_int * max(n, 1))(*[dtype_code(o) for o in outs])
-        if workspace is None:
-            raise ValueError("a workspace is needed")
         ws, nbytes = _workspace(workspace)
         self._keep = (grads, outs, workspace)
         self._ws = workspace
         self._plan = GradPlan()
-        _call("rar_grad_prepare", ptrs, optrs, _sizes([g.numel() for g in grads]), dts, odts, n, ws, nbytes,
-              ctypes.byref(self._plan), _stream(stream, workspace))
+        rc = (_binding._lib or lib()).rar_grad_prepare(
+            ptrs, optrs, _sizes([g.numel() for g in grads]), dts, odts, n, ws, nbytes, ctypes.byref(self._plan),
+            _stream(stream, workspace))
+        _check(rc, "rar_grad_prepare")
         self._ref = ctypes.byref(self._plan)
 
     def norm(self, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
         """norm (one float32 on the device) <- |scale| * the norm of all gradients."""
-        _floats(norm, 1, "norm")
-        _call("rar_grad_norm", self._ref, norm_type, scale, _ptr(norm), _stream(stream, self._ws))
+        address = _floats(norm, 1, "norm")
+        _on_gpu(norm)
+        rc = (_binding._lib or lib()).rar_grad_norm(self._ref, norm_type, scale, address, _stream(stream, self._ws))
+        _check(rc, "rar_grad_norm")
 
     def clip(self, max_norm: float, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
         """The same norm, and every gradient times scale * min(1, max_norm / (norm + 1e-6))."""
-        _floats(norm, 1, "norm")
-        _call("rar_grad_clip", self._ref, norm_type, scale, max_norm, _ptr(norm), _stream(stream, self._ws))
+        address = _floats(norm, 1, "norm")
+        _on_gpu(norm)
+        rc = (_binding._lib or lib()).rar_grad_clip(
+            self._ref, norm_type, scale, max_norm, address, _stream(stream, self._ws))
+        _check(rc, "rar_grad_clip")
 
 
 def grad_norm(grads, workspace, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
@@ -222,8 +230,11 @@ def embedding_forward(weight, ids, out, scale: float = 1.0, stream=None):
     tokens = ids.numel()
     ostride = _out_rows(out, dim, tokens, "out")
     wstride = _out_rows(weight, dim, vocab, "weight")
-    _call("rar_embedding_forward", _dptr(weight), wstride, dtype_code(weight), vocab, dim, _dptr(ids), code, tokens,
-          scale, _dptr(out), ostride, dtype_code(out), _stream(stream, out))
+    _on_gpu(weight, ids, out)
+    rc = (_binding._lib or lib()).rar_embedding_forward(
+        weight.data_ptr(), wstride, dtype_code(weight), vocab, dim, ids.data_ptr(), code, tokens, scale,
+        out.data_ptr(), ostride, dtype_code(out), _stream(stream, out))
+    _check(rc, "rar_embedding_forward")
 
 
 def embedding_workspace_bytes(tokens: int, vocab: int, dim: int) -> int:
@@ -245,18 +256,24 @@ def embedding_backward(dout, ids, dweight, workspace, scale: float = 1.0, paddin
         raise ValueError(f"dout has {n} rows for {tokens} ids")
     wstride = _out_rows(dweight, dim, vocab, "dweight")
     ws, nbytes = _workspace(workspace)
-    _call("rar_embedding_backward", _dptr(dout), dstride, dtype_code(dout), _dptr(ids), code, tokens, vocab, dim,
-          scale, -1 if padding_id is None else padding_id, int(accumulate), _dptr(dweight), wstride,
-          dtype_code(dweight), ws, nbytes, _stream(stream, dweight))
+    _on_gpu(dout, ids, dweight, workspace)
+    rc = (_binding._lib or lib()).rar_embedding_backward(
+        dout.data_ptr(), dstride, dtype_code(dout), ids.data_ptr(), code, tokens, vocab, dim, scale,
+        -1 if padding_id is None else padding_id, int(accumulate), dweight.data_ptr(), wstride, dtype_code(dweight),
+        ws, nbytes, _stream(stream, dweight))
+    _check(rc, "rar_embedding_backward")
 
 
 # ------------------------------------------------------------------ layer norm
 
 def _weight_type(default: int, *ts):
-    codes = {dtype_code(t) for t in ts if t is not None}
-    if len(codes) > 1:
-        raise ValueError("weight, bias and their gradients must share one type")
-    return codes.pop() if codes else default
+    code = None
+    for t in ts:
+        if t is not None:
+            if code is not None and dtype_code(t) != code:
+                raise ValueError("weight, bias and their gradients must share one type")
+            code = dtype_code(t)
+    return default if code is None else code
 
 
 def layernorm_forward(x, weight, bias, out, eps: float = 1e-5, mean=None, rstd=None, stream=None):
@@ -268,14 +285,14 @@ def layernorm_forward(x, weight, bias, out, eps: float = 1e-5, mean=None, rstd=N
     ystride = _out_rows(out, dim, rows, "out")
     if out.dtype != x.dtype:
         raise ValueError("out must have x's type")
-    _vector(weight, dim, "weight")
-    _vector(bias, dim, "bias")
-    _floats(mean, rows, "mean")
-    _floats(rstd, rows, "rstd")
+    w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
+    m, r = _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd")
     dt = dtype_code(x)
     wdt = _weight_type(dt, weight, bias)
-    _call("rar_layernorm_forward", _dptr(x), xstride, _ptr(weight), _ptr(bias), rows, dim, dt, wdt, eps, _dptr(out),
-          ystride, _ptr(mean), _ptr(rstd), _stream(stream, x))
+    _on_gpu(x, weight, bias, out, mean, rstd)
+    rc = (_binding._lib or lib()).rar_layernorm_forward(
+        x.data_ptr(), xstride, w, b, rows, dim, dt, wdt, eps, out.data_ptr(), ystride, m, r, _stream(stream, x))
+    _check(rc, "rar_layernorm_forward")
 
 
 def layernorm_workspace_bytes(rows: int, dim: int) -> int:
@@ -294,13 +311,13 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias, workspac
     if dout.dtype != x.dtype or (dx is not None and dx.dtype != x.dtype):
         raise ValueError("dout and dx must have x's type")
     gstride = dim if dx is None else _out_rows(dx, dim, rows, "dx")
-    for t, name in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")):
-        _vector(t, dim, name)
-    _floats(mean, rows, "mean")
-    _floats(rstd, rows, "rstd")
+    w, dw, db = _vector(weight, dim, "weight"), _vector(dweight, dim, "dweight"), _vector(dbias, dim, "dbias")
+    m, r = _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd")
     dt = dtype_code(x)
     wdt = _weight_type(dt, weight, dweight, dbias)
     ws, nbytes = _workspace(workspace)
-    _call("rar_layernorm_backward", _dptr(dout), dstride, _dptr(x), xstride, _ptr(weight), _ptr(mean), _ptr(rstd),
-          rows, dim, dt, wdt, _ptr(dx), gstride, _ptr(dweight), _ptr(dbias), int(accumulate), ws, nbytes,
-          _stream(stream, x))
+    _on_gpu(dout, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    rc = (_binding._lib or lib()).rar_layernorm_backward(
+        dout.data_ptr(), dstride, x.data_ptr(), xstride, w, m, r, rows, dim, dt, wdt,
+        None if dx is None else dx.data_ptr(), gstride, dw, db, int(accumulate), ws, nbytes, _stream(stream, x))
+    _check(rc, "rar_layernorm_backward")
