@@ -230,19 +230,55 @@ __global__ __launch_bounds__(NT * RB) void layernorm_row_kernel(Rows x, const vo
   }
 }
 
+// Sums of dy h and dy over all rows for 64 columns, a column a lane, each
+// wavefront of the workgroup every W-th row, the wavefronts in order; the
+// result goes straight to dw and db.
+template <int DT>
+__device__ __forceinline__ void grad_columns(const LayernormGrad& a, uint64_t rows, uint64_t dim, uint64_t c0,
+                                             uint32_t W, float* lds) {
+  const uint32_t lane = threadIdx.x & 63, w = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint64_t c = c0 + lane;
+  float dw = 0.0f, db = 0.0f;
+  if (c < dim) {
+#pragma unroll 8
+    for (uint64_t r = w; r < rows; r += W) {
+      const float dy = load_elem<DT>(a.dy.p, r * a.dy.stride + c);
+      const float h = (load_elem<DT>(a.x.p, r * a.x.stride + c) - a.mean[r]) * a.rstd[r];
+      dw = __builtin_fmaf(dy, h, dw);
+      db += dy;
+    }
+  }
+  lds[w * 128 + lane] = dw;
+  lds[w * 128 + 64 + lane] = db;
+  __syncthreads();
+  if (w > 1) return;  // wavefront 0 finishes dw, wavefront 1 db
+  void* out = w ? a.dbias : a.dweight;
+  if (!out || c >= dim) return;
+  float v = 0.0f;
+  for (uint32_t k = 0; k < W; ++k) v += lds[k * 128 + w * 64 + lane];
+  if (a.accumulate) v += load_elem_dt((const char*)out, c, a.wdt);
+  store_elem_dt((char*)out, c, a.wdt, v);
+}
+
 // Backward: the same walk over the rows with the sums of dy h and dy over
 // the workgroup's rows kept in registers; at the end the RB row slots are
 // added (through LDS) and stored as the workgroup's partial sums.
+// Of few rows the workgroups carry only dx (`partial` false), and those past
+// `groups` take the sums column by column, in the same launch.
 template <int DT, int NT, int V, int RB>
 __global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGrad a, uint64_t rows,
-                                                                           uint64_t dim) {
+                                                                       uint64_t dim, uint32_t groups, bool partial) {
   extern __shared__ float lds[];
+  if (blockIdx.x >= groups) {
+    grad_columns<DT>(a, rows, dim, (uint64_t)(blockIdx.x - groups) * 64, NT * RB / 64, lds);
+    return;
+  }
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
   const uint32_t slot = row_slot<NT>();
   const RowShape<DT, NT, V> sh(threadIdx.x % NT, dim);
   float* red = lds + slot * (4 * NT / 64);
   int turn = 0;
-  const uint64_t step = (uint64_t)gridDim.x * RB;
+  const uint64_t step = (uint64_t)groups * RB;
   const bool lines = rows_on_lines<DT>(a.dx);
   uint64_t r = (uint64_t)blockIdx.x * RB + slot;
   RowRaw<DT, V> rx, ry;
@@ -305,7 +341,7 @@ __global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGr
       store_row(sh, a.dx.p + r * a.dx.stride * ES, lines, g);
     }
   }
-  if (!a.dweight && !a.dbias) return;
+  if (!partial) return;
   // the row slots' sums, halving the slots each time: the upper half hands
   // its sums to the lower through LDS (in a fixed order like any other)
   if constexpr (RB > 1) {
@@ -486,6 +522,7 @@ unsigned row_grid(uint64_t rows) { return (unsigned)(rows < 65536 ? rows : 65536
 // Workgroups of the backward pass: one per CU, since each leaves a partial
 // row of 2 * dim floats, as far as there are rows for its slots.
 constexpr uint64_t kGradGroups = 256;
+constexpr uint64_t kFewRows = 512, kFewBytes = 2 << 20;
 uint64_t grad_groups(uint64_t rows, int rb) { return std::min<uint64_t>(kGradGroups, (rows + rb - 1) / rb); }
 
 template <int DT, int NT, int V, int RB>
@@ -533,10 +570,26 @@ template <int DT, int NT, int V, int RB>
 hipError_t backward_rows(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
   const uint64_t groups = grad_groups(rows, RB);
   const size_t lds = (RB * 4 * NT / 64 + RB / 2 * 2 * NT * (V * vec_elems<DT, DT>() + 1)) * sizeof(float);
-  hipLaunchKernelGGL((layernorm_grad_row_kernel<DT, NT, V, RB>), dim3((unsigned)groups), dim3(NT * RB), lds,
-                     stream, a, rows, dim);
-  const hipError_t e = launch_status(stream);
-  return e != hipSuccess ? e : join_partials(a, groups, dim, stream);
+  const size_t column_lds = NT * RB / 64 * 128 * sizeof(float);
+  const bool sums = a.dweight || a.dbias;
+  auto launch = [&](uint64_t row_groups, uint64_t columns, bool partial) {
+    hipLaunchKernelGGL((layernorm_grad_row_kernel<DT, NT, V, RB>), dim3((unsigned)(row_groups + columns)),
+                       dim3(NT * RB), std::max(lds, column_lds), stream, a, rows, dim, (uint32_t)row_groups, partial);
+    return launch_status(stream);
+  };
+  if (rows > kFewRows || rows * dim * DtypeSize<DT>::value > kFewBytes || !sums) {
+    const hipError_t e = launch(groups, 0, sums);
+    return e != hipSuccess ? e : join_partials(a, groups, dim, stream);
+  }
+  // Few rows: a second reading of x and dy (from the caches) by columns costs
+  // less than a second launch that adds partial rows (256 x 1024 bf16 9.5 us
+  // against 12.0), while a column's rows are few (512 x 8192: 37 us against
+  // 16).  It comes first where dx is written over dy or x.
+  const uint64_t columns = (dim + 63) / 64;
+  if (!a.dx.p) return launch(0, columns, false);
+  if (a.dx.p != a.dy.p && a.dx.p != a.x.p) return launch(groups, columns, false);
+  const hipError_t e = launch(0, columns, false);
+  return e != hipSuccess ? e : launch(groups, 0, false);
 }
 
 template <int DT>
