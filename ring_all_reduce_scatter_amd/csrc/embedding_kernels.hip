@@ -468,10 +468,10 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
   const uint32_t mine = w / kJoinEach, p = blockIdx.x * kJoinPieces + mine;
   const uint32_t total = start[vocab];
   uint32_t row = 0, z = 0;  // z: past the last piece of the run that begins in p and is cut
-  if (p + 1 < pc.n && (p + 1) * pc.ch < total) {
-    const uint32_t i1 = (p + 1) * pc.ch;
+  if (p + 1 < pc.n) {
+    const uint32_t i1 = (p + 1) * pc.ch, before = entries[i1 - 1].row;  // inside the buffer, in use or not
     row = entries[i1].row;
-    if (entries[i1 - 1].row == row && start[row] >= p * pc.ch) z = (start[row + 1] - 1) / pc.ch + 1;
+    if (i1 < total && before == row && start[row] >= p * pc.ch) z = (start[row + 1] - 1) / pc.ch + 1;
   }
   const bool alone = z != 0 && z - p <= kJoinShort;
   if (w % kJoinEach == 0) {

@@ -336,8 +336,8 @@ __global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGr
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i) g.v[j].v[i] = rs * (g.v[j].v[i] - mg - h.v[j].v[i] * mgh);
-      g.t = rs * (g.t - mg - h.t * mgh);
+        for (int i = 0; i < E; ++i) g.v[j].v[i] = rs * __builtin_fmaf(-h.v[j].v[i], mgh, g.v[j].v[i] - mg);
+      g.t = rs * __builtin_fmaf(-h.t, mgh, g.t - mg);
       store_row(sh, a.dx.p + r * a.dx.stride * ES, lines, g);
     }
   }
