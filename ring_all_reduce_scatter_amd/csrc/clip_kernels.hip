@@ -11,6 +11,15 @@
 // vector units have the rate to spare (one 64-bit FMA an element against at
 // least 2 bytes of memory).  Partial sums are added in a fixed order, so a
 // result depends on the set alone.
+//
+// Bound by memory: the norm reads the set once, a clip once more beside its
+// writes.  Times on one MI355X, inputs cold: norm of 378 million bf16
+// elements 115 us (6.6 TB/s), clip of the same list 354 us (norm 114, clip
+// 237 at 6.4 TB/s); 40 tensors of 19.6 million f32 elements in all 36 us
+// (three passes of 78 MB at the copy rate: 37).  One cooperative launch that
+// held the set on the chip between the norm and the product would spare the
+// second read, but such a launch alone takes 19.5 us here against 2.5, more
+// than that read costs for any set that fits.
 #include <algorithm>
 
 #include "operator_launch.hpp"

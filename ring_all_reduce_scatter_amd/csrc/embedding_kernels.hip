@@ -5,8 +5,16 @@
 //
 // The gradient is a sum over the tokens of each table row.  The tokens are
 // sorted by row first (token_sort_kernel), keeping their order within a
-// row, so that every row's sum is formed in ascending token order in
-// binary32, without atomics: the same inputs give the same bits.
+// row, so that every row's sum is formed in binary32 in an order that the
+// ids alone fix (ascending, in pieces), without atomics on the sums: the
+// same inputs give the same bits.
+//
+// All of it is bound by memory for batches and by latency for a few tokens.
+// Times on one MI355X, inputs cold: lookup of 16,383 rows of 4096 bf16 29.7
+// us (6.2 TB/s of its 185 MB); gradient of 32,768 x 2048 bf16 tokens into
+// 50,021 f32 rows 135 us: sort 13, sums and zero rows 94 (5.8 TB/s of 549
+// MB), cut runs 9, and the launches between; 509 x 512 f32 tokens into 8192
+// rows 8.6 us, one launch of 8.
 #include <algorithm>
 
 #include "operator_launch.hpp"
@@ -74,6 +82,10 @@ __device__ __forceinline__ void store_seg(char* base, uint64_t row, uint64_t c0,
 }
 
 // ------------------------------------------------------------------ lookup
+// A wavefront per token and kSeg columns: each instruction moves a contiguous
+// kilobyte, and a batch has enough wavefronts to need no loop.  Rows of the
+// table go through the caches (frequent tokens are read again); the output is
+// stored nontemporal (write-through was 2 % slower).
 
 template <int DW, int DO, typename ID>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(Rows weight, uint64_t vocab, uint64_t dim,
@@ -135,13 +147,15 @@ hipError_t embedding_ids(const Rows& w, uint64_t vocab, uint64_t dim, const void
 // place the kept tokens, or, where a wavefront met more than it can keep,
 // walk the ids again.  Tokens that share a row and a wavefront iteration are
 // ranked by their lanes.  Every workgroup reads all ids: 256 workgroups read
-// them from the L2, and no pass over memory or launch is added.
+// them from the L2, and no pass over memory or launch is added.  It is bound
+// by the latency of its phases: 7 us for 1100 ids, 13 us for 32,768 (30 us
+// before the owned tokens were kept, each iteration of the second walk then
+// waiting for its ids and, in the workgroup of a frequent token, its ranks).
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSortKeep = 256;      // owned tokens that a wavefront keeps from the first walk
 constexpr uint32_t kSortMaxRows = 1792;  // counters of 112 KiB, kept tokens of 32: of the CU's 160
-
 constexpr int kSortAhead = 16;           // ids in flight per lane
 
 // Table rows of the tokens t, t + 64, ... below end; kNoRow for a token that
@@ -285,7 +299,7 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __re
 }
 
 hipError_t token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t vocab, int64_t padding,
-                             const TokenSort& sort, hipStream_t stream) {
+                      const TokenSort& sort, hipStream_t stream) {
   uint32_t R = (uint32_t)((vocab + 255) / 256);
   if (R < 16) R = 16;
   if (R > kSortMaxRows) R = kSortMaxRows;
@@ -311,7 +325,11 @@ hipError_t token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t voc
 // cut by the piece's beginning goes to the piece's head partial, one that
 // begins here and is cut by its end to its tail partial (binary32); after
 // the launch the tail and the heads that follow it are added in order.
-// Rows without tokens are zeroed by further wavefronts of the same launch.
+// (A wavefront per table row took 1827 us where this takes 135: the most
+// frequent of 32,768 natural tokens makes up 6 % of them.)
+// Rows without tokens are zeroed by further wavefronts of the same launch,
+// whose stores overlap the others' loads; done by the sort's workgroups the
+// same call took 147 us.
 
 struct Pieces {
   uint32_t tokens;
@@ -516,7 +534,9 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
 // out of all ids (one a thread), zeroes the rows that have none, sorts the
 // others in LDS by counting for each how many come before it (an entry is
 // row << 10 | token, so they are ordered as numbers), and adds them in
-// sixteen pieces as above, with the partial sums in LDS.
+// sixteen pieces as above, with the partial sums in LDS.  Against the three
+// launches above: 7.4 us instead of 16.5 for 509 x 512 f32 tokens into 8192
+// rows.
 
 constexpr uint32_t kFewTokens = 1024, kFewWaves = kFewTokens / 64, kFewRows = 1024;
 

@@ -12,6 +12,15 @@
 // to its store, so memory is read and written once: 16 lanes for short rows,
 // a wavefront, or four or eight of them.  Rows too long for that go through
 // the loops at the end of this file, which read a row once per pass.
+// The lanes per row follow from the row's length alone.  Both directions are
+// bound by memory for batches, by launch latency for few rows.  Times on one
+// MI355X, inputs cold: forward 16,384 x 4096 f16 46 us (5.8 TB/s of 268 MB),
+// one row of 4096 bf16 3.1 us; backward 16,384 x 8192 bf16 144 us (139 and 5
+// for the partial rows; 5.8 TB/s of 839 MB), 2047 x 1001 f32 7.3 and 3.5 us.
+// Measured and left out: a contiguous range of rows per workgroup instead of
+// every n-th (forward 55 us, backward 151), ordinary loads instead of
+// streaming ones (50 and 153), 16 wavefronts of half the columns backward
+// (156).
 #include <algorithm>
 
 #include "operator_launch.hpp"
