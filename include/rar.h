@@ -528,7 +528,8 @@ typedef struct {
   uint64_t ntiles;
 } rar_grad_plan;
 
-/* Workspace for rar_grad_prepare; 0 on bad args. */
+/* Workspace for rar_grad_prepare; 0 on bad args.  A set may hold up to
+ * 2^24 - 16 tiles of 16 KiB (RAR_ENOTSUP beyond). */
 size_t rar_grad_workspace_bytes(const size_t* counts, size_t ntensors);
 
 /* grads: ntensors device pointers to counts[t] elements of dtypes[t] (types
@@ -574,7 +575,9 @@ size_t rar_embedding_workspace_bytes(size_t tokens, size_t vocab, size_t dim);
  * t with ids[t] == v, in binary32.  Ids outside [0, vocab) and the id
  * padding_id (-1: none) contribute nothing.  Rows without tokens become zero,
  * or stay untouched with accumulate.  dout_stride may be 0 (one row for all
- * tokens).  tokens, vocab and dim below 2^31. */
+ * tokens).  RAR_ENOTSUP beyond 2^30 tokens, 2^31 - 1 rows or columns, or
+ * what one launch holds (2^26 wavefronts of 512 columns by 8 to 64 tokens,
+ * or of 8 KiB of dweight). */
 int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype, const void* ids,
                            int id_type, size_t tokens, size_t vocab, size_t dim, float scale,
                            int64_t padding_id, int accumulate, void* dweight, size_t dweight_stride,

@@ -92,19 +92,20 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(Rows weight, uint64
                                                               const ID* __restrict__ ids, uint32_t units,
                                                               uint32_t segs, float scale, Rows out) {
   constexpr int E = vec_elems<DW, DO>();
-  const uint32_t u = grid_wave();
-  if (u >= units) return;
-  const uint64_t t = u / segs, c = (uint64_t)(u - (uint32_t)t * segs) * kSeg;
-  const int64_t id = ids[t];
-  SegCols<E> g = {};
-  if ((uint64_t)id < vocab) {
-    g = load_seg<DW, E>(weight.p, (uint64_t)id * weight.stride, c, dim);
+  for (uint64_t w = grid_wave(); w < units; w += (uint64_t)gridDim.x * (kThreads / 64)) {
+    const uint32_t u = (uint32_t)w;
+    const uint64_t t = u / segs, c = (uint64_t)(u - (uint32_t)t * segs) * kSeg;
+    const int64_t id = ids[t];
+    SegCols<E> g = {};
+    if ((uint64_t)id < vocab) {
+      g = load_seg<DW, E>(weight.p, (uint64_t)id * weight.stride, c, dim);
 #pragma unroll
-    for (int j = 0; j < SegCols<E>::V; ++j)
+      for (int j = 0; j < SegCols<E>::V; ++j)
 #pragma unroll
-      for (int i = 0; i < E; ++i) g.x[j].v[i] *= scale;
+        for (int i = 0; i < E; ++i) g.x[j].v[i] *= scale;
+    }
+    store_seg<DO, E, false>(out.p, t * out.stride, c, dim, g);
   }
-  store_seg<DO, E, false>(out.p, t * out.stride, c, dim, g);
 }
 
 template <int DW, int DO, typename ID>
@@ -113,8 +114,10 @@ hipError_t embedding_typed(const Rows& w, uint64_t vocab, uint64_t dim, const vo
   const uint32_t segs = (uint32_t)((dim + kSeg - 1) / kSeg);
   const uint32_t units = (uint32_t)(tokens * segs);
   constexpr uint32_t waves = kThreads / 64;
-  hipLaunchKernelGGL((embedding_kernel<DW, DO, ID>), dim3(units / waves + (units % waves != 0)), dim3(kThreads), 0,
-                     stream, w, vocab, dim, (const ID*)ids, units, segs, scale, out);
+  // a wavefront each, as far as one launch holds them (2^32 threads)
+  const uint32_t groups = std::min<uint32_t>(units / waves + (units % waves != 0), 1u << 23);
+  hipLaunchKernelGGL((embedding_kernel<DW, DO, ID>), dim3(groups), dim3(kThreads), 0, stream, w, vocab, dim,
+                     (const ID*)ids, units, segs, scale, out);
   return launch_status(stream);
 }
 
@@ -657,6 +660,15 @@ hipError_t embedding_grad_few(const Rows& dout, const void* ids, bool ids64, uin
   return launch_status(stream);
 }
 
+// Rows that one zeroing wavefront looks through, about 8 KiB: one row of 2048
+// f32 (the whole call takes 134 us so, 143 with 16 rows), 16 rows of 128 bf16
+// (44 us; with one, each wavefront waits for its row's starts for a store of
+// 256 bytes).
+uint32_t zero_rows(uint64_t dim, int dt) {
+  const uint64_t row_bytes = dim * (dt == DT_F32 ? 4 : 2);
+  return row_bytes >= 8192 ? 1 : (uint32_t)std::min<uint64_t>(8192 / row_bytes, 16);
+}
+
 template <int DI, int DO>
 hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   if (a.tokens == 0 && a.accumulate) return hipSuccess;
@@ -666,14 +678,10 @@ hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   hipError_t e = token_sort(a.ids, a.ids64, a.tokens, a.vocab, a.padding, a.sort, stream);
   if (e != hipSuccess) return e;
   const uint64_t ch = embedding_piece(a.tokens, a.dim);
-  // a wavefront zeroes about 8 KiB: one row of 2048 f32 (the whole call takes
-  // 134 us so, 143 with 16 rows), 16 rows of 128 bf16 (44 us; with one, each
-  // wavefront waits for its row's starts for a store of 256 bytes)
-  const uint64_t row_bytes = a.dim * DtypeSize<DO>::value;
-  const uint32_t zrows = row_bytes >= 8192 ? 1 : (uint32_t)std::min<uint64_t>(8192 / row_bytes, 16);
+  const uint32_t zrows = zero_rows(a.dim, DO);
   const Pieces pc{(uint32_t)a.tokens, (uint32_t)ch, (uint32_t)((a.tokens + ch - 1) / ch), (uint32_t)((a.dim + kSeg - 1) / kSeg), a.dim,
                   zrows, a.partials};
-  const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : (a.vocab + zrows - 1) / zrows);
+  const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : embedding_zero_waves(a.vocab, a.dim, DO));
   constexpr int waves = kThreads / 64;
   hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads), 0,
                      stream, a.dout, a.vocab, a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
@@ -709,6 +717,11 @@ uint64_t embedding_piece(uint64_t tokens, uint64_t dim) {
   uint64_t ch = kBatch;
   while (ch < 64 && (tokens + ch - 1) / ch * segs > 4096) ch *= 2;
   return ch;
+}
+
+uint64_t embedding_zero_waves(uint64_t vocab, uint64_t dim, int dt) {
+  const uint64_t rows = zero_rows(dim, dt);
+  return (vocab + rows - 1) / rows;
 }
 
 hipError_t launch_embedding_grad(const EmbeddingGrad& a, hipStream_t stream) {

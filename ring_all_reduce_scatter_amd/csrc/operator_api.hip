@@ -15,8 +15,10 @@ using namespace rar;
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr uint64_t kMaxGrid = 0x7fffffffull;
-constexpr uint64_t kMaxUnits = 0xfffffff0ull;  // wavefronts of one launch (32-bit numbers)
+// A launch holds fewer than 2^32 threads.
+constexpr uint64_t kMaxTiles = (1ull << 24) - 16;  // workgroups of 256
+constexpr uint64_t kMaxUnits = (1ull << 26) - 16;  // wavefronts
+constexpr size_t kMaxTokens = (size_t)1 << 30, kMaxDim = 0x7fffffff;
 
 size_t es_of(int dt) { return dt == RAR_F32 ? 4 : 2; }
 bool dt_ok(int dt) { return dt == RAR_F32 || dt == RAR_F16 || dt == RAR_BF16; }
@@ -77,7 +79,7 @@ bool clip_layout(const size_t* counts, size_t nt, ClipLayout* l) {
     if (counts[t] >= (size_t)1 << 43) return false;
     ntiles += clip_tiles(counts[t], RAR_F32);
   }
-  if (nt >= (size_t)1 << 24 || ntiles > kMaxGrid) return false;
+  if (nt >= (size_t)1 << 24 || ntiles > 0x7fffffffull) return false;
   l->descs = round_up((5 * nt + 1) * sizeof(uint64_t), kAlign);
   l->partials = l->descs + round_up((size_t)ntiles * kClipDescBytes, kAlign);
   l->result = l->partials + kClipMaxBlocks * sizeof(double);
@@ -92,7 +94,7 @@ ClipSet clip_set(const rar_grad_plan* p) {
 }
 
 int check_plan(const rar_grad_plan* p, int norm_type, double scale, const float* norm) {
-  if (!p || !p->workspace || ((uintptr_t)p->workspace & 15u) || p->ntiles > kMaxGrid) return RAR_EINVAL;
+  if (!p || !p->workspace || ((uintptr_t)p->workspace & 15u) || p->ntiles > kMaxTiles) return RAR_EINVAL;
   if (p->desc_offset == 0 || (p->desc_offset | p->partial_offset | p->result_offset) & 15u) return RAR_EINVAL;
   if (norm_type != RAR_NORM_L2 && norm_type != RAR_NORM_MAX) return RAR_EINVAL;
   if (!std::isfinite(scale)) return RAR_EINVAL;
@@ -149,6 +151,7 @@ int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, co
     tab[3 * nt + 1 + t] = counts[t];
     tab[4 * nt + 1 + t] = (uint64_t)dtypes[t] | (uint64_t)(outs ? out_dtypes[t] : dtypes[t]) << 8;
   }
+  if (tiles > kMaxTiles) return RAR_ENOTSUP;
   tab[nt] = tiles;
   rar_grad_plan p{};
   p.workspace = workspace;
@@ -209,7 +212,7 @@ namespace {
 
 int embedding_sizes(size_t tokens, size_t vocab, size_t dim) {
   if (vocab == 0 || dim == 0) return RAR_EINVAL;
-  if (tokens > 0x7fffffffull || vocab > 0x7fffffffull || dim > 0x7fffffffull) return RAR_ENOTSUP;
+  if (tokens > kMaxTokens || vocab > 0x7fffffff || dim > kMaxDim) return RAR_ENOTSUP;
   return RAR_OK;
 }
 
@@ -246,7 +249,7 @@ int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_d
   const Range r[] = {{(uintptr_t)out, ob, true, 0}, {(uintptr_t)weight, wb, false, 0},
                      {(uintptr_t)ids, ib * tokens, false, 0}};
   if ((rc = check_ranges(r, 3))) return rc;
-  if (tokens * ((dim + 511) / 512) > kMaxUnits) return RAR_ENOTSUP;
+  if (tokens * ((dim + 511) / 512) > 0xfffffff0ull) return RAR_ENOTSUP;  // numbered in 32 bits
   return hip_rc(launch_embedding(Rows{(char*)weight, weight_stride, weight_dtype}, vocab, dim, ids,
                                  id_type == RAR_I64, tokens, scale, Rows{(char*)out, out_stride, out_dtype},
                                  (hipStream_t)stream));
@@ -279,7 +282,7 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   if ((rc = check_ranges(r, 4))) return rc;
   const EmbeddingLayout l = embedding_layout(tokens, vocab, dim);
   const size_t pieces = (tokens + embedding_piece(tokens, dim) - 1) / embedding_piece(tokens, dim);
-  if (pieces * ((dim + 511) / 512) + vocab > kMaxUnits) return RAR_ENOTSUP;
+  if (pieces * ((dim + 511) / 512) + embedding_zero_waves(vocab, dim, dweight_dtype) > kMaxUnits) return RAR_ENOTSUP;
   char* base = (char*)workspace;
   EmbeddingGrad a{};
   a.dout = Rows{(char*)dout, dout_stride, dout_dtype};
@@ -303,6 +306,7 @@ int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, co
                           size_t dim, int dtype, int weight_dtype, float eps, void* y, size_t y_stride, float* mean,
                           float* rstd, void* stream) {
   if (!dt_ok(dtype) || !dt_ok(weight_dtype)) return RAR_EDTYPE;
+  if (dim > kMaxDim) return RAR_ENOTSUP;
   size_t xb, yb;
   if (dim == 0 || y_stride < dim || !(eps >= 0.0f) || !rows_bytes(rows, dim, x_stride, es_of(dtype), &xb) ||
       !rows_bytes(rows, dim, y_stride, es_of(dtype), &yb))
@@ -326,7 +330,7 @@ int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, co
 }
 
 size_t rar_layernorm_workspace_bytes(size_t rows, size_t dim) {
-  if (dim == 0 || dim >= (size_t)1 << 36) return 0;
+  if (dim == 0 || dim > kMaxDim) return 0;
   return round_up(layernorm_splits(rows, dim) * 2 * dim * sizeof(float), kAlign);
 }
 
@@ -337,7 +341,8 @@ int rar_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size
   if (!dt_ok(dtype) || !dt_ok(weight_dtype)) return RAR_EDTYPE;
   size_t yb, xb, db = 0;
   const size_t es = es_of(dtype), ws = es_of(weight_dtype);
-  if (dim == 0 || dim >= (size_t)1 << 36 || !rows_bytes(rows, dim, dy_stride, es, &yb) ||
+  if (dim > kMaxDim) return RAR_ENOTSUP;
+  if (dim == 0 || !rows_bytes(rows, dim, dy_stride, es, &yb) ||
       !rows_bytes(rows, dim, x_stride, es, &xb) || (dx && (dx_stride < dim || !rows_bytes(rows, dim, dx_stride, es, &db))))
     return RAR_EINVAL;
   int rc;

@@ -55,6 +55,8 @@ struct TokenSort {
 // Entries that one wavefront of the gradient takes; partials holds two rows
 // of dim floats, rounded up to 512, for each such piece.
 uint64_t embedding_piece(uint64_t tokens, uint64_t dim);
+// Wavefronts that zero the rows without tokens.
+uint64_t embedding_zero_waves(uint64_t vocab, uint64_t dim, int dt);
 struct EmbeddingGrad {
   Rows dout, dweight;
   const void* ids;

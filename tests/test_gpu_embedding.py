@@ -158,6 +158,25 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(w.float(), want.to(torch.bfloat16).float())
 
 
+def test_more_tokens_than_one_wavefront_each():
+    """2^25 wavefronts fill the largest launch; the lookup goes round."""
+    tokens = (1 << 25) + 70
+    ids = torch.randint(-1, 17, (tokens,), device=DEV, dtype=torch.int32)
+    w = torch.randn(17, 8, device=DEV).to(torch.bfloat16)
+    w[16] = 0
+    out = torch.full((tokens, 8), 3.0, device=DEV, dtype=torch.bfloat16)
+    rar.embedding_forward(w[:16], ids, out)
+    want = w[torch.where(ids < 0, 16, ids).long()]
+    assert torch.equal(out, want)
+
+
+def test_many_tokens():
+    ids = _ids("skew", 400_000, 3000, dtype=torch.int32)
+    dout = torch.randn(400_000, 24, device=DEV)
+    dw = _grad(dout, ids, 3000, torch.float32)
+    assert_within(dw, *ref.embedding_grad(dout, ids, 3000, 1.0, torch.float32), "gradient")
+
+
 def test_gradient_against_differences():
     """The lookup is linear in the table: for f = sum(out * dout) the change
     along a direction is the gradient's product with it, up to roundings."""

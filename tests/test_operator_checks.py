@@ -237,3 +237,18 @@ def test_layernorm_backward_refusals():
     assert _ln_grad(dw=B + 7 * G + 4) == EOVERLAP and _ln_grad(ws=B + 6 * G + 16) == EOVERLAP
     assert _ln_grad(db=B + 2 * G + 4) == EOVERLAP and _ln_grad(dw=B + 3 * G) == EOVERLAP
     assert rar.lib().rar_layernorm_workspace_bytes(5, 0) == 0
+
+
+def test_sizes_that_no_launch_holds():
+    """Refused before anything is enqueued: a launch holds fewer than 2^32 threads."""
+    big = (1 << 24) * 8192  # 2^24 tiles of bf16 elements
+    L = rar.lib()
+    need = L.rar_grad_workspace_bytes(_arr(ctypes.c_size_t, [big]), 1)
+    assert need > 0
+    assert _prepare([B], [big], [2], ws=B - (1 << 36), nbytes=need) == ENOTSUP
+    assert _embed(tokens=(1 << 30) + 1) == ENOTSUP
+    assert _embed(tokens=1 << 30, dim=4096, ws=4096, os_=4096, vocab=8, out=1 << 45) == ENOTSUP
+    assert _embed_grad(tokens=(1 << 30) + 1, nbytes=1 << 40) == ENOTSUP
+    assert _embed_grad(vocab=1 << 30, dim=4096, ws=4096, ds=4096, dw=1 << 45, work=1 << 44) == ENOTSUP
+    assert _ln(dim=1 << 31, ys=1 << 31) == ENOTSUP and _ln_grad(dim=1 << 31) == ENOTSUP
+    assert L.rar_layernorm_workspace_bytes(5, 1 << 31) == 0
