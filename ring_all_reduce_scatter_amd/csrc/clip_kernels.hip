@@ -106,13 +106,6 @@ __device__ __forceinline__ Acc<KIND> block_join(Acc<KIND> a, double* lds) {
   return r;
 }
 
-// This wavefront's stores have been acknowledged.
-__device__ __forceinline__ void stores_done() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-}
-
 // Tiles are taken by groups of kThreads threads (four wavefronts).
 __device__ __forceinline__ uint32_t tile_lane() { return threadIdx.x % kThreads; }
 

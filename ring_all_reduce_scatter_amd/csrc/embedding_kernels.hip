@@ -12,9 +12,9 @@
 // All of it is bound by memory for batches and by latency for a few tokens.
 // Times on one MI355X, inputs cold: lookup of 16,383 rows of 4096 bf16 29.7
 // us (6.2 TB/s of its 185 MB); gradient of 32,768 x 2048 bf16 tokens into
-// 50,021 f32 rows 135 us: sort 13, sums and zero rows 94 (5.8 TB/s of 549
-// MB), cut runs 9, and the launches between; 509 x 512 f32 tokens into 8192
-// rows 8.6 us, one launch of 8.
+// 50,021 f32 rows 125 us: sort 13, sums and zero rows 95 (5.8 TB/s of 549
+// MB), and the launch between; 509 x 512 f32 tokens into 8192 rows 8.6 us,
+// one launch of 8.
 #include <algorithm>
 
 #include "operator_launch.hpp"
@@ -205,6 +205,8 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const ID* __re
   const uint32_t lo = blockIdx.x * R;
   const uint32_t rows = vocab - lo < R ? vocab - lo : R;
   for (uint32_t i = tid; i < kSortWaves * R; i += kSortThreads) cnt[i] = 0;
+  for (uint64_t i = (uint64_t)blockIdx.x * kSortThreads + tid; i < sort.ncounts; i += (uint64_t)gridDim.x * kSortThreads)
+    sort.counts[i] = 0;
   __syncthreads();
   const uint32_t part = ((tokens + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   const uint32_t t0 = (uint32_t)w * part;  // at most tokens + 1024: below 2^32
@@ -326,13 +328,21 @@ hipError_t token_sort(const void* ids, bool ids64, uint64_t tokens, uint64_t voc
 // and kSeg columns, adds the gradients of each run of equal rows, and stores
 // a run that lies inside its piece straight to the table's gradient.  A run
 // cut by the piece's beginning goes to the piece's head partial, one that
-// begins here and is cut by its end to its tail partial (binary32); after
-// the launch the tail and the heads that follow it are added in order.
-// (A wavefront per table row took 1827 us where this takes 135: the most
+// begins here and is cut by its end to its tail partial (binary32).
+// The last wavefront to leave a part of a run adds them, the tail and the
+// heads that follow it in order, in two levels so that a row with very many
+// parts is not added by one wavefront alone: first the parts of each group
+// of kGroup pieces, then the groups.  Parts and counts are accessed at
+// device scope, past the XCD's L2, and a part's store has been acknowledged
+// before it is counted, so the last wavefront reads what all have stored.
+// The pieces are the launch's first wavefronts, so these waits pass under the
+// zeroing of the table's other rows (a further launch for the cut runs took
+// 10 us and its start).
+// (A wavefront per table row took 1827 us where this takes 125: the most
 // frequent of 32,768 natural tokens makes up 6 % of them.)
 // Rows without tokens are zeroed by further wavefronts of the same launch,
 // whose stores overlap the others' loads; done by the sort's workgroups the
-// same call took 147 us.
+// call took 12 us more.
 
 struct Pieces {
   uint32_t tokens;
@@ -342,7 +352,9 @@ struct Pieces {
   uint64_t dim;
   uint32_t zrows;   // rows that one wavefront looks through for empty ones (at most 64)
   float* partials;  // [n][2][segs * kSeg]: head, tail
+  uint32_t* counts; // [2][n][segs]: arrived parts of the group, groups of the run, that begin in a piece
 };
+constexpr uint32_t kGroup = 16, kPartBatch = 4;
 
 // Rounds a finished sum into the table's gradient.
 template <int DO, int E, bool WT = true>
@@ -356,35 +368,84 @@ __device__ __forceinline__ void finish_row(const Rows& dw, uint64_t row, uint64_
   store_seg<DO, E, WT>(dw.p, row * dw.stride, c0, dim, acc);
 }
 
-// Partial sums: a lane's eight values side by side in one workspace row of
-// segs * kSeg floats, so no column is missing.
+// Partial sums: a lane's eight values as two vectors 256 columns apart, in a
+// row of kSeg floats (so no column is missing) of the workspace or of LDS.
 template <int E>
-__device__ __forceinline__ float* partial_at(const Pieces& pc, uint32_t piece, int tail, uint64_t c0) {
-  return pc.partials + ((uint64_t)piece * 2 + tail) * pc.segs * kSeg + c0 + (threadIdx.x & 63) * 4;
+__device__ __forceinline__ u32x4 partial_half(const SegCols<E>& s, int h) {
+  u32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(s.x[(4 * h) / E].v[(4 * h) % E + i]);
+  return x;
 }
+template <int E>
+__device__ __forceinline__ void set_partial_half(SegCols<E>& s, int h, u32x4 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s.x[(4 * h) / E].v[(4 * h) % E + i] = __uint_as_float(x[i]);
+}
+// In LDS: p the lane's place.
 template <int E>
 __device__ __forceinline__ void store_partial(float* p, const SegCols<E>& s) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    u32x4 x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(s.x[(4 * h) / E].v[(4 * h) % E + i]);
-    *(u32x4*)(p + h * 256) = x;
-  }
+  for (int h = 0; h < 2; ++h) *(u32x4*)(p + h * 256) = partial_half(s, h);
 }
 template <int E>
 __device__ __forceinline__ SegCols<E> load_partial(const float* p) {
   SegCols<E> s;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const u32x4 x = *(const u32x4*)(p + h * 256);
+  for (int h = 0; h < 2; ++h) set_partial_half(s, h, *(const u32x4*)(p + h * 256));
+  return s;
+}
+// In the workspace, at device scope.
+constexpr int kSc1 = 16;  // cache-policy operand
+__device__ __forceinline__ WtRange part_range(const Pieces& pc, uint32_t piece, uint32_t tail, uint64_t c0) {
+  return wt_range((const char*)(pc.partials + ((uint64_t)piece * 2 + tail) * pc.segs * kSeg + c0), kSeg * 4);
+}
+template <int E>
+__device__ __forceinline__ void store_part(WtRange r, const SegCols<E>& s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.x[(4 * h) / E].v[(4 * h) % E + i] = __uint_as_float(x[i]);
-  }
+  for (int h = 0; h < 2; ++h)
+    __builtin_amdgcn_raw_buffer_store_b128(partial_half(s, h), r, (int)((threadIdx.x & 63) * 16 + h * 1024), 0, kSc1);
+}
+template <int E>
+__device__ __forceinline__ SegCols<E> load_part(WtRange r) {
+  SegCols<E> s;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    set_partial_half(s, h,
+                     __builtin_amdgcn_raw_buffer_load_b128(r, (int)((threadIdx.x & 63) * 16 + h * 1024), 0, kSc1));
   return s;
 }
 
 constexpr uint32_t kBatch = 8;  // rows of dout in flight per wavefront
+
+// Counts this wavefront; how many came before it.  The loads that follow in
+// the program stay after it (the fence is the compiler's alone).
+__device__ __forceinline__ uint32_t arrive(uint32_t* count) {
+  uint32_t before = 0;
+  if ((threadIdx.x & 63) == 0) before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  before = (uint32_t)__builtin_amdgcn_readfirstlane(before);
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  return before;
+}
+
+// Adds the parts of the pieces a, a + step, ... below z, in order, of a run
+// that begins in piece `first`; a batch of loads is in flight at a time, the
+// last one repeated at its end.
+template <int E>
+__device__ __forceinline__ void add_parts(const Pieces& pc, uint32_t a, uint32_t z, uint32_t step, uint32_t first,
+                                          uint64_t c0, SegCols<E>& sum) {
+  for (uint32_t k0 = a; k0 < z; k0 += kPartBatch * step) {
+    SegCols<E> part[kPartBatch];
+#pragma unroll
+    for (uint32_t i = 0; i < kPartBatch; ++i) {
+      const uint32_t k = k0 + i * step < z ? k0 + i * step : k0;
+      part[i] = load_part<E>(part_range(pc, k, k == first, c0));
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kPartBatch; ++i)
+      if (k0 + i * step < z) sum.add(part[i]);
+  }
+}
 
 template <int DI, int DO>
 __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uint64_t vocab,
@@ -408,7 +469,8 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
     return;
   }
   const uint32_t p = u / pc.segs;
-  const uint64_t c0 = (uint64_t)(u - p * pc.segs) * kSeg;
+  const uint32_t seg = u - p * pc.segs;
+  const uint64_t c0 = (uint64_t)seg * kSeg;
   const uint32_t total = start[vocab];
   const uint32_t i0 = p * pc.ch;
   // the piece's entries, one a lane, and the rows beside it; past the used
@@ -422,8 +484,9 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
   auto entry_token = [&](uint32_t i) { return (uint32_t)__builtin_amdgcn_readlane(own.token, i); };
   auto entry_row = [&](uint32_t i) { return (uint32_t)__builtin_amdgcn_readlane(own.row, i); };
   uint32_t row = entry_row(0);
-  bool head = i0 > 0 && row_before == row;  // the run began in an earlier piece
+  const bool began = i0 > 0 && row_before == row;  // the first run began in an earlier piece
   const bool cut = i0 + m < total && row_after == entry_row(m - 1);
+  bool head = began;
   SegCols<E> acc = {};
   for (uint32_t b = 0; b < m; b += kBatch) {
     SegCols<E> g[kBatch];
@@ -435,7 +498,7 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
       if (b + k >= m) break;
       const uint32_t r = entry_row(b + k);
       if (r != row) {  // uniform
-        if (head) store_partial(partial_at<E>(pc, p, 0, c0), acc);
+        if (head) store_part(part_range(pc, p, 0, c0), acc);
         else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
         head = false;
         row = r;
@@ -444,90 +507,34 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
       acc.add(g[k]);
     }
   }
-  if (head) store_partial(partial_at<E>(pc, p, 0, c0), acc);
-  else if (cut) store_partial(partial_at<E>(pc, p, 1, c0), acc);
+  const bool tail = cut && !head;
+  if (head) store_part(part_range(pc, p, 0, c0), acc);
+  else if (cut) store_part(part_range(pc, p, 1, c0), acc);
   else finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, acc);
-}
-
-// Adds up the runs that were cut.  A run belongs to the piece it begins in,
-// whose tail and the heads of the pieces up to the run's end are its parts.
-// A workgroup looks at kJoinPieces pieces, kJoinEach wavefronts each.  Runs
-// of up to kJoinShort parts are added there and then, each wavefront taking
-// every kJoinEach-th column segment; for longer ones all wavefronts of the
-// workgroup come together, kJoinEach for a segment's consecutive shares,
-// which are then added in order.  E is the gradient kernel's: it fixes which
-// columns a lane's partial sums are.
-constexpr uint32_t kJoinWaves = 16, kJoinPieces = 4, kJoinEach = kJoinWaves / kJoinPieces, kJoinShort = 16;
-
-template <int E>
-__device__ __forceinline__ SegCols<E> add_parts(const Pieces& pc, uint32_t p, uint32_t a, uint32_t z, uint64_t c0) {
-  SegCols<E> acc = {};
-  for (uint32_t k0 = a; k0 < z; k0 += kBatch) {  // all loads of a batch in flight, the last one repeated at its end
-    SegCols<E> part[kBatch];
-#pragma unroll
-    for (uint32_t i = 0; i < kBatch; ++i) {
-      const uint32_t k = k0 + i < z ? k0 + i : z - 1;
-      part[i] = load_partial<E>(partial_at<E>(pc, k, k == p, c0));
+  if (!began && !tail) return;
+  stores_done();
+  // the run of the head part, then the run of the tail part
+  for (uint32_t part = 0; part < 2; ++part) {
+    if (!(part ? tail : began)) continue;
+    const uint32_t to = part ? entry_row(m - 1) : entry_row(0);
+    const uint32_t first = start[to] / pc.ch, end = (start[to + 1] - 1) / pc.ch;  // the run's pieces
+    const uint32_t group = p / kGroup * kGroup;
+    const uint32_t a = first > group ? first : group, z = end < group + kGroup - 1 ? end : group + kGroup - 1;
+    SegCols<E> sum = {};
+    if (z > a) {  // the group's last part adds them
+      if (arrive(&pc.counts[(uint64_t)a * pc.segs + seg]) != z - a) continue;
+      add_parts(pc, a, z + 1, 1, first, c0, sum);
     }
-#pragma unroll
-    for (uint32_t i = 0; i < kBatch; ++i)
-      if (k0 + i < z) acc.add(part[i]);
-  }
-  return acc;
-}
-
-template <int DO, int E>
-__global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_t vocab,
-                                                                          const uint32_t* __restrict__ start,
-                                                                          const TokenEntry* __restrict__ entries,
-                                                                          Pieces pc, float scale, bool accumulate,
-                                                                          Rows dw) {
-  extern __shared__ float lds[];                       // [kJoinWaves][kSeg], then per piece its run's end and row
-  uint32_t* run_end = (uint32_t*)(lds + kJoinWaves * kSeg);  // 0: nothing left to add
-  uint32_t* run_row = run_end + kJoinPieces;
-  const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t mine = w / kJoinEach, p = blockIdx.x * kJoinPieces + mine;
-  const uint32_t total = start[vocab];
-  uint32_t row = 0, z = 0;  // z: past the last piece of the run that begins in p and is cut
-  if (p + 1 < pc.n) {
-    const uint32_t i1 = (p + 1) * pc.ch, before = entries[i1 - 1].row;  // inside the buffer, in use or not
-    row = entries[i1].row;
-    if (i1 < total && before == row && start[row] >= p * pc.ch) z = (start[row + 1] - 1) / pc.ch + 1;
-  }
-  const bool alone = z != 0 && z - p <= kJoinShort;
-  if (w % kJoinEach == 0) {
-    run_end[mine] = alone ? 0 : z;
-    run_row[mine] = row;
-  }
-  if (alone)
-    for (uint32_t seg = w % kJoinEach; seg < pc.segs; seg += kJoinEach) {
-      const uint64_t c0 = (uint64_t)seg * kSeg;
-      finish_row<DO, E>(dw, row, c0, pc.dim, scale, accumulate, add_parts<E>(pc, p, p, z, c0));
-    }
-  __syncthreads();
-  for (uint32_t q = 0; q < kJoinPieces; ++q) {
-    const uint32_t end = (uint32_t)__builtin_amdgcn_readfirstlane(run_end[q]);
-    if (end == 0) continue;
-    const uint32_t first = blockIdx.x * kJoinPieces + q;
-    const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane(run_row[q]);
-    // S segments at a time, 16 / S wavefronts each
-    const uint32_t S = pc.segs < 3 ? pc.segs : 4, shares = kJoinWaves / S;
-    const uint32_t per = (end - first + shares - 1) / shares, share = w / S;
-    const uint32_t a = first + share * per < end ? first + share * per : end, b = a + per < end ? a + per : end;
-    float* at = lds + w * kSeg + (threadIdx.x & 63) * 4;
-    for (uint32_t s0 = 0; s0 < pc.segs; s0 += S) {
-      const uint32_t seg = s0 + w % S;
-      const uint64_t c0 = (uint64_t)seg * kSeg;
-      SegCols<E> acc = {};
-      if (seg < pc.segs) acc = add_parts<E>(pc, first, a, b, c0);
-      store_partial(at, acc);
-      __syncthreads();
-      if (share == 0 && seg < pc.segs) {
-        for (uint32_t k = 1; k < shares; ++k) acc.add(load_partial<E>(at + k * S * kSeg));
-        finish_row<DO, E>(dw, to, c0, pc.dim, scale, accumulate, acc);
+    if (end / kGroup != first / kGroup) {  // the run's last group adds them
+      if (z > a) {
+        store_part(part_range(pc, a, a == first, c0), sum);
+        stores_done();
       }
-      __syncthreads();
+      if (arrive(&pc.counts[((uint64_t)pc.n + first) * pc.segs + seg]) != end / kGroup - first / kGroup) continue;
+      sum = load_part<E>(part_range(pc, first, 1, c0));
+      add_parts(pc, (first / kGroup + 1) * kGroup, end + 1, kGroup, first, c0, sum);
     }
+    finish_row<DO, E>(dw, to, c0, pc.dim, scale, accumulate, sum);
   }
 }
 
@@ -537,8 +544,8 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(uint64_
 // out of all ids (one a thread), zeroes the rows that have none, sorts the
 // others in LDS by counting for each how many come before it (an entry is
 // row << 10 | token, so they are ordered as numbers), and adds them in
-// sixteen pieces as above, with the partial sums in LDS.  Against the three
-// launches above: 7.4 us instead of 16.5 for 509 x 512 f32 tokens into 8192
+// sixteen pieces as above, with the partial sums in LDS.  Against three
+// launches (sort, sums, cut runs): 7.4 us instead of 16.5 for 509 x 512 f32 tokens into 8192
 // rows.
 
 constexpr uint32_t kFewTokens = 1024, kFewWaves = kFewTokens / 64, kFewRows = 1024;
@@ -661,9 +668,8 @@ hipError_t embedding_grad_few(const Rows& dout, const void* ids, bool ids64, uin
 }
 
 // Rows that one zeroing wavefront looks through, about 8 KiB: one row of 2048
-// f32 (the whole call takes 134 us so, 143 with 16 rows), 16 rows of 128 bf16
-// (44 us; with one, each wavefront waits for its row's starts for a store of
-// 256 bytes).
+// f32 (with 16 rows the whole call takes 9 us more), 16 rows of 128 bf16 (with
+// one, each wavefront waits for its row's starts for a store of 256 bytes).
 uint32_t zero_rows(uint64_t dim, int dt) {
   const uint64_t row_bytes = dim * (dt == DT_F32 ? 4 : 2);
   return row_bytes >= 8192 ? 1 : (uint32_t)std::min<uint64_t>(8192 / row_bytes, 16);
@@ -680,15 +686,11 @@ hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   const uint64_t ch = embedding_piece(a.tokens, a.dim);
   const uint32_t zrows = zero_rows(a.dim, DO);
   const Pieces pc{(uint32_t)a.tokens, (uint32_t)ch, (uint32_t)((a.tokens + ch - 1) / ch), (uint32_t)((a.dim + kSeg - 1) / kSeg), a.dim,
-                  zrows, a.partials};
+                  zrows, a.partials, a.sort.counts};
   const uint64_t units = (uint64_t)pc.n * pc.segs + (a.accumulate ? 0 : embedding_zero_waves(a.vocab, a.dim, DO));
   constexpr int waves = kThreads / 64;
   hipLaunchKernelGGL((embedding_grad_kernel<DI, DO>), dim3((unsigned)((units + waves - 1) / waves)), dim3(kThreads), 0,
                      stream, a.dout, a.vocab, a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
-  if ((e = launch_status(stream)) != hipSuccess || pc.n < 2) return e;
-  hipLaunchKernelGGL((embedding_join_kernel<DO, vec_elems<DI, DO>()>), dim3((pc.n - 1 + kJoinPieces - 1) / kJoinPieces),
-                     dim3(kJoinWaves * 64), (kJoinWaves * kSeg + 2 * kJoinPieces) * sizeof(float), stream, a.vocab,
-                     a.sort.start, a.sort.entries, pc, a.scale, a.accumulate, a.dweight);
   return launch_status(stream);
 }
 

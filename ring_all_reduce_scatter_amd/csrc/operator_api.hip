@@ -216,16 +216,19 @@ int embedding_sizes(size_t tokens, size_t vocab, size_t dim) {
   return RAR_OK;
 }
 
-// Workspace: row starts, sorted tokens, partial sums.
+// Workspace: row starts, sorted tokens, partial sums, counts.
 struct EmbeddingLayout {
-  size_t entries, partials, bytes;
+  size_t entries, partials, counts, ncounts, bytes;
 };
 EmbeddingLayout embedding_layout(size_t tokens, size_t vocab, size_t dim) {
   EmbeddingLayout l;
   const size_t ch = embedding_piece(tokens, dim);
   l.entries = round_up((vocab + 1) * sizeof(uint32_t), kAlign);
   l.partials = l.entries + round_up(tokens * sizeof(TokenEntry), kAlign);
-  l.bytes = l.partials + round_up((tokens + ch - 1) / ch * 2 * round_up(dim, 512) * sizeof(float), kAlign);
+  const size_t pieces = (tokens + ch - 1) / ch, columns = round_up(dim, 512);
+  l.counts = l.partials + pieces * 2 * columns * sizeof(float);
+  l.ncounts = pieces * 2 * (columns / 512);
+  l.bytes = l.counts + round_up(l.ncounts * sizeof(uint32_t), kAlign);
   return l;
 }
 
@@ -292,7 +295,7 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   a.vocab = vocab;
   a.dim = dim;
   a.padding = padding_id;
-  a.sort = TokenSort{(uint32_t*)base, (TokenEntry*)(base + l.entries)};
+  a.sort = TokenSort{(uint32_t*)base, (TokenEntry*)(base + l.entries), (uint32_t*)(base + l.counts), l.ncounts};
   a.partials = (float*)(base + l.partials);
   a.scale = scale;
   a.ids64 = id_type == RAR_I64;

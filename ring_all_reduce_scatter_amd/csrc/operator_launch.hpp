@@ -48,12 +48,16 @@ hipError_t launch_embedding(const Rows& weight, uint64_t vocab, uint64_t dim, co
 struct TokenEntry {
   uint32_t token, row;
 };
+// The sort also clears the counts that the gradient's launch begins with.
 struct TokenSort {
   uint32_t* start;
   TokenEntry* entries;
+  uint32_t* counts;
+  uint64_t ncounts;
 };
 // Entries that one wavefront of the gradient takes; partials holds two rows
-// of dim floats, rounded up to 512, for each such piece.
+// of dim floats, rounded up to 512, for each such piece, counts two words
+// for each piece and 512 columns.
 uint64_t embedding_piece(uint64_t tokens, uint64_t dim);
 // Wavefronts that zero the rows without tokens.
 uint64_t embedding_zero_waves(uint64_t vocab, uint64_t dim, int dt);

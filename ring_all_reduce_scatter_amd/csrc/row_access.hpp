@@ -157,6 +157,13 @@ __device__ __forceinline__ void store_elem_dt(char* base, uint64_t i, int dt, fl
   else store_elem<DT_BF16>(base, i, x);
 }
 
+// This wavefront's stores have been acknowledged.
+__device__ __forceinline__ void stores_done() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
 // Sums over a DPP row of 16 lanes, and over the 64 lanes of a wavefront (all
 // active); every lane receives its own.  The four rows of a wavefront are
 // joined by scalar reads.
