@@ -540,28 +540,29 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
 
 // ------------------------------------------------------------------ gradient of few tokens
 // Up to kFewTokens tokens are sorted, added and stored by one launch.  A
-// workgroup takes R table rows and kSeg columns: it picks its rows' tokens
-// out of all ids (one a thread), zeroes the rows that have none, sorts the
-// others in LDS by counting for each how many come before it (an entry is
-// row << 10 | token, so they are ordered as numbers), and adds them in
-// sixteen pieces as above, with the partial sums in LDS.  Against three
-// launches (sort, sums, cut runs): 7.4 us instead of 16.5 for 509 x 512 f32 tokens into 8192
-// rows.
+// workgroup of W wavefronts takes R table rows and kSeg columns: it picks its
+// rows' tokens out of all ids (one a thread), zeroes the rows that have none,
+// sorts the others in LDS by counting for each how many come before it (an
+// entry is row << 10 | token, so they are ordered as numbers), and adds them
+// in W pieces as above, with the partial sums in LDS.  Against three launches
+// (sort, sums, cut runs): 7.4 us instead of 16.5 for 509 x 512 f32 tokens
+// into 8192 rows.  Four wavefronts are enough for 256 tokens, and more of
+// these workgroups fit a CU: 100 x 512 f32 tokens into 32,768 rows take 12.9
+// us so, 14.1 with sixteen.
+constexpr uint32_t kFewTokens = 1024, kFewRows = 1024;
 
-constexpr uint32_t kFewTokens = 1024, kFewWaves = kFewTokens / 64, kFewRows = 1024;
-
-template <int DI, int DO, typename ID>
-__global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dout, const ID* __restrict__ ids,
+template <int DI, int DO, typename ID, uint32_t W>
+__global__ __launch_bounds__(W * 64) void embedding_grad_few_kernel(Rows dout, const ID* __restrict__ ids,
                                                                          uint32_t tokens, uint32_t vocab, uint64_t dim,
                                                                          int64_t padding, uint32_t R, float scale,
                                                                          bool accumulate, Rows dw) {
   constexpr int E = vec_elems<DI, DO>();
   extern __shared__ uint32_t sm[];
-  uint32_t* count = sm;                                            // [kFewWaves]
-  uint32_t* used = sm + kFewWaves;                                 // [kFewRows / 32] bits
-  uint32_t* list = used + kFewRows / 32;                           // [kFewTokens]
-  uint32_t* sorted = list + kFewTokens;                            // [kFewTokens]
-  float* part = (float*)(sorted + kFewTokens);                     // [kFewWaves][2][kSeg]
+  uint32_t* count = sm;                      // [W]
+  uint32_t* used = sm + W;                   // [kFewRows / 32] bits
+  uint32_t* list = used + kFewRows / 32;     // [W * 64]
+  uint32_t* sorted = list + W * 64;          // [W * 64]
+  float* part = (float*)(sorted + W * 64);   // [W][2][kSeg]
   const uint32_t tid = threadIdx.x, lane = tid & 63;
   const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t lo = blockIdx.x * R, rows = vocab - lo < R ? vocab - lo : R;
@@ -574,7 +575,7 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
   __syncthreads();
   uint32_t at = (uint32_t)__popcll(mask & lanes_before()), total = 0;
 #pragma unroll
-  for (uint32_t k = 0; k < kFewWaves; ++k) {
+  for (uint32_t k = 0; k < W; ++k) {
     if (k < w) at += count[k];
     total += count[k];
   }
@@ -594,14 +595,14 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
   }
   if (!accumulate)
     // whole rows, shared out among the workgroups of these rows
-    for (uint32_t r = w * gridDim.y + blockIdx.y; r < rows; r += kFewWaves * gridDim.y)
+    for (uint32_t r = w * gridDim.y + blockIdx.y; r < rows; r += W * gridDim.y)
       if (!(used[r >> 5] >> (r & 31) & 1u))
         for (uint32_t k = 0; k < gridDim.y; ++k)
           store_seg<DO, vec_elems<DO, DO>(), false>(dw.p, (uint64_t)(lo + r) * dw.stride, (uint64_t)k * kSeg, dim, {});
   if (total == 0) return;
   __syncthreads();
   // pieces of ch entries, the w-th this wavefront's
-  const uint32_t ch = (total + kFewWaves - 1) / kFewWaves;
+  const uint32_t ch = (total + W - 1) / W;
   const uint32_t i0 = w * ch, i1 = i0 + ch < total ? i0 + ch : total;
   float* mine = part + lane * 4;
   bool begins = false;  // a run begins in this piece and goes on in the next
@@ -646,24 +647,22 @@ __global__ __launch_bounds__(kFewTokens) void embedding_grad_few_kernel(Rows dou
   finish_row<DO, E, false>(dw, lo + row, c0, dim, scale, accumulate, acc);
 }
 
-template <int DI, int DO>
-hipError_t embedding_grad_few(const Rows& dout, const void* ids, bool ids64, uint64_t tokens, uint64_t vocab,
-                              uint64_t dim, int64_t padding, float scale, bool accumulate, const Rows& dw,
-                              hipStream_t stream) {
-  const uint64_t segs = (dim + kSeg - 1) / kSeg;
-  // two workgroups per CU, each of at least a row per wavefront
-  uint64_t R = (vocab * segs + 511) / 512;
-  R = R < kFewWaves ? kFewWaves : (R > kFewRows ? kFewRows : R);
-  const dim3 grid((unsigned)((vocab + R - 1) / R), (unsigned)segs), block(kFewTokens);
-  const size_t lds = (kFewWaves + kFewRows / 32 + 2 * kFewTokens + kFewWaves * 2 * kSeg) * sizeof(uint32_t);
-  if (ids64)
-    hipLaunchKernelGGL((embedding_grad_few_kernel<DI, DO, int64_t>), grid, block, lds, stream, dout,
-                       (const int64_t*)ids, (uint32_t)tokens, (uint32_t)vocab, dim, padding, (uint32_t)R, scale,
-                       accumulate, dw);
+template <int DI, int DO, uint32_t W>
+hipError_t embedding_grad_few(const EmbeddingGrad& a, hipStream_t stream) {
+  const uint64_t segs = (a.dim + kSeg - 1) / kSeg;
+  // 32 wavefronts per CU, each workgroup of at least a row per wavefront
+  constexpr uint64_t groups = 256 * 32 / W;
+  const uint64_t R = std::min<uint64_t>(std::max<uint64_t>((a.vocab * segs + groups - 1) / groups, W), kFewRows);
+  const dim3 grid((unsigned)((a.vocab + R - 1) / R), (unsigned)segs), block(W * 64);
+  const size_t lds = (W + kFewRows / 32 + 2 * W * 64 + W * 2 * kSeg) * sizeof(uint32_t);
+  if (a.ids64)
+    hipLaunchKernelGGL((embedding_grad_few_kernel<DI, DO, int64_t, W>), grid, block, lds, stream, a.dout,
+                       (const int64_t*)a.ids, (uint32_t)a.tokens, (uint32_t)a.vocab, a.dim, a.padding, (uint32_t)R,
+                       a.scale, a.accumulate, a.dweight);
   else
-    hipLaunchKernelGGL((embedding_grad_few_kernel<DI, DO, int32_t>), grid, block, lds, stream, dout,
-                       (const int32_t*)ids, (uint32_t)tokens, (uint32_t)vocab, dim, padding, (uint32_t)R, scale,
-                       accumulate, dw);
+    hipLaunchKernelGGL((embedding_grad_few_kernel<DI, DO, int32_t, W>), grid, block, lds, stream, a.dout,
+                       (const int32_t*)a.ids, (uint32_t)a.tokens, (uint32_t)a.vocab, a.dim, a.padding, (uint32_t)R,
+                       a.scale, a.accumulate, a.dweight);
   return launch_status(stream);
 }
 
@@ -679,8 +678,7 @@ template <int DI, int DO>
 hipError_t embedding_grad_typed(const EmbeddingGrad& a, hipStream_t stream) {
   if (a.tokens == 0 && a.accumulate) return hipSuccess;
   if (a.tokens > 0 && a.tokens <= kFewTokens && a.dim <= (uint64_t)kSeg * 65535)
-    return embedding_grad_few<DI, DO>(a.dout, a.ids, a.ids64, a.tokens, a.vocab, a.dim, a.padding, a.scale,
-                                      a.accumulate, a.dweight, stream);
+    return a.tokens <= 256 ? embedding_grad_few<DI, DO, 4>(a, stream) : embedding_grad_few<DI, DO, 16>(a, stream);
   hipError_t e = token_sort(a.ids, a.ids64, a.tokens, a.vocab, a.padding, a.sort, stream);
   if (e != hipSuccess) return e;
   const uint64_t ch = embedding_piece(a.tokens, a.dim);
