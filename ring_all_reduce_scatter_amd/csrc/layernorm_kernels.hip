@@ -10,8 +10,8 @@
 //
 // A row stays in the registers of NT lanes, V vectors a lane, from its load
 // to its store, so memory is read and written once: 16 lanes for short rows,
-// a wavefront, or four or eight of them.  Rows too long for that go through
-// the loops at the end of this file, which read a row once per pass.
+// a wavefront, or two, four or eight of them.  Rows too long for that go
+// through the loops at the end of this file, which read a row once per pass.
 // The lanes per row follow from the row's length alone.  Both directions are
 // bound by memory for batches, by launch latency for few rows.  Times on one
 // MI355X, inputs cold: forward 16,384 x 4096 f16 46 us (5.8 TB/s of 268 MB),
@@ -557,6 +557,11 @@ hipError_t layernorm_dt(const Rows& x, const void* weight, const void* bias, int
   if (vecs <= 64) RAR_FORWARD(16, 4, 16);
   if (vecs <= 128) RAR_FORWARD(64, 2, 4);
   if (vecs <= 256) RAR_FORWARD(64, 4, 4);
+  // Between, three vectors on each of two wavefronts' lanes: 67 million values
+  // in rows of 2560 bf16 46.7 us (60 with 256 lanes, whose second vectors most
+  // lanes lack), of 2816 46.8 (56).  In binary32 the gain ends sooner: 1200
+  // columns 91 us (98), 1344 91.7 (92.8), 1440 93 (90).
+  if (vecs <= (DT == DT_F32 ? 340 : 384)) RAR_FORWARD(128, 3, 2);
   if (vecs <= 512) RAR_FORWARD(256, 2, 1);
   if (vecs <= 1024) RAR_FORWARD(256, 4, 1);
   if (vecs <= 2048) RAR_FORWARD(512, 4, 1);
@@ -610,6 +615,8 @@ hipError_t layernorm_grad_dt(const LayernormGrad& a, uint64_t rows, uint64_t dim
   if (vecs <= 64) return backward_rows<DT, 16, 4, 32>(a, rows, dim, stream);
   if (vecs <= 128) return backward_rows<DT, 64, 2, 8>(a, rows, dim, stream);
   if (vecs <= 256) return backward_rows<DT, 64, 4, 8>(a, rows, dim, stream);
+  // 2560 bf16 columns 74 us (87 with 256 lanes), 1200 binary32 140 (148).
+  if (vecs <= 384) return backward_rows<DT, 128, 3, 4>(a, rows, dim, stream);
   if (vecs <= 512) return backward_rows<DT, 256, 2, 2>(a, rows, dim, stream);
   if (vecs <= 1024) return backward_rows<DT, 256, 4, 2>(a, rows, dim, stream);
   if (vecs <= 2048) return backward_rows<DT, 512, 4, 1>(a, rows, dim, stream);

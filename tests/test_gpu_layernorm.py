@@ -46,7 +46,8 @@ def _check_backward(dy, x, w, mean, rstd, got, wdt, old=(None, None), what=""):
 
 SHAPES = [(1, 1), (3, 2), (1, 64), (5, 63), (70, 129), (4, 512), (33, 513), (257, 768), (1, 1000), (130, 1024),
           (9, 1025), (65, 2048), (3, 2049), (1, 4096), (40, 4096), (17, 4097), (5, 8192), (11, 8191), (3, 16384),
-          (2, 16391), (3, 40_003), (2000, 96), (9000, 33)]
+          (2, 16391), (3, 40_003), (2000, 96), (9000, 33), (37, 2561),
+          (20, 1300), (600, 40), (700, 250), (513, 2570), (1, 300)]
 
 
 @pytest.mark.parametrize("dts", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
