@@ -550,7 +550,8 @@ int rar_grad_prepare(void* const* grads, void* const* outs, const size_t* counts
  * 0 for a set without elements.  scale = 1/N makes a ring's sum over N ranks
  * their mean.  An L2 norm is summed in binary64, so no finite gradient
  * overflows or vanishes in it.  A NaN anywhere gives NaN, else an infinity
- * gives infinity. */
+ * gives infinity.  norm must lie apart from the workspace (RAR_EOVERLAP) and
+ * from the set's tensors, which only the caller can check. */
 int rar_grad_norm(const rar_grad_plan* plan, int norm_type, double scale, float* norm, void* stream);
 
 /* The same norm, then every output <- round(gradient * f) with

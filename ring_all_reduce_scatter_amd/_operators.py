@@ -12,6 +12,7 @@ refused with ValueError before any launch.
 from __future__ import annotations
 
 import ctypes
+from bisect import bisect_right
 
 from . import _binding
 from ._binding import F32, GradPlan, RarError, _sizes, dtype_code, lib
@@ -148,6 +149,25 @@ def _is_dense(t) -> bool:
     return True
 
 
+def _merged(ranges):
+    """Address ranges [begin, end) in order, joined where they overlap:
+    (begins, ends)."""
+    begins, ends = [], []
+    for a, b in sorted(ranges):
+        if ends and a < ends[-1]:
+            ends[-1] = max(ends[-1], b)
+        else:
+            begins.append(a)
+            ends.append(b)
+    return begins, ends
+
+
+def _touches(begins, ends, a: int, nbytes: int) -> bool:
+    """Whether [a, a + nbytes) meets one of the merged ranges."""
+    i = bisect_right(begins, a + nbytes - 1) - 1
+    return i >= 0 and ends[i] > a
+
+
 class GradClip:
     """Global norm and clipping of fixed gradient tensors, prepared once.
 
@@ -185,6 +205,7 @@ class GradClip:
         ws, nbytes = _workspace(workspace)
         self._keep = (grads, outs, workspace)
         self._ws = workspace
+        self._ranges = None
         self._plan = GradPlan()
         rc = (_binding._lib or lib()).rar_grad_prepare(
             ptrs, optrs, _sizes([g.numel() for g in grads]), dts, odts, n, ws, nbytes, ctypes.byref(self._plan),
@@ -192,16 +213,26 @@ class GradClip:
         _check(rc, "rar_grad_prepare")
         self._ref = ctypes.byref(self._plan)
 
-    def norm(self, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
-        """norm (one float32 on the device) <- |scale| * the norm of all gradients."""
+    def _norm_address(self, norm):
         address = _floats(norm, 1, "norm")
+        if self._ranges is None:  # empty tensors have no address
+            self._ranges = _merged((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                                   for ts in self._keep[:2] for t in ts or () if t.numel())
+        if norm is not None and _touches(*self._ranges, address, 4):
+            raise ValueError("norm must lie apart from the gradients and outputs")
+        return address
+
+    def norm(self, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
+        """norm (one float32 on the device, apart from the tensors) <- |scale|
+        * the norm of all gradients."""
+        address = self._norm_address(norm)
         _on_gpu(norm)
         rc = (_binding._lib or lib()).rar_grad_norm(self._ref, norm_type, scale, address, _stream(stream, self._ws))
         _check(rc, "rar_grad_norm")
 
     def clip(self, max_norm: float, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
         """The same norm, and every gradient times scale * min(1, max_norm / (norm + 1e-6))."""
-        address = _floats(norm, 1, "norm")
+        address = self._norm_address(norm)
         _on_gpu(norm)
         rc = (_binding._lib or lib()).rar_grad_clip(
             self._ref, norm_type, scale, max_norm, address, _stream(stream, self._ws))

@@ -93,12 +93,19 @@ ClipSet clip_set(const rar_grad_plan* p) {
   return ClipSet{ws + p->desc_offset, ws + p->partial_offset, result, result + kClipCountBytes, p->ntiles};
 }
 
+// The norm is written while the workspace is read, so it has to lie apart
+// from it; that it lies apart from the tensors the caller has to see to
+// (their addresses are in the workspace, which the host does not read).
 int check_plan(const rar_grad_plan* p, int norm_type, double scale, const float* norm) {
   if (!p || !p->workspace || ((uintptr_t)p->workspace & 15u) || p->ntiles > kMaxTiles) return RAR_EINVAL;
   if (p->desc_offset == 0 || (p->desc_offset | p->partial_offset | p->result_offset) & 15u) return RAR_EINVAL;
   if (norm_type != RAR_NORM_L2 && norm_type != RAR_NORM_MAX) return RAR_EINVAL;
   if (!std::isfinite(scale)) return RAR_EINVAL;
-  return check_ptr(norm, sizeof(float));
+  const int rc = check_ptr(norm, sizeof(float));
+  if (rc) return rc;
+  const Range r[] = {{(uintptr_t)norm, sizeof(float), true, 0},
+                     {(uintptr_t)p->workspace, p->result_offset + kClipCountBytes + kAlign, true, 0}};
+  return check_ranges(r, 2);
 }
 
 int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, const int* dtypes,

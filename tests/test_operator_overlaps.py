@@ -1,0 +1,51 @@
+"""Overlaps that the gradient operators' calls refuse or serve, before any
+launch.  CPU only: the addresses are never read."""
+import ctypes
+
+import pytest
+import torch
+
+import ring_all_reduce_scatter_amd as rar
+from ring_all_reduce_scatter_amd import _binding as b
+from ring_all_reduce_scatter_amd import _operators as op
+
+OK, EOVERLAP = 0, 7
+B, G = 1 << 40, 1 << 30
+
+
+def _empty_plan():
+    L, p = rar.lib(), b.GradPlan()
+    need = L.rar_grad_workspace_bytes(None, 0)
+    assert L.rar_grad_prepare(None, None, None, None, None, 0, B, need, ctypes.byref(p), None) == OK
+    return p, need
+
+
+def test_norm_in_the_workspace_is_refused():
+    """Written there it would change descriptors (addresses) or counts that
+    the same call reads."""
+    L = rar.lib()
+    p, need = _empty_plan()
+    for at in (B, B + 4, B + p.desc_offset, B + p.partial_offset + 8, B + p.result_offset, B + need - 4):
+        assert L.rar_grad_norm(ctypes.byref(p), 0, 1.0, at, None) == EOVERLAP, hex(at)
+        assert L.rar_grad_clip(ctypes.byref(p), 1, 1.0, 1.0, at, None) == EOVERLAP, hex(at)
+
+
+def test_merged_ranges():
+    begins, ends = op._merged([(100, 200), (300, 304), (150, 260), (200, 210), (260, 264)])
+    assert list(zip(begins, ends)) == [(100, 260), (260, 264), (300, 304)]
+    for a, n, hit in ((96, 4, False), (97, 4, True), (256, 4, True), (260, 4, True), (264, 4, False), (296, 4, False),
+                      (297, 4, True), (300, 4, True), (304, 4, False), (0, 4, False), (0, 1000, True)):
+        assert op._touches(begins, ends, a, n) == hit, (a, n)
+    assert not op._touches([], [], 5, 4)
+
+
+def test_norm_among_the_tensors_is_refused_by_the_binding():
+    clip = op.GradClip.__new__(op.GradClip)  # without a device there is no plan to prepare
+    flat, outs = torch.zeros(64), torch.zeros(32, dtype=torch.float16)
+    clip._keep = ([flat[:32], flat[40:41], torch.empty(0)], [outs[:16], outs[20:21]], None)
+    clip._ranges = None
+    for bad in (flat[:1], flat[31:32], flat[40:41], outs[14:16].view(torch.float32), outs[20:22].view(torch.float32)):
+        with pytest.raises(ValueError, match="apart from"):
+            clip._norm_address(bad)
+    for good in (flat[32:33], flat[39:40], flat[41:42], torch.zeros(1)):
+        assert clip._norm_address(good) == good.data_ptr()
