@@ -550,14 +550,15 @@ int rar_grad_prepare(void* const* grads, void* const* outs, const size_t* counts
  * 0 for a set without elements.  scale = 1/N makes a ring's sum over N ranks
  * their mean.  An L2 norm is summed in binary64, so no finite gradient
  * overflows or vanishes in it.  A NaN anywhere gives NaN, else an infinity
- * gives infinity.  norm must lie apart from the workspace (RAR_EOVERLAP) and
- * from the set's tensors, which only the caller can check. */
+ * gives infinity (NaN where scale is 0).  norm must lie apart from the
+ * workspace (RAR_EOVERLAP) and from the set's tensors, which only the caller
+ * can check. */
 int rar_grad_norm(const rar_grad_plan* plan, int norm_type, double scale, float* norm, void* stream);
 
 /* The same norm, then every output <- round(gradient * f) with
- * f = scale * min(1, max_norm / (norm + 1e-6)) rounded to binary32.  An
- * infinite norm makes f zero, a NaN norm makes every output NaN.
- * max_norm >= 0 (infinity scales without clipping), scale finite. */
+ * f = scale * min(1, max_norm / (norm + 1e-6)) rounded to binary32.  A NaN
+ * norm makes every output NaN; else an infinite max_norm gives f = scale (no
+ * clipping) and an infinite norm makes f zero.  max_norm >= 0, scale finite. */
 int rar_grad_clip(const rar_grad_plan* plan, int norm_type, double scale, double max_norm,
                   float* norm, void* stream);
 

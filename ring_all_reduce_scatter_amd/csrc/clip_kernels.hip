@@ -168,7 +168,8 @@ __device__ __forceinline__ float finish_norm(const Acc<KIND>& acc, const NormRes
   else total = __builtin_sqrt(acc.s);
   total *= __builtin_fabs(m.scale);
   double c = m.max_norm / (total + 1e-6);
-  if (c > 1.0) c = 1.0;  // a NaN norm stays a NaN factor
+  // a NaN norm stays a NaN factor; infinity over infinity is no limit either
+  if (!(c <= 1.0) && total == total) c = 1.0;
   const float f = (float)(m.scale * c);
   if (threadIdx.x == 0) {
     *m.norm = (float)total;

@@ -246,3 +246,28 @@ def test_norm_groups_take_tiles_in_turns(dt, n, kind):
         r = g.double() * f
         tol = ref.rounded(r, r.abs() * 2 * U + 2.0 ** -148, o.dtype)
         assert bool(((o.double() - r).abs() <= tol).all()), f"tensor {i}"
+
+
+@pytest.mark.parametrize("kind", [rar.NORM_L2, rar.NORM_MAX])
+@pytest.mark.parametrize("n", [3000, 300_001])  # one launch, and two
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_infinite_max_norm_only_scales(dt, n, kind):
+    """One overflowed element of a set that is unscaled: the others keep their
+    values.  A NaN still makes everything NaN, and so does zero times infinity."""
+    gen = _gen(n)
+    g = torch.randn(n, generator=gen, device=DEV).to(DTYPES[dt])
+    g[n // 2] = -math.inf
+    ws, norm, out = _bytes(rar.grad_clip_workspace_bytes([n])), torch.zeros(1, device=DEV), torch.empty_like(g)
+    plan = rar.GradClip([g], ws, outs=[out])
+    for scale in (1.0, -0.25):
+        out.fill_(3.0)
+        plan.clip(math.inf, norm, kind, scale=scale)
+        assert norm.item() == math.inf
+        _same(out, (g.float() * scale).to(g.dtype), f"scale {scale}")
+    plan.clip(math.inf, norm, kind, scale=0.0)
+    assert math.isnan(norm.item()) and bool(out.isnan().all())
+    plan.clip(1e30, norm, kind)  # a finite limit: the factor is zero
+    assert norm.item() == math.inf and int((out != 0).sum()) == 1 and bool(out[n // 2].isnan())
+    g[0] = math.nan
+    plan.clip(math.inf, norm, kind)
+    assert math.isnan(norm.item()) and bool(out.isnan().all())
