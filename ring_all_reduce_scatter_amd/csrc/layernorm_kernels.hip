@@ -411,8 +411,10 @@ __global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGr
 
 // Adds the partial rows: 64 columns of dw (blockIdx.y = 0) or db per
 // workgroup, each wavefront every kJoinWaves-th partial row, the wavefronts
-// in order.
+// in order.  The workgroups of more columns than one grid dimension holds
+// (2^32 threads) lie in blockIdx.z.
 constexpr int kJoinWaves = 16;
+constexpr uint64_t kJoinGridX = 1 << 20;
 
 __global__ __launch_bounds__(kJoinWaves * 64) void layernorm_join_kernel(LayernormGrad a, uint64_t splits,
                                                                           uint64_t dim) {
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void layernorm_join_kernel(Layerno
   void* out = blockIdx.y ? a.dbias : a.dweight;
   if (!out) return;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const uint64_t c = (uint64_t)blockIdx.x * 64 + lane;
+  const uint64_t c = (blockIdx.z * kJoinGridX + blockIdx.x) * 64 + lane;
   const float* p = a.partials + blockIdx.y * dim + c;
   float v = 0.0f;
   if (c < dim)
@@ -575,8 +577,10 @@ hipError_t layernorm_dt(const Rows& x, const void* weight, const void* bias, int
 
 hipError_t join_partials(const LayernormGrad& a, uint64_t splits, uint64_t dim, hipStream_t stream) {
   if (!a.dweight && !a.dbias) return hipSuccess;
-  hipLaunchKernelGGL(layernorm_join_kernel, dim3((unsigned)((dim + 63) / 64), 2), dim3(kJoinWaves * 64),
-                     kJoinWaves * 64 * sizeof(float), stream, a, splits, dim);
+  const uint64_t groups = (dim + 63) / 64;
+  const dim3 grid((unsigned)std::min(groups, kJoinGridX), 2, (unsigned)((groups + kJoinGridX - 1) / kJoinGridX));
+  hipLaunchKernelGGL(layernorm_join_kernel, grid, dim3(kJoinWaves * 64), kJoinWaves * 64 * sizeof(float), stream, a,
+                     splits, dim);
   return launch_status(stream);
 }
 

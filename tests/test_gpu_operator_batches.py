@@ -203,6 +203,23 @@ def test_layernorm_backward_of_long_rows_in_row_groups(rows, dim, dts):
     _check_grad_batch(rows, dim, *dts, seed=rows)
 
 
+@pytest.mark.parametrize("dim", [(1 << 28) - 1, (1 << 28) + 70])
+def test_layernorm_backward_of_rows_past_one_grid_dimension(dim):
+    """2^28 columns are 2^32 threads of the launch that adds partial rows."""
+    rows = 2
+    gen = _gen(9)
+    pattern = torch.randint(-3, 4, (rows, dim), generator=gen, device=DEV, dtype=torch.int8)
+    x, dy = pattern.to(torch.bfloat16), pattern.roll(1, 1).to(torch.bfloat16)
+    mean, rstd = torch.tensor([1.0, -1.0], device=DEV), torch.tensor([0.5, 2.0], device=DEV)
+    dw = torch.full((dim,), 7.0, device=DEV, dtype=torch.bfloat16)
+    db = torch.full_like(dw, 7.0)
+    ws = _bytes(rar.layernorm_workspace_bytes(rows, dim))
+    rar.layernorm_backward(dy, x, None, mean, rstd, None, dw, db, ws)
+    h = (x.float() - mean[:, None]) * rstd[:, None]
+    _same(dw, (dy.float() * h).sum(0).to(torch.bfloat16), "dw")
+    _same(db, dy.float().sum(0).to(torch.bfloat16), "db")
+
+
 # ------------------------------------------------------------------ norm and clip
 
 def _norm_of(grads, kind):
