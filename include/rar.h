@@ -519,13 +519,15 @@ typedef enum rar_id_type { RAR_I32 = 0, RAR_I64 = 1 } rar_id_type;
 typedef enum rar_norm_type { RAR_NORM_L2 = 0, RAR_NORM_MAX = 1 } rar_norm_type;
 
 /* A set of gradient tensors prepared once and measured or clipped many
- * times.  Plain data owned by the caller; filled by rar_grad_prepare. */
+ * times.  Plain data owned by the caller; filled by rar_grad_prepare or
+ * rar_grad_prepare_norm. */
 typedef struct {
   void* workspace;          /* the prepared workspace */
   uint64_t desc_offset;     /* bytes from workspace to the tile descriptors */
   uint64_t partial_offset;  /* ... to the partial sums */
   uint64_t result_offset;   /* ... to the counts of arrived workgroups and the last factor */
   uint64_t ntiles;
+  uint64_t clips;           /* 0: prepared for its norm alone */
 } rar_grad_plan;
 
 /* Workspace for rar_grad_prepare; 0 on bad args.  A set may hold up to
@@ -545,6 +547,12 @@ size_t rar_grad_workspace_bytes(const size_t* counts, size_t ntensors);
 int rar_grad_prepare(void* const* grads, void* const* outs, const size_t* counts, const int* dtypes,
                      const int* out_dtypes, size_t ntensors, void* workspace, size_t ws_bytes,
                      rar_grad_plan* plan, void* stream);
+
+/* The same for the norm alone: the tensors are read only, so they may
+ * overlap one another and a tensor that the set holds twice counts twice.
+ * rar_grad_clip refuses such a plan (RAR_EINVAL). */
+int rar_grad_prepare_norm(void* const* grads, const size_t* counts, const int* dtypes, size_t ntensors,
+                          void* workspace, size_t ws_bytes, rar_grad_plan* plan, void* stream);
 
 /* *norm (device, binary32) <- |scale| * the norm of all elements of the set;
  * 0 for a set without elements.  scale = 1/N makes a ring's sum over N ranks

@@ -55,7 +55,7 @@ class GradPlan(ctypes.Structure):
     """Mirror of rar_grad_plan: a prepared set of gradient tensors."""
     _fields_ = [("workspace", ctypes.c_void_p), ("desc_offset", ctypes.c_uint64),
                 ("partial_offset", ctypes.c_uint64), ("result_offset", ctypes.c_uint64),
-                ("ntiles", ctypes.c_uint64)]
+                ("ntiles", ctypes.c_uint64), ("clips", ctypes.c_uint64)]
 
 
 class CompressCfg(ctypes.Structure):
@@ -127,6 +127,7 @@ _SIGS = {
     "rar_grad_workspace_bytes": (_c_size, [_c_vp, _c_size]),
     "rar_grad_prepare": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_size, _c_vp, _c_size,
                                   ctypes.POINTER(GradPlan), _c_vp]),
+    "rar_grad_prepare_norm": (_c_int, [_c_vp, _c_vp, _c_vp, _c_size, _c_vp, _c_size, ctypes.POINTER(GradPlan), _c_vp]),
     "rar_grad_norm": (_c_int, [ctypes.POINTER(GradPlan), _c_int, ctypes.c_double, _c_vp, _c_vp]),
     "rar_grad_clip": (_c_int, [ctypes.POINTER(GradPlan), _c_int, ctypes.c_double, ctypes.c_double, _c_vp, _c_vp]),
     "rar_embedding_forward": (_c_int, [_c_vp, _c_size, _c_int, _c_size, _c_size, _c_vp, _c_int, _c_size,

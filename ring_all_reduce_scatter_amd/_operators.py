@@ -174,19 +174,22 @@ class GradClip:
     grads: device tensors of any mix of float32, float16 and bfloat16, each
     filling one range of memory.  outs: where clip() writes, one tensor per
     gradient with its shape and strides (any of the three types); None clips
-    in place.  workspace: grad_clip_workspace_bytes([g.numel() for g in
+    in place.  norm_only: nothing is written and clip() is refused, so the
+    gradients may overlap (one that is held twice counts twice).  workspace: grad_clip_workspace_bytes([g.numel() for g in
     grads]) bytes.  Everything must stay alive and keep its storage, and
     nothing else may write the workspace, while this object is used; its
     calls use the one workspace, so they must follow one another (one stream,
     or streams that wait for each other)."""
 
-    def __init__(self, grads, workspace, outs=None, stream=None):
+    def __init__(self, grads, workspace, outs=None, stream=None, norm_only: bool = False):
         grads = list(grads)
         outs = None if outs is None else list(outs)
         for g in grads:
             if not _is_dense(g):
                 raise ValueError("gradients must fill one range of memory (no gaps, no expanded dimensions)")
         if outs is not None:
+            if norm_only:
+                raise ValueError("a set prepared for its norm alone has no outputs")
             if len(outs) != len(grads):
                 raise ValueError("need one output per gradient")
             for g, o in zip(grads, outs):
@@ -207,11 +210,13 @@ class GradClip:
         self._ws = workspace
         self._ranges = None
         self._plan = GradPlan()
-        rc = (_binding._lib or lib()).rar_grad_prepare(
-            ptrs, optrs, _sizes([g.numel() for g in grads]), dts, odts, n, ws, nbytes, ctypes.byref(self._plan),
-            _stream(stream, workspace))
+        counts, plan, st = _sizes([g.numel() for g in grads]), ctypes.byref(self._plan), _stream(stream, workspace)
+        if norm_only:
+            rc = (_binding._lib or lib()).rar_grad_prepare_norm(ptrs, counts, dts, n, ws, nbytes, plan, st)
+        else:
+            rc = (_binding._lib or lib()).rar_grad_prepare(ptrs, optrs, counts, dts, odts, n, ws, nbytes, plan, st)
         _check(rc, "rar_grad_prepare")
-        self._ref = ctypes.byref(self._plan)
+        self._ref = plan
 
     def _norm_address(self, norm):
         address = _floats(norm, 1, "norm")
@@ -240,8 +245,8 @@ class GradClip:
 
 
 def grad_norm(grads, workspace, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
-    """One GradClip(grads, workspace).norm(...): preparation and norm."""
-    GradClip(grads, workspace, stream=stream).norm(norm, norm_type, scale, stream)
+    """One GradClip(grads, workspace, norm_only=True).norm(...): preparation and norm."""
+    GradClip(grads, workspace, stream=stream, norm_only=True).norm(norm, norm_type, scale, stream)
 
 
 def clip_grad_norm(grads, max_norm: float, workspace, norm, outs=None, norm_type: int = NORM_L2, scale: float = 1.0,

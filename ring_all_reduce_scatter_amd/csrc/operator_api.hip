@@ -108,7 +108,9 @@ int check_plan(const rar_grad_plan* p, int norm_type, double scale, const float*
   return check_ranges(r, 2);
 }
 
-int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, const int* dtypes,
+// clips: the set is written, to outs or (NULL) in place; without, its tensors
+// are only read and may overlap.
+int grad_prepare(void* const* grads, bool clips, void* const* outs, const size_t* counts, const int* dtypes,
                  const int* out_dtypes, size_t nt, void* workspace, size_t ws_bytes, rar_grad_plan* plan,
                  hipStream_t st) {
   if (!plan || (nt && (!grads || !counts || !dtypes)) || (outs && !out_dtypes)) return RAR_EINVAL;
@@ -127,7 +129,7 @@ int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, co
     int rc = check_ptr(grads[t], es_of(dtypes[t]));
     if (!rc) rc = check_ptr(out, es_of(odt));
     if (rc) return rc;
-    o.push_back(Out{(uintptr_t)out, counts[t] * es_of(odt), t});
+    if (clips) o.push_back(Out{(uintptr_t)out, counts[t] * es_of(odt), t});
   }
   if (!workspace || ws_bytes < l.bytes) return RAR_EWORKSPACE;
   if ((uintptr_t)workspace & 15u) return RAR_EALIGN;
@@ -166,6 +168,7 @@ int grad_prepare(void* const* grads, void* const* outs, const size_t* counts, co
   p.partial_offset = l.partials;
   p.result_offset = l.result;
   p.ntiles = tiles;
+  p.clips = clips;
   if (tiles) {
     const uint64_t none[kClipCountBytes / sizeof(uint64_t)] = {};  // no workgroup has arrived
     int rc = hip_rc(launch_fill_u64((uint64_t*)((char*)workspace + l.result), none,
@@ -192,9 +195,19 @@ int rar_grad_prepare(void* const* grads, void* const* outs, const size_t* counts
                      const int* out_dtypes, size_t ntensors, void* workspace, size_t ws_bytes, rar_grad_plan* plan,
                      void* stream) {
   try {
-    return grad_prepare(grads, outs, counts, dtypes, out_dtypes, ntensors, workspace, ws_bytes, plan,
+    return grad_prepare(grads, true, outs, counts, dtypes, out_dtypes, ntensors, workspace, ws_bytes, plan,
                         (hipStream_t)stream);
   } catch (...) {  // host memory for the checks or the table
+    return RAR_EHIP;
+  }
+}
+
+int rar_grad_prepare_norm(void* const* grads, const size_t* counts, const int* dtypes, size_t ntensors,
+                          void* workspace, size_t ws_bytes, rar_grad_plan* plan, void* stream) {
+  try {
+    return grad_prepare(grads, false, nullptr, counts, dtypes, nullptr, ntensors, workspace, ws_bytes, plan,
+                        (hipStream_t)stream);
+  } catch (...) {
     return RAR_EHIP;
   }
 }
@@ -209,7 +222,7 @@ int rar_grad_clip(const rar_grad_plan* plan, int norm_type, double scale, double
                   void* stream) {
   const int rc = check_plan(plan, norm_type, scale, norm);
   if (rc) return rc;
-  if (!(max_norm >= 0.0)) return RAR_EINVAL;
+  if (!plan->clips || !(max_norm >= 0.0)) return RAR_EINVAL;
   return hip_rc(launch_grad_clip(clip_set(plan), norm_type, scale, max_norm, norm, (hipStream_t)stream));
 }
 

@@ -288,3 +288,18 @@ def test_infinite_max_norm_only_scales(dt, n, kind):
     g[0] = math.nan
     plan.clip(math.inf, norm, kind)
     assert math.isnan(norm.item()) and bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("kind", [rar.NORM_L2, rar.NORM_MAX])
+def test_norm_of_tensors_that_overlap(kind):
+    """A norm writes no tensor, so one may be held twice or overlap another."""
+    flat = torch.randn(40_000, generator=_gen(1), device=DEV)
+    grads = [flat[:30_000], flat[:30_000], flat[10_000:], flat]
+    ws, norm = _bytes(rar.grad_clip_workspace_bytes([g.numel() for g in grads])), torch.zeros(1, device=DEV)
+    rar.grad_norm(grads, ws, norm, norm_type=kind, scale=0.5)
+    _check_norm(norm, _norm_of(grads, kind) * 0.5, "overlapping")
+    plan = rar.GradClip(grads, ws, norm_only=True)
+    with pytest.raises(rar.RarError):
+        plan.clip(1.0, norm)
+    with pytest.raises(rar.RarError):
+        rar.clip_grad_norm(grads, 1.0, ws, norm)

@@ -9,7 +9,7 @@ import ring_all_reduce_scatter_amd as rar
 from ring_all_reduce_scatter_amd import _binding as b
 from ring_all_reduce_scatter_amd import _operators as op
 
-OK, EOVERLAP = 0, 7
+OK, EINVAL, EDTYPE, EALIGN, EWORKSPACE, EOVERLAP = 0, 1, 2, 3, 4, 7
 B, G = 1 << 40, 1 << 30
 
 
@@ -49,3 +49,25 @@ def test_norm_among_the_tensors_is_refused_by_the_binding():
             clip._norm_address(bad)
     for good in (flat[32:33], flat[39:40], flat[41:42], torch.zeros(1)):
         assert clip._norm_address(good) == good.data_ptr()
+
+
+def test_set_prepared_for_its_norm_alone():
+    """Tensors that are read only may overlap, but for the workspace."""
+    L, p = rar.lib(), b.GradPlan()
+    counts = (ctypes.c_size_t * 2)(0, 3000)
+    dts = (ctypes.c_int * 2)(0, 0)
+    need = L.rar_grad_workspace_bytes(counts, 2)
+
+    def prepare(grads, n=2, ws=B + 2 * G, nbytes=need, dts=dts):
+        return L.rar_grad_prepare_norm((ctypes.c_void_p * 2)(*grads), counts, dts, n, ws, nbytes, ctypes.byref(p), None)
+
+    assert L.rar_grad_prepare_norm(None, None, None, 0, B, need, ctypes.byref(p), None) == OK and p.clips == 0
+    assert prepare([None, None], n=1) == OK and p.ntiles == 0
+    assert L.rar_grad_clip(ctypes.byref(p), 0, 1.0, 1.0, B + 5 * G, None) == EINVAL
+    assert prepare([None, B + 2 * G + 256]) == EOVERLAP and prepare([None, B + 2 * G - 4]) == EOVERLAP
+    assert prepare([None, None]) == EOVERLAP and prepare([None, B + 2]) == EALIGN
+    assert prepare([None, B], ws=None) == EWORKSPACE and prepare([None, B], nbytes=64) == EWORKSPACE
+    assert prepare([None, B], dts=(ctypes.c_int * 2)(0, 3)) == EDTYPE
+    assert L.rar_grad_prepare(None, None, None, None, None, 0, B, need, ctypes.byref(p), None) == OK and p.clips == 1
+    with pytest.raises(ValueError, match="norm alone"):
+        rar.GradClip([torch.zeros(4)], torch.zeros(1 << 16, dtype=torch.uint8), outs=[torch.zeros(4)], norm_only=True)
