@@ -25,14 +25,25 @@ bool dt_ok(int dt) { return dt == RAR_F32 || dt == RAR_F16 || dt == RAR_BF16; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int hip_rc(hipError_t e) { return e == hipSuccess ? RAR_OK : RAR_EHIP; }
 
-// A byte range; an output may coincide with inputs of the same `same` tag
-// (not 0), element for element.
+// A byte range, or (stride not 0) rows of `row` bytes every `stride` bytes in
+// it; an output may coincide with inputs of the same `same` tag (not 0),
+// element for element.
 struct Range {
   uintptr_t p;
   size_t bytes;
   bool written;
   int same;
+  size_t stride = 0, row = 0;
 };
+
+// Whether the rows of one range lie in the gaps between the other's: columns
+// of one matrix.
+bool in_gaps(const Range& a, const Range& b) {
+  if (a.stride == 0 || a.stride != b.stride) return false;
+  const size_t off = a.p < b.p ? (b.p - a.p) % a.stride : (a.p - b.p) % a.stride;
+  const size_t first = a.p < b.p ? a.row : b.row, second = a.p < b.p ? b.row : a.row;
+  return first <= off && second <= a.stride - off;
+}
 
 // Every written range apart from every other one, but for those of equal
 // tag, address and length.  The ranges are few: one call's tensors.
@@ -43,6 +54,7 @@ int check_ranges(const Range* a, int n) {
       if (a[i].bytes == 0 || a[j].bytes == 0) continue;
       if (a[i].p >= a[j].p + a[j].bytes || a[j].p >= a[i].p + a[i].bytes) continue;
       if (a[i].same && a[i].same == a[j].same && a[i].p == a[j].p && a[i].bytes == a[j].bytes) continue;
+      if (in_gaps(a[i], a[j])) continue;
       return RAR_EOVERLAP;
     }
   return RAR_OK;
@@ -269,7 +281,9 @@ int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_d
   if ((rc = check_ptr(weight, es_of(weight_dtype))) || (rc = check_ptr(ids, ib)) ||
       (rc = check_ptr(out, es_of(out_dtype))))
     return rc;
-  const Range r[] = {{(uintptr_t)out, ob, true, 0}, {(uintptr_t)weight, wb, false, 0},
+  const size_t oe = es_of(out_dtype), we = es_of(weight_dtype);
+  const Range r[] = {{(uintptr_t)out, ob, true, 0, out_stride * oe, dim * oe},
+                     {(uintptr_t)weight, wb, false, 0, weight_stride * we, dim * we},
                      {(uintptr_t)ids, ib * tokens, false, 0}};
   if ((rc = check_ranges(r, 3))) return rc;
   if (tokens * ((dim + 511) / 512) > 0xfffffff0ull) return RAR_ENOTSUP;  // numbered in 32 bits
@@ -300,8 +314,11 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   const size_t need = rar_embedding_workspace_bytes(tokens, vocab, dim);
   if (!workspace || ws_bytes < need) return RAR_EWORKSPACE;
   if ((uintptr_t)workspace & 15u) return RAR_EALIGN;
-  const Range r[] = {{(uintptr_t)dweight, wb, true, 0}, {(uintptr_t)workspace, need, true, 0},
-                     {(uintptr_t)dout, db, false, 0}, {(uintptr_t)ids, ib * tokens, false, 0}};
+  const size_t we = es_of(dweight_dtype), de = es_of(dout_dtype);
+  const Range r[] = {{(uintptr_t)dweight, wb, true, 0, dweight_stride * we, dim * we},
+                     {(uintptr_t)workspace, need, true, 0},
+                     {(uintptr_t)dout, db, false, 0, dout_stride * de, dim * de},
+                     {(uintptr_t)ids, ib * tokens, false, 0}};
   if ((rc = check_ranges(r, 4))) return rc;
   const EmbeddingLayout l = embedding_layout(tokens, vocab, dim);
   const size_t pieces = (tokens + embedding_piece(tokens, dim) - 1) / embedding_piece(tokens, dim);
@@ -341,8 +358,9 @@ int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, co
       (weight && (rc = check_ptr(weight, ws))) || (bias && (rc = check_ptr(bias, ws))) ||
       (mean && (rc = check_ptr(mean, 4))) || (rstd && (rc = check_ptr(rstd, 4))))
     return rc;
-  const Range r[] = {{(uintptr_t)y, yb, true, 1},
-                     {(uintptr_t)x, xb, false, x_stride == y_stride ? 1 : 0},
+  const size_t es = es_of(dtype);
+  const Range r[] = {{(uintptr_t)y, yb, true, 1, y_stride * es, dim * es},
+                     {(uintptr_t)x, xb, false, x_stride == y_stride ? 1 : 0, x_stride * es, dim * es},
                      {(uintptr_t)weight, weight ? dim * ws : 0, false, 0},
                      {(uintptr_t)bias, bias ? dim * ws : 0, false, 0},
                      {(uintptr_t)mean, mean ? rows * 4 : 0, true, 0},
@@ -379,9 +397,9 @@ int rar_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size
   const size_t need = sums ? rar_layernorm_workspace_bytes(rows, dim) : 0;
   if (sums && (!workspace || ws_bytes < need)) return RAR_EWORKSPACE;
   if (sums && ((uintptr_t)workspace & 15u)) return RAR_EALIGN;
-  const Range r[] = {{(uintptr_t)dx, db, true, 1},
-                     {(uintptr_t)dy, yb, false, dy_stride == dx_stride ? 1 : 0},
-                     {(uintptr_t)x, xb, false, x_stride == dx_stride ? 1 : 0},
+  const Range r[] = {{(uintptr_t)dx, db, true, 1, dx_stride * es, dim * es},
+                     {(uintptr_t)dy, yb, false, dy_stride == dx_stride ? 1 : 0, dy_stride * es, dim * es},
+                     {(uintptr_t)x, xb, false, x_stride == dx_stride ? 1 : 0, x_stride * es, dim * es},
                      {(uintptr_t)weight, weight ? dim * ws : 0, false, 0},
                      {(uintptr_t)mean, rows * 4, false, 0},
                      {(uintptr_t)rstd, rows * 4, false, 0},

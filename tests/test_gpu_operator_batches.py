@@ -303,3 +303,47 @@ def test_norm_of_tensors_that_overlap(kind):
         plan.clip(1.0, norm)
     with pytest.raises(rar.RarError):
         rar.clip_grad_norm(grads, 1.0, ws, norm)
+
+
+# ------------------------------------------------------------------ columns of one matrix
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim", [(5, 40), (700, 129), (1300, 1000), (70, 9000)])
+def test_layernorm_between_columns_of_one_matrix(rows, dim, dt):
+    """Inputs and outputs as columns of one buffer, in either order."""
+    t, gen = DTYPES[dt], _gen(dim)
+    w, b = torch.randn(dim, generator=gen, device=DEV), torch.randn(dim, generator=gen, device=DEV)
+    x, dy = _ints((rows, dim), t, gen), _ints((rows, dim), t, gen)
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    rar.layernorm_forward(x, w, b, y, mean=mean, rstd=rstd)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    ws = _bytes(rar.layernorm_workspace_bytes(rows, dim))
+    rar.layernorm_backward(dy, x, w, mean, rstd, dx, dw, db, ws)
+    for order in ((0, 1, 2, 3), (3, 2, 1, 0)):
+        m = torch.full((rows, 4 * dim + 1), 9.0, device=DEV, dtype=t)
+        xs, ys, dys, dxs = (m[:, i * dim:(i + 1) * dim] for i in order)
+        xs.copy_(x)
+        dys.copy_(dy)
+        rar.layernorm_forward(xs, w, b, ys)
+        dw2, db2 = torch.full_like(dw, 7.0), torch.full_like(db, 7.0)
+        rar.layernorm_backward(dys, xs, w, mean, rstd, dxs, dw2, db2, ws)
+        for name, got, want in (("x", xs, x), ("y", ys, y), ("dy", dys, dy), ("dx", dxs, dx), ("dw", dw2, dw),
+                                ("db", db2, db), ("gap", m[:, -1], torch.full_like(m[:, -1], 9.0))):
+            _same(got, want, name)
+
+
+@pytest.mark.parametrize("tokens,dim", [(300, 40), (2000, 700)])
+def test_embedding_between_columns_of_one_matrix(tokens, dim):
+    gen = _gen(dim)
+    ids = torch.randint(-1, tokens, (tokens,), generator=gen, device=DEV)
+    m = torch.full((tokens, 2 * dim + 3), 9.0, device=DEV)
+    a, c = m[:, :dim], m[:, dim + 1:2 * dim + 1]
+    a.copy_(_ints((tokens, dim), torch.float32, gen))
+    want = torch.where(ids[:, None] < 0, 0.0, a[ids.clamp(min=0)])
+    rar.embedding_forward(a, ids, c)  # the table beside its output
+    _same(c, want, "lookup")
+    grad = torch.zeros(tokens, dim, device=DEV).index_add_(0, ids.clamp(min=0), torch.where(ids[:, None] < 0, 0.0, c))
+    ws = _bytes(rar.embedding_workspace_bytes(tokens, tokens, dim))
+    rar.embedding_backward(c, ids, a, ws)
+    _same(a, grad, "gradient")
+    assert bool((m[:, dim] == 9.0).all()) and bool((m[:, 2 * dim + 1:] == 9.0).all())

@@ -71,3 +71,19 @@ def test_set_prepared_for_its_norm_alone():
     assert L.rar_grad_prepare(None, None, None, None, None, 0, B, need, ctypes.byref(p), None) == OK and p.clips == 1
     with pytest.raises(ValueError, match="norm alone"):
         rar.GradClip([torch.zeros(4)], torch.zeros(1 << 16, dtype=torch.uint8), outs=[torch.zeros(4)], norm_only=True)
+
+
+def _ln(x, y, rows=10, dim=64, xs=200, ys=200, dt=2):
+    return rar.lib().rar_layernorm_forward(x, xs, None, None, rows, dim, dt, 0, 1e-5, y, ys, None, None, None)
+
+
+def test_rows_that_share_bytes_are_refused():
+    """Columns of one matrix are apart only where neither reaches the other's
+    columns, in its own row or the next."""
+    e = 2
+    for off in (1, 63, 137, 199, 200 + 63, 5 * 200 + 137):
+        assert _ln(B, B + off * e) == EOVERLAP, off
+        assert _ln(B + off * e, B) == EOVERLAP, -off
+    assert _ln(B, B + 64 * e, xs=199) == EOVERLAP
+    assert _ln(B, B + 100 * e, xs=100) == EOVERLAP  # every second row of x is a row of y's
+    assert _ln(B, B + 64 * e, xs=32) == EOVERLAP  # x's rows overlap
