@@ -168,6 +168,16 @@ def _touches(begins, ends, a: int, nbytes: int) -> bool:
     return i >= 0 and ends[i] > a
 
 
+def _same_order(o, g) -> bool:
+    """Element k of o's memory is element k of g's, both dense: equal shapes,
+    and equal steps wherever a dimension has a second element."""
+    if o.shape != g.shape:
+        return False
+    if o.stride() == g.stride() or (o.is_contiguous() and g.is_contiguous()):
+        return True
+    return all(a == b for a, b, n in zip(o.stride(), g.stride(), g.shape) if n != 1)
+
+
 class GradClip:
     """Global norm and clipping of fixed gradient tensors, prepared once.
 
@@ -193,7 +203,7 @@ class GradClip:
             if len(outs) != len(grads):
                 raise ValueError("need one output per gradient")
             for g, o in zip(grads, outs):
-                if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+                if not _same_order(o, g):
                     raise ValueError("an output must have its gradient's shape and strides")
         if workspace is None:
             raise ValueError("a workspace is needed")

@@ -87,3 +87,17 @@ def test_rows_that_share_bytes_are_refused():
     assert _ln(B, B + 64 * e, xs=199) == EOVERLAP
     assert _ln(B, B + 100 * e, xs=100) == EOVERLAP  # every second row of x is a row of y's
     assert _ln(B, B + 64 * e, xs=32) == EOVERLAP  # x's rows overlap
+
+
+def test_dimensions_of_one_element_have_no_step():
+    """An output in its gradient's order, whatever the strides of dimensions
+    of one element say."""
+    ws = torch.zeros(rar.grad_clip_workspace_bytes([32]), dtype=torch.uint8)
+    g = torch.zeros(8, 4).t()[None]
+    o = torch.zeros(1, 8, 4).as_strided((1, 4, 8), (1, 1, 4))
+    assert g.stride() != o.stride() and not g.is_contiguous() and not o.is_contiguous()
+    with pytest.raises(ValueError, match="GPU tensor"):  # only the host check is left
+        rar.GradClip([g], ws, outs=[o])
+    for bad in (torch.zeros(1, 4, 8), torch.zeros(4, 8), torch.zeros(4, 1, 8).transpose(0, 1)):
+        with pytest.raises(ValueError, match="shape and strides"):
+            rar.GradClip([g], ws, outs=[bad])
