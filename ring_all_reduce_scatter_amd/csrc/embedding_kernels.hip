@@ -350,7 +350,7 @@ struct Pieces {
   uint32_t n;       // pieces
   uint32_t segs;    // column segments of kSeg
   uint64_t dim;
-  uint32_t zrows;   // rows that one wavefront looks through for empty ones (at most 64)
+  uint32_t zrows;   // rows that one wavefront looks through for empty ones (at most 16)
   float* partials;  // [n][2][segs * kSeg]: head, tail
   uint32_t* counts; // [2][n][segs]: arrived parts of the group, groups of the run, that begin in a piece
 };

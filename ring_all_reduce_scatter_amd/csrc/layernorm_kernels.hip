@@ -627,7 +627,7 @@ hipError_t layernorm_grad_dt(const LayernormGrad& a, uint64_t rows, uint64_t dim
   hipError_t e = hipSuccess;
   // dw and db first: dx may be written over dy or x
   if (a.dweight || a.dbias) {
-    const uint64_t splits = std::min(layernorm_splits(rows, dim), (rows + 63) / 64);
+    const uint64_t splits = std::min(layernorm_splits(rows), (rows + 63) / 64);
     hipLaunchKernelGGL((layernorm_dw_part_kernel<DT>), dim3((unsigned)((dim + kThreads - 1) / kThreads), (unsigned)splits),
                        dim3(kThreads), 0, stream, a, rows, dim, (rows + splits - 1) / splits);
     if ((e = launch_status(stream)) != hipSuccess) return e;
@@ -653,8 +653,7 @@ hipError_t launch_layernorm(const Rows& x, const void* weight, const void* bias,
   }
 }
 
-uint64_t layernorm_splits(uint64_t rows, uint64_t dim) {
-  (void)dim;
+uint64_t layernorm_splits(uint64_t rows) {
   return std::max<uint64_t>(1, std::min<uint64_t>(kGradGroups, rows));
 }
 

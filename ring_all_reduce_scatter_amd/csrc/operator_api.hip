@@ -372,7 +372,7 @@ int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, co
 
 size_t rar_layernorm_workspace_bytes(size_t rows, size_t dim) {
   if (dim == 0 || dim > kMaxDim) return 0;
-  return round_up(layernorm_splits(rows, dim) * 2 * dim * sizeof(float), kAlign);
+  return round_up(layernorm_splits(rows) * 2 * dim * sizeof(float), kAlign);
 }
 
 int rar_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size_t x_stride, const void* weight,

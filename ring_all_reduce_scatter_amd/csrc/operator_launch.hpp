@@ -79,7 +79,7 @@ hipError_t launch_layernorm(const Rows& x, const void* weight, const void* bias,
                             float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream);
 // Row groups whose sums of the weight's and bias's gradients are kept apart
 // in the workspace (2 * splits * dim floats) before they are added.
-uint64_t layernorm_splits(uint64_t rows, uint64_t dim);
+uint64_t layernorm_splits(uint64_t rows);
 struct LayernormGrad {
   Rows dy, x, dx;
   const void* weight;

@@ -115,21 +115,6 @@ __device__ __forceinline__ VecF<E> load_vec_upto(const char* base, uint64_t elem
   return f;
 }
 template <int DT, int E>
-__device__ __forceinline__ VecRaw<DT, E> load_raw_upto(const char* base, uint64_t elem, int n) {
-  if (n >= E) return load_raw<DT, E>(base, elem);
-  VecRaw<DT, E> r;
-#pragma unroll
-  for (int i = 0; i < VecRaw<DT, E>::W; ++i) {
-    if constexpr (DT == DT_F32) {
-      r.w[i] = i < n ? ((const uint32_t*)base)[elem + i] : 0u;
-    } else {
-      const uint16_t* p = (const uint16_t*)base + elem;
-      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-    }
-  }
-  return r;
-}
-template <int DT, int E>
 __device__ __forceinline__ void store_vec_upto(char* base, uint64_t elem, int n, const VecF<E>& f) {
   if (n >= E) {
     store_vec<DT, E>(base, elem, f);
