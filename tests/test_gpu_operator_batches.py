@@ -53,7 +53,8 @@ def _ids(kind, tokens, vocab, gen):
 
 BATCHES = [(1025, 3, 513, "one"), (1500, 700, 1001, "two"), (3001, 900, 2048, "skew"), (5000, 40, 520, "one"),
            (20_000, 5000, 1536, "skew"), (70_000, 3, 600, "one"), (70_000, 3, 24, "two"), (400_000, 3000, 24, "skew"),
-           (32_768, 50_021, 2048, "skew"), (2000, 300, 4100, "two")]
+           (32_768, 50_021, 2048, "skew"), (2000, 300, 4100, "two"),
+          (3, 2, 512 * 65_535 + 3, "two")]  # more segments than a grid dimension of the few-token launch
 
 
 @pytest.mark.parametrize("dts", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
@@ -67,8 +68,9 @@ def test_sorted_gradient_is_exact_in_every_segment(tokens, vocab, dim, kind, dts
     pad = int(ids[0]) if kind == "skew" else None
     ok = (ids >= 0) if pad is None else (ids >= 0) & (ids != pad)
     want = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV)
-    for c in range(0, dim, 1024):
-        want[:, c:c + 1024].index_add_(0, ids[ok], dout[ok, c:c + 1024].double())
+    step = max(1024, (1 << 26) // tokens)  # columns in binary64 at a time
+    for c in range(0, dim, step):
+        want[:, c:c + step].index_add_(0, ids[ok], dout[ok, c:c + step].double())
     assert float(want.abs().max()) < 2.0 ** 22  # a sum is exact in binary32, whatever its order
     ws = _bytes(rar.embedding_workspace_bytes(tokens, vocab, dim))
     ws.fill_(0x5A)
