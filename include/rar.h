@@ -504,10 +504,10 @@ int rar_bucketed_launch(const rar_bucketed_plan* plan, void* stream);
 /* are sums over a batch's tokens, the rings sum them over the ranks, and  */
 /* the global norm is taken over the reduced tensors.                      */
 /* Device pointers of these calls need only their element's alignment      */
-/* (workspaces: 16 bytes); rows may lie any number of elements apart, so    */
+/* (workspaces: 16 bytes); rows may lie any number of elements apart, so   */
 /* views of flat buffers and rows of odd length are served as they are;    */
-/* rows of equal stride may lie between one another (columns of one         */
-/* matrix), any other overlap of an output is refused (RAR_EOVERLAP).       */
+/* rows of equal stride may lie between one another (columns of one        */
+/* matrix), any other overlap of an output is refused (RAR_EOVERLAP).      */
 /* Sums are held in binary32 or more and formed in a fixed order: equal    */
 /* inputs give equal bits.  Host memory that runs out in a call's checks   */
 /* is reported as RAR_EHIP.                                                */

@@ -12,9 +12,10 @@
 // All of it is bound by memory for batches and by latency for a few tokens.
 // Times on one MI355X, inputs cold: lookup of 16,383 rows of 4096 bf16 29.7
 // us (6.2 TB/s of its 185 MB); gradient of 32,768 x 2048 bf16 tokens into
-// 50,021 f32 rows 125 us: sort 13, sums and zero rows 95 (5.8 TB/s of 549
-// MB), and the launch between; 509 x 512 f32 tokens into 8192 rows 8.6 us,
-// one launch of 8.
+// 50,021 f32 rows 125 us: sort 13, sums and zero rows 113 (4.9 TB/s of 549
+// MB; 95 where the memory-side cache holds the inputs), the second launch
+// following the first without a gap; 509 x 512 f32 tokens into 8192 rows 8.6
+// us, one launch of 9.4 with cold inputs in a kernel trace (8.2 warm).
 #include <algorithm>
 
 #include "operator_launch.hpp"
@@ -545,7 +546,7 @@ __global__ __launch_bounds__(kThreads) void embedding_grad_kernel(Rows dout, uin
 // sorts the others in LDS by counting for each how many come before it (an
 // entry is row << 10 | token, so they are ordered as numbers), and adds them
 // in W pieces as above, with the partial sums in LDS.  Against three launches
-// (sort, sums, cut runs): 7.4 us instead of 16.5 for 509 x 512 f32 tokens
+// (sort, sums, cut runs): 8.6 us instead of 16.5 for 509 x 512 f32 tokens
 // into 8192 rows.  Four wavefronts are enough for 256 tokens, and more of
 // these workgroups fit a CU: 100 x 512 f32 tokens into 32,768 rows take 12.9
 // us so, 14.1 with sixteen.

@@ -20,7 +20,9 @@
 // Measured and left out: a contiguous range of rows per workgroup instead of
 // every n-th (forward 55 us, backward 151), ordinary loads instead of
 // streaming ones (50 and 153), 16 wavefronts of half the columns backward
-// (156).
+// (156).  The loops for longer rows are far from that: forward 2048 x 32,768
+// bf16 218 us (42 at the copy rate), backward 366 (63), backward 4096 x 12,288
+// f32 295 (95).
 #include <algorithm>
 
 #include "operator_launch.hpp"
