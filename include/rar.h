@@ -520,6 +520,16 @@ typedef enum rar_id_type { RAR_I32 = 0, RAR_I64 = 1 } rar_id_type;
  * value. */
 typedef enum rar_norm_type { RAR_NORM_L2 = 0, RAR_NORM_MAX = 1 } rar_norm_type;
 
+/* The host arrays of a set's preparation, as rar_grad_prepare takes them. */
+typedef struct {
+  void* const* grads;
+  void* const* outs;
+  const size_t* counts;
+  const int* dtypes;
+  const int* out_dtypes;
+  size_t ntensors;
+} rar_grad_set;
+
 /* A set of gradient tensors prepared once and measured or clipped many
  * times.  Plain data owned by the caller; filled by rar_grad_prepare or
  * rar_grad_prepare_norm. */
@@ -530,6 +540,8 @@ typedef struct {
   uint64_t result_offset;   /* ... to the counts of arrived workgroups and the last factor */
   uint64_t ntiles;
   uint64_t clips;           /* 0: prepared for its norm alone */
+  const rar_grad_set* set;  /* NULL from the preparation; a caller that keeps the arrays may point
+                               here to them, for the calls to compare their norm with */
 } rar_grad_plan;
 
 /* Workspace for rar_grad_prepare; 0 on bad args.  A set may hold up to
@@ -561,8 +573,8 @@ int rar_grad_prepare_norm(void* const* grads, const size_t* counts, const int* d
  * their mean.  An L2 norm is summed in binary64, so no finite gradient
  * overflows or vanishes in it.  A NaN anywhere gives NaN, else an infinity
  * gives infinity (NaN where scale is 0).  norm must lie apart from the
- * workspace (RAR_EOVERLAP) and from the set's tensors, which only the caller
- * can check. */
+ * workspace and from the set's tensors: RAR_EOVERLAP in the workspace and,
+ * where plan->set is given, among the tensors. */
 int rar_grad_norm(const rar_grad_plan* plan, int norm_type, double scale, float* norm, void* stream);
 
 /* The same norm, then every output <- round(gradient * f) with

@@ -51,11 +51,17 @@ class BucketedPlan(ctypes.Structure):
                 ("sent", ctypes.c_uint64 * 64), ("recv", ctypes.c_uint64 * 64)]
 
 
+class GradSet(ctypes.Structure):
+    """Mirror of rar_grad_set: host arrays of a set's preparation."""
+    _fields_ = [("grads", ctypes.c_void_p), ("outs", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("dtypes", ctypes.c_void_p), ("out_dtypes", ctypes.c_void_p), ("ntensors", ctypes.c_size_t)]
+
+
 class GradPlan(ctypes.Structure):
     """Mirror of rar_grad_plan: a prepared set of gradient tensors."""
     _fields_ = [("workspace", ctypes.c_void_p), ("desc_offset", ctypes.c_uint64),
                 ("partial_offset", ctypes.c_uint64), ("result_offset", ctypes.c_uint64),
-                ("ntiles", ctypes.c_uint64), ("clips", ctypes.c_uint64)]
+                ("ntiles", ctypes.c_uint64), ("clips", ctypes.c_uint64), ("set", ctypes.POINTER(GradSet))]
 
 
 class CompressCfg(ctypes.Structure):

@@ -105,9 +105,25 @@ ClipSet clip_set(const rar_grad_plan* p) {
   return ClipSet{ws + p->desc_offset, ws + p->partial_offset, result, result + kClipCountBytes, p->ntiles};
 }
 
-// The norm is written while the workspace is read, so it has to lie apart
-// from it; that it lies apart from the tensors the caller has to see to
-// (their addresses are in the workspace, which the host does not read).
+// Whether norm lies among the tensors of a set.
+bool in_set(const rar_grad_set& s, const float* norm) {
+  const uintptr_t a = (uintptr_t)norm;
+  auto meets = [a](const void* p, size_t bytes) {
+    return a < (uintptr_t)p + bytes && (uintptr_t)p < a + sizeof(float);
+  };
+  for (size_t t = 0; t < s.ntensors; ++t) {
+    if (s.counts[t] == 0) continue;
+    if (meets(s.grads[t], s.counts[t] * es_of(s.dtypes[t])) ||
+        (s.outs && meets(s.outs[t], s.counts[t] * es_of(s.out_dtypes[t]))))
+      return true;
+  }
+  return false;
+}
+
+// The norm is written while the workspace is read and before a clip reads the
+// tensors, so it has to lie apart from them.  (The plan holds the tensors'
+// addresses in the workspace, which the host does not read: they are compared
+// where the caller keeps them.)
 int check_plan(const rar_grad_plan* p, int norm_type, double scale, const float* norm) {
   if (!p || !p->workspace || ((uintptr_t)p->workspace & 15u) || p->ntiles > kMaxTiles) return RAR_EINVAL;
   if (p->desc_offset == 0 || (p->desc_offset | p->partial_offset | p->result_offset) & 15u) return RAR_EINVAL;
@@ -117,7 +133,8 @@ int check_plan(const rar_grad_plan* p, int norm_type, double scale, const float*
   if (rc) return rc;
   const Range r[] = {{(uintptr_t)norm, sizeof(float), true, 0},
                      {(uintptr_t)p->workspace, p->result_offset + kClipCountBytes + kAlign, true, 0}};
-  return check_ranges(r, 2);
+  if (check_ranges(r, 2)) return RAR_EOVERLAP;
+  return p->set && in_set(*p->set, norm) ? RAR_EOVERLAP : RAR_OK;
 }
 
 // clips: the set is written, to outs or (NULL) in place; without, its tensors

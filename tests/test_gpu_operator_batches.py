@@ -349,3 +349,16 @@ def test_embedding_between_columns_of_one_matrix(tokens, dim):
     rar.embedding_backward(c, ids, a, ws)
     _same(a, grad, "gradient")
     assert bool((m[:, dim] == 9.0).all()) and bool((m[:, 2 * dim + 1:] == 9.0).all())
+
+
+def test_norm_among_the_tensors_is_refused():
+    flat, out = torch.ones(64, device=DEV), torch.zeros(32, dtype=torch.float16, device=DEV)
+    grads = [flat[:32], torch.empty(0, device=DEV)]
+    plan = rar.GradClip(grads, _bytes(rar.grad_clip_workspace_bytes([32, 0])), outs=[out, torch.empty(0, device=DEV)])
+    for bad in (flat[:1], flat[31:32], out[:2].view(torch.float32), out[30:].view(torch.float32)):
+        for call in (lambda: plan.norm(bad), lambda: plan.clip(1.0, bad)):
+            with pytest.raises(rar.RarError, match="overlap"):
+                call()
+    plan.norm(flat[32:33])
+    _check_norm(flat[32:33], 32 ** 0.5, "beside the tensors")
+    assert bool((flat[:32] == 1).all()) and bool((out == 0).all())

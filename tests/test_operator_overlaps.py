@@ -7,7 +7,6 @@ import torch
 
 import ring_all_reduce_scatter_amd as rar
 from ring_all_reduce_scatter_amd import _binding as b
-from ring_all_reduce_scatter_amd import _operators as op
 
 OK, EINVAL, EDTYPE, EALIGN, EWORKSPACE, EOVERLAP = 0, 1, 2, 3, 4, 7
 B, G = 1 << 40, 1 << 30
@@ -30,25 +29,34 @@ def test_norm_in_the_workspace_is_refused():
         assert L.rar_grad_clip(ctypes.byref(p), 1, 1.0, 1.0, at, None) == EOVERLAP, hex(at)
 
 
-def test_merged_ranges():
-    begins, ends = op._merged([(100, 200), (300, 304), (150, 260), (200, 210), (260, 264)])
-    assert list(zip(begins, ends)) == [(100, 260), (260, 264), (300, 304)]
-    for a, n, hit in ((96, 4, False), (97, 4, True), (256, 4, True), (260, 4, True), (264, 4, False), (296, 4, False),
-                      (297, 4, True), (300, 4, True), (304, 4, False), (0, 4, False), (0, 1000, True)):
-        assert op._touches(begins, ends, a, n) == hit, (a, n)
-    assert not op._touches([], [], 5, 4)
+def test_norm_among_the_tensors_is_refused():
+    """Where the plan points to the set's host arrays."""
+    L = rar.lib()
+    p, _ = _empty_plan()
+    assert not p.set
+    grads, outs = (ctypes.c_void_p * 3)(B + G, B + G + 256, None), (ctypes.c_void_p * 3)(B + G + 512, B + G, None)
+    counts = (ctypes.c_size_t * 3)(32, 1, 0)
+    f16, f32 = (ctypes.c_int * 3)(1, 1, 1), (ctypes.c_int * 3)(0, 0, 0)
 
+    def refused(offset, outs=None, odts=None, dts=f32):
+        s = b.GradSet(*(None if a is None else ctypes.addressof(a) for a in (grads, outs, counts, dts, odts)), 3)
+        p.set = ctypes.pointer(s)
+        # the limit is refused afterwards, so that nothing is launched
+        rc = L.rar_grad_clip(ctypes.byref(p), 0, 1.0, -1.0, B + G + offset, None)
+        assert rc in (EINVAL, EOVERLAP)
+        return rc == EOVERLAP
 
-def test_norm_among_the_tensors_is_refused_by_the_binding():
-    clip = op.GradClip.__new__(op.GradClip)  # without a device there is no plan to prepare
-    flat, outs = torch.zeros(64), torch.zeros(32, dtype=torch.float16)
-    clip._keep = ([flat[:32], flat[40:41], torch.empty(0)], [outs[:16], outs[20:21]], None)
-    clip._ranges = None
-    for bad in (flat[:1], flat[31:32], flat[40:41], outs[14:16].view(torch.float32), outs[20:22].view(torch.float32)):
-        with pytest.raises(ValueError, match="apart from"):
-            clip._norm_address(bad)
-    for good in (flat[32:33], flat[39:40], flat[41:42], torch.zeros(1)):
-        assert clip._norm_address(good) == good.data_ptr()
+    for dts, es in ((f32, 4), (f16, 2)):
+        for bad in (0, 32 * es - 4, 256):
+            assert refused(bad, dts=dts), bad
+        for good in (-4, 32 * es, 252, 260, 512):
+            assert not refused(good, dts=dts), good
+    assert refused(512, outs, f16) and refused(512 + 60, outs, f16) and not refused(512 + 64, outs, f16)
+    assert refused(512 + 64, outs, f32)
+    grads[0] = B + G + 2  # an element inside, the other beside the four bytes
+    counts[0] = 1
+    assert refused(0, dts=f16) and not refused(4, dts=f16)
+    assert L.rar_grad_norm(ctypes.byref(p), 0, 1.0, B + G, None) == EOVERLAP
 
 
 def test_set_prepared_for_its_norm_alone():
