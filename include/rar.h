@@ -586,7 +586,9 @@ int rar_grad_clip(const rar_grad_plan* plan, int norm_type, double scale, double
 
 /* out[t] <- round(scale * weight[ids[t]]) for t < tokens: rows of dim
  * elements, weight rows weight_stride and out rows out_stride elements
- * apart.  An id outside [0, vocab) gives a row of zeros. */
+ * apart.  An id outside [0, vocab) gives a row of zeros.  RAR_ENOTSUP beyond
+ * 2^30 tokens, 2^31 - 1 rows or columns, or 2^32 - 16 pieces of 512 columns
+ * of out. */
 int rar_embedding_forward(const void* weight, size_t weight_stride, int weight_dtype, size_t vocab,
                           size_t dim, const void* ids, int id_type, size_t tokens, float scale,
                           void* out, size_t out_stride, int out_dtype, void* stream);
@@ -611,7 +613,8 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
  * elements: mu the row's mean, r = 1 / sqrt(mean((x - mu)^2) + eps).  weight
  * and bias (dim elements of weight_dtype each) may be NULL (1 and 0).
  * mean and rstd (rows binary32 each, NULL if not wanted) receive mu and r.
- * y may be x with the same stride; x_stride may be 0. */
+ * y may be x with the same stride; x_stride may be 0.  RAR_ENOTSUP beyond
+ * 2^31 - 1 columns, backward too. */
 int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, const void* bias,
                           size_t rows, size_t dim, int dtype, int weight_dtype, float eps, void* y,
                           size_t y_stride, float* mean, float* rstd, void* stream);
