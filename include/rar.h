@@ -500,9 +500,10 @@ int rar_bucketed_launch(const rar_bucketed_plan* plan, void* stream);
 
 /* ---------------------------------------------------------------------- */
 /* Operators next to the rings: the reductions that make and finish the    */
-/* gradients of a data-parallel step.  Embedding and layer-norm gradients  */
-/* are sums over a batch's tokens, the rings sum them over the ranks, and  */
-/* the global norm is taken over the reduced tensors.                      */
+/* gradients of a data-parallel step.  Embedding, layer-norm and           */
+/* feed-forward gradients are sums over a batch's tokens, the rings sum    */
+/* them over the ranks, and the global norm is taken over the reduced      */
+/* tensors.                                                                */
 /* Device pointers of these calls need only their element's alignment      */
 /* (workspaces: 16 bytes); rows may lie any number of elements apart, so   */
 /* views of flat buffers and rows of odd length are served as they are;    */
@@ -635,6 +636,88 @@ int rar_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size
                            size_t dim, int dtype, int weight_dtype, void* dx, size_t dx_stride,
                            void* dweight, void* dbias, int accumulate, void* workspace,
                            size_t ws_bytes, void* stream);
+
+/* Activation checkpoints: a matrix of rows x dim held in 8 bits an element
+ * between a forward and a backward pass, as block floating point over blocks
+ * of 32 columns of a row.  With E the largest biased binary32 exponent of the
+ * block's values and e = max(E, 1) - 127, a value x becomes
+ * q = clamp(rne(x * 2^(6-e)), -127, 127) and stands for q * 2^(e-6); a block
+ * that holds an infinity or NaN stands for NaN throughout.  Both products are
+ * exact, so a checkpoint's bytes and values do not depend on the call that
+ * wrote it.  The buffer holds rows * 32 nb code bytes (nb = ceil(dim / 32),
+ * zeros past dim), then rows * nb exponent bytes E; it must be 16-byte
+ * aligned.
+ * rar_checkpoint_bytes is 0 for no rows and on bad args.  checkpoint_bytes:
+ * what the buffer holds (RAR_EWORKSPACE if too little).  x_stride may be 0.
+ * RAR_ENOTSUP beyond 2^31 - 1 columns. */
+size_t rar_checkpoint_bytes(size_t rows, size_t dim);
+int rar_checkpoint_pack(const void* x, size_t x_stride, size_t rows, size_t dim, int dtype,
+                        void* checkpoint, size_t checkpoint_bytes, void* stream);
+/* out <- the values a checkpoint stands for, rounded to out_dtype. */
+int rar_checkpoint_unpack(const void* checkpoint, size_t checkpoint_bytes, size_t rows, size_t dim,
+                          void* out, size_t out_stride, int out_dtype, void* stream);
+
+/* rar_layernorm_forward that also writes x's checkpoint, from the same
+ * reading of x (y may still be x). */
+int rar_layernorm_forward_checkpoint(const void* x, size_t x_stride, const void* weight,
+                                     const void* bias, size_t rows, size_t dim, int dtype,
+                                     int weight_dtype, float eps, void* y, size_t y_stride,
+                                     float* mean, float* rstd, void* checkpoint,
+                                     size_t checkpoint_bytes, void* stream);
+
+/* rar_layernorm_backward with the values of x's checkpoint in x's place; dtype
+ * is that of dy and dx, the workspace rar_layernorm_workspace_bytes. */
+int rar_layernorm_backward_checkpoint(const void* dy, size_t dy_stride, const void* checkpoint,
+                                      size_t checkpoint_bytes, const void* weight,
+                                      const float* mean, const float* rstd, size_t rows, size_t dim,
+                                      int dtype, int weight_dtype, void* dx, size_t dx_stride,
+                                      void* dweight, void* dbias, int accumulate, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* Activations of the gated feed-forward block: g / (1 + exp(-g)),
+ * g (1 + erf(g / sqrt 2)) / 2, and the latter's form with
+ * tanh(sqrt(2 / pi) (g + 0.044715 g^3)) in erf's place. */
+typedef enum rar_act { RAR_ACT_SILU = 0, RAR_ACT_GELU = 1, RAR_ACT_GELU_TANH = 2 } rar_act;
+
+/* What a forward pass keeps of its projections g and u for the backward pass:
+ * nothing, rows of the activations' type, or checkpoints. */
+typedef enum rar_keep { RAR_KEEP_NONE = 0, RAR_KEEP_ROWS = 1, RAR_KEEP_CHECKPOINT = 2 } rar_keep;
+
+/* Gated feed-forward block.  x: rows x dim, wgate and wup: hidden x dim (rows
+ * *_stride elements apart, one matrix of 2 * hidden rows may hold both), all
+ * of `dtype`:
+ *   g = x wgate^T,  u = x wup^T,  h <- round(act(g) * u)
+ * with sums, activation and product in binary32.  keep: gate and up receive g
+ * and u, rounded to rows of hidden elements *_stride apart, or as checkpoints
+ * of rows x hidden, where *_stride is the buffer's bytes.  x_stride and the
+ * weights' strides may be 0.  RAR_ENOTSUP beyond 2^26 columns of dim or
+ * hidden, 2^30 rows, or 2^22 tiles of 128 x 64 of any matrix of the call. */
+int rar_gated_ff_forward(const void* x, size_t x_stride, const void* wgate, size_t wgate_stride,
+                         const void* wup, size_t wup_stride, size_t rows, size_t dim, size_t hidden,
+                         int dtype, int act, void* h, size_t h_stride, int keep, void* gate,
+                         size_t gate_stride, void* up, size_t up_stride, void* stream);
+
+/* Workspace for rar_gated_ff_backward; 0 for no rows and on bad args. */
+size_t rar_gated_ff_workspace_bytes(size_t rows, size_t dim, size_t hidden, int dtype);
+
+/* From dh and the kept projections g and u (RAR_KEEP_ROWS or
+ * RAR_KEEP_CHECKPOINT, as the forward pass wrote them):
+ *   dg = round(dh * u * act'(g)),  du = round(dh * act(g))
+ *   dx     <- round(dg wgate + du wup)
+ *   dwgate <- round(dg^T x),  dwup <- round(du^T x),
+ * with accumulate added to what dwgate and dwup hold.  dg and du are rounded
+ * to dtype, as the matrix instructions take them; all sums are binary32.
+ * dweight_dtype: dtype or RAR_F32.  dx may be NULL, dwgate and dwup may both
+ * be NULL.  rows == 0 makes dwgate and dwup zero (untouched with accumulate).
+ * No output may overlap anything else.  dh_stride, x_stride and the strides of
+ * weights and kept rows may be 0. */
+int rar_gated_ff_backward(const void* dh, size_t dh_stride, const void* x, size_t x_stride,
+                          const void* wgate, size_t wgate_stride, const void* wup,
+                          size_t wup_stride, int keep, const void* gate, size_t gate_stride,
+                          const void* up, size_t up_stride, size_t rows, size_t dim, size_t hidden,
+                          int dtype, int act, void* dx, size_t dx_stride, void* dwgate,
+                          size_t dwgate_stride, void* dwup, size_t dwup_stride, int dweight_dtype,
+                          int accumulate, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------- */
 

@@ -17,6 +17,9 @@ from ._binding import (  # noqa: F401
     ring_allreduce_compressed_noalloc, NOALLOC_SCRATCH_BYTES,
 )
 from ._operators import (  # noqa: F401
-    NORM_L2, NORM_MAX, GradClip, clip_grad_norm, embedding_backward, embedding_forward, embedding_workspace_bytes,
-    grad_clip_workspace_bytes, grad_norm, layernorm_backward, layernorm_forward, layernorm_workspace_bytes,
+    ACT_GELU, ACT_GELU_TANH, ACT_SILU, KEEP_CHECKPOINT, KEEP_NONE, KEEP_ROWS, NORM_L2, NORM_MAX, GradClip,
+    checkpoint_bytes, checkpoint_pack, checkpoint_unpack, clip_grad_norm, embedding_backward, embedding_forward,
+    embedding_workspace_bytes, gated_ff_backward, gated_ff_forward, gated_ff_workspace_bytes,
+    grad_clip_workspace_bytes, grad_norm, layernorm_backward, layernorm_backward_checkpoint, layernorm_forward,
+    layernorm_forward_checkpoint, layernorm_workspace_bytes,
 )

@@ -148,6 +148,22 @@ _SIGS = {
     "rar_layernorm_backward": (_c_int, [_c_vp, _c_size, _c_vp, _c_size, _c_vp, _c_vp, _c_vp, _c_size, _c_size,
                                         _c_int, _c_int, _c_vp, _c_size, _c_vp, _c_vp, _c_int, _c_vp, _c_size,
                                         _c_vp]),
+    "rar_checkpoint_bytes": (_c_size, [_c_size, _c_size]),
+    "rar_checkpoint_pack": (_c_int, [_c_vp, _c_size, _c_size, _c_size, _c_int, _c_vp, _c_size, _c_vp]),
+    "rar_checkpoint_unpack": (_c_int, [_c_vp, _c_size, _c_size, _c_size, _c_vp, _c_size, _c_int, _c_vp]),
+    "rar_layernorm_forward_checkpoint": (_c_int, [_c_vp, _c_size, _c_vp, _c_vp, _c_size, _c_size, _c_int, _c_int,
+                                                  ctypes.c_float, _c_vp, _c_size, _c_vp, _c_vp, _c_vp, _c_size,
+                                                  _c_vp]),
+    "rar_layernorm_backward_checkpoint": (_c_int, [_c_vp, _c_size, _c_vp, _c_size, _c_vp, _c_vp, _c_vp, _c_size,
+                                                   _c_size, _c_int, _c_int, _c_vp, _c_size, _c_vp, _c_vp, _c_int,
+                                                   _c_vp, _c_size, _c_vp]),
+    "rar_gated_ff_forward": (_c_int, [_c_vp, _c_size, _c_vp, _c_size, _c_vp, _c_size, _c_size, _c_size, _c_size,
+                                      _c_int, _c_int, _c_vp, _c_size, _c_int, _c_vp, _c_size, _c_vp, _c_size, _c_vp]),
+    "rar_gated_ff_workspace_bytes": (_c_size, [_c_size, _c_size, _c_size, _c_int]),
+    "rar_gated_ff_backward": (_c_int, [_c_vp, _c_size, _c_vp, _c_size, _c_vp, _c_size, _c_vp, _c_size, _c_int, _c_vp,
+                                       _c_size, _c_vp, _c_size, _c_size, _c_size, _c_size, _c_int, _c_int, _c_vp,
+                                       _c_size, _c_vp, _c_size, _c_vp, _c_size, _c_int, _c_int, _c_vp, _c_size,
+                                       _c_vp]),
     "rar_status_string": (ctypes.c_char_p, [_c_int]),
     "rar_version": (ctypes.c_char_p, []),
 }

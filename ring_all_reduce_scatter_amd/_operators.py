@@ -1,6 +1,7 @@
 """Operators next to the rings: global gradient norm and clipping, embedding
-lookup and gradient, layer norm forward and backward (include/rar.h states
-their formulas).
+lookup and gradient, activation checkpoints in 8 bits, layer norm and the
+gated feed-forward block forward and backward (include/rar.h states their
+formulas).
 
 Argument marshalling only, as in _binding: the caller owns every tensor,
 outputs and workspaces included, and every step runs in the library's
@@ -22,6 +23,8 @@ from ._binding import F32, GradPlan, GradSet, RarError, _sizes, dtype_code, lib
 # as an address, and shapes are read once per tensor.
 
 NORM_L2, NORM_MAX = 0, 1
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
+KEEP_NONE, KEEP_ROWS, KEEP_CHECKPOINT = 0, 1, 2
 _I32, _I64 = 0, 1
 
 
@@ -287,6 +290,53 @@ def embedding_backward(dout, ids, dweight, workspace, scale: float = 1.0, paddin
     _check(rc, "rar_embedding_backward")
 
 
+# ------------------------------------------------------------------ activation checkpoints
+
+def checkpoint_bytes(rows: int, dim: int) -> int:
+    """Bytes of a checkpoint of rows x dim: 33 for every 32 columns begun of a row."""
+    return lib().rar_checkpoint_bytes(rows, dim)
+
+
+def _checkpoint(t, rows: int, dim: int, what: str = "checkpoint"):
+    """(address, bytes) of a checkpoint's buffer."""
+    if t.element_size() != 1 or t.is_floating_point() or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous bytes (uint8)")
+    n, need = t.numel(), rows * 33 * ((dim + 31) // 32)
+    if n < need:
+        raise ValueError(f"{what} holds {n} bytes, {need} are needed")
+    return t.data_ptr(), n
+
+
+def checkpoint_pack(x, checkpoint, stream=None):
+    """checkpoint (checkpoint_bytes(rows, dim) bytes or more) <- x (..., dim)
+    in 8 bits: blocks of 32 columns of a row share a power-of-two step, 1/64
+    to 1/128 of the block's largest value.  A block with an infinity or NaN
+    comes back as NaN."""
+    dim = _width(x, "x")
+    rows, stride = _rows(x, dim, "x")
+    ck, nbytes = _checkpoint(checkpoint, rows, dim)
+    code = dtype_code(x)
+    _on_gpu(x, checkpoint)
+    rc = (_binding._lib or lib()).rar_checkpoint_pack(x.data_ptr(), stride, rows, dim, code, ck, nbytes,
+                                                      _stream(stream, x))
+    _check(rc, "rar_checkpoint_pack")
+
+
+def checkpoint_unpack(checkpoint, out, stream=None):
+    """out (..., dim), of any of the three types, <- the values that a
+    checkpoint of its shape stands for."""
+    dim = _width(out, "out")
+    rows, stride = _rows(out, dim, "out")
+    if rows > 1 and stride < dim:
+        raise ValueError("out has rows that overlap")
+    ck, nbytes = _checkpoint(checkpoint, rows, dim)
+    code = dtype_code(out)
+    _on_gpu(checkpoint, out)
+    rc = (_binding._lib or lib()).rar_checkpoint_unpack(ck, nbytes, rows, dim, out.data_ptr(),
+                                                        stride if rows > 1 else dim, code, _stream(stream, out))
+    _check(rc, "rar_checkpoint_unpack")
+
+
 # ------------------------------------------------------------------ layer norm
 
 def _weight_type(default: int, *ts):
@@ -344,3 +394,142 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias, workspac
         dout.data_ptr(), dstride, x.data_ptr(), xstride, w, m, r, rows, dim, dt, wdt,
         None if dx is None else dx.data_ptr(), gstride, dw, db, int(accumulate), ws, nbytes, _stream(stream, x))
     _check(rc, "rar_layernorm_backward")
+
+
+def layernorm_forward_checkpoint(x, weight, bias, out, checkpoint, eps: float = 1e-5, mean=None, rstd=None,
+                                 stream=None):
+    """layernorm_forward that also writes x's checkpoint (checkpoint_pack's
+    bytes) from the same reading of x."""
+    dim = _width(x, "x")
+    rows, xstride = _rows(x, dim, "x")
+    ystride = _out_rows(out, dim, rows, "out")
+    if out.dtype != x.dtype:
+        raise ValueError("out must have x's type")
+    ck, nbytes = _checkpoint(checkpoint, rows, dim)
+    w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
+    m, r = _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd")
+    dt = dtype_code(x)
+    wdt = _weight_type(dt, weight, bias)
+    _on_gpu(x, weight, bias, out, checkpoint, mean, rstd)
+    rc = (_binding._lib or lib()).rar_layernorm_forward_checkpoint(
+        x.data_ptr(), xstride, w, b, rows, dim, dt, wdt, eps, out.data_ptr(), ystride, m, r, ck, nbytes,
+        _stream(stream, x))
+    _check(rc, "rar_layernorm_forward_checkpoint")
+
+
+def layernorm_backward_checkpoint(dout, checkpoint, weight, mean, rstd, dx, dweight, dbias, workspace,
+                                  accumulate: bool = False, stream=None):
+    """layernorm_backward with the values of x's checkpoint in x's place."""
+    dim = _width(dout, "dout")
+    rows, dstride = _rows(dout, dim, "dout")
+    if dx is not None and dx.dtype != dout.dtype:
+        raise ValueError("dx must have dout's type")
+    ck, cbytes = _checkpoint(checkpoint, rows, dim)
+    gstride = dim if dx is None else _out_rows(dx, dim, rows, "dx")
+    w, dw, db = _vector(weight, dim, "weight"), _vector(dweight, dim, "dweight"), _vector(dbias, dim, "dbias")
+    m, r = _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd")
+    dt = dtype_code(dout)
+    wdt = _weight_type(dt, weight, dweight, dbias)
+    ws, nbytes = _workspace(workspace)
+    _on_gpu(dout, checkpoint, weight, mean, rstd, dx, dweight, dbias, workspace)
+    rc = (_binding._lib or lib()).rar_layernorm_backward_checkpoint(
+        dout.data_ptr(), dstride, ck, cbytes, w, m, r, rows, dim, dt, wdt, None if dx is None else dx.data_ptr(),
+        gstride, dw, db, int(accumulate), ws, nbytes, _stream(stream, dout))
+    _check(rc, "rar_layernorm_backward_checkpoint")
+
+
+# ------------------------------------------------------------------ gated feed-forward
+
+def _ff_weights(x, wgate, wup):
+    """(dim, hidden, rows between wgate's, wup's rows)"""
+    dim = _width(x, "x")
+    if wgate.dim() != 2 or wgate.shape[0] == 0 or wup.shape != wgate.shape:
+        raise ValueError(f"wgate and wup must both be (hidden, {dim}), got shapes {tuple(wgate.shape)} and "
+                         f"{tuple(wup.shape)}")
+    if wgate.dtype != x.dtype or wup.dtype != x.dtype:
+        raise ValueError("wgate and wup must have x's type")
+    return dim, wgate.shape[0], _rows(wgate, dim, "wgate")[1], _rows(wup, dim, "wup")[1]
+
+
+def _ff_kept(gate, up, rows: int, hidden: int, dtype, written: bool):
+    """(keep, address and stride or bytes of gate, the same of up)"""
+    if gate is None and up is None:
+        return KEEP_NONE, None, 0, None, 0
+    if gate is None or up is None or gate.dtype != up.dtype:
+        raise ValueError("gate and up must be of one kind")
+    if gate.dtype != dtype:
+        return (KEEP_CHECKPOINT, *_checkpoint(gate, rows, hidden, "gate"), *_checkpoint(up, rows, hidden, "up"))
+    steps = []
+    for t, what in ((gate, "gate"), (up, "up")):
+        if written:
+            steps.append(_out_rows(t, hidden, rows, what))
+            continue
+        n, stride = _rows(t, hidden, what)
+        if n != rows:
+            raise ValueError(f"{what} has {n} rows, {rows} are needed")
+        steps.append(stride)
+    return KEEP_ROWS, gate.data_ptr(), steps[0], up.data_ptr(), steps[1]
+
+
+def gated_ff_forward(x, wgate, wup, out, act: int = ACT_SILU, gate=None, up=None, stream=None):
+    """out (..., hidden) <- act(x wgate^T) * (x wup^T) for x (..., dim) and
+    weights (hidden, dim) of its type; they may be the halves of one matrix.
+    gate and up receive the two projections for gated_ff_backward: tensors of
+    out's shape and type, or checkpoints in 8 bits (checkpoint_bytes(rows,
+    hidden) bytes each), written straight from the sums."""
+    dim, hidden, gstride, ustride = _ff_weights(x, wgate, wup)
+    rows, xstride = _rows(x, dim, "x")
+    ostride = _out_rows(out, hidden, rows, "out")
+    if out.dtype != x.dtype:
+        raise ValueError("out must have x's type")
+    keep, g, gs, u, us = _ff_kept(gate, up, rows, hidden, x.dtype, True)
+    dt = dtype_code(x)
+    _on_gpu(x, wgate, wup, out, gate, up)
+    rc = (_binding._lib or lib()).rar_gated_ff_forward(
+        x.data_ptr(), xstride, wgate.data_ptr(), gstride, wup.data_ptr(), ustride, rows, dim, hidden, dt, act,
+        out.data_ptr(), ostride, keep, g, gs, u, us, _stream(stream, x))
+    _check(rc, "rar_gated_ff_forward")
+
+
+def gated_ff_workspace_bytes(rows: int, dim: int, hidden: int, dtype) -> int:
+    """Workspace of gated_ff_backward for activations of this torch type."""
+    import torch
+    return lib().rar_gated_ff_workspace_bytes(rows, dim, hidden, dtype_code(torch.empty(0, dtype=dtype)))
+
+
+def gated_ff_backward(dout, x, wgate, wup, gate, up, dx, dwgate, dwup, workspace, act: int = ACT_SILU,
+                      accumulate: bool = False, stream=None):
+    """Gradients of gated_ff_forward from what it kept in gate and up.  dx (x's
+    shape and type) may be None, dwgate and dwup (the weights' shape, x's type
+    or float32) may both be None; with accumulate the weights' gradients are
+    added to what they hold."""
+    dim, hidden, gstride, ustride = _ff_weights(x, wgate, wup)
+    rows, xstride = _rows(x, dim, "x")
+    n, dstride = _rows(dout, hidden, "dout")
+    if n != rows:
+        raise ValueError(f"dout has {n} rows, x has {rows}")
+    if dout.dtype != x.dtype or (dx is not None and dx.dtype != x.dtype):
+        raise ValueError("dout and dx must have x's type")
+    keep, g, gs, u, us = _ff_kept(gate, up, rows, hidden, x.dtype, False)
+    if keep == KEEP_NONE:
+        raise ValueError("gate and up are needed")
+    if (dwgate is None) != (dwup is None) or (dwup is not None and dwup.dtype != dwgate.dtype):
+        raise ValueError("dwgate and dwup must be of one kind")
+    dt = dtype_code(x)
+    xs = dim if dx is None else _out_rows(dx, dim, rows, "dx")
+    wdt, dg, dgs, du, dus = dt, None, dim, None, dim
+    if dwgate is not None:
+        wdt = dtype_code(dwgate)
+        if wdt != dt and wdt != F32:
+            raise ValueError("dwgate and dwup must have x's type or be float32")
+        if dwgate.dim() != 2 or dwup.dim() != 2:
+            raise ValueError("dwgate and dwup must have the weights' shape")
+        dgs, dus = _out_rows(dwgate, dim, hidden, "dwgate"), _out_rows(dwup, dim, hidden, "dwup")
+        dg, du = dwgate.data_ptr(), dwup.data_ptr()
+    ws, nbytes = _workspace(workspace)
+    _on_gpu(dout, x, wgate, wup, gate, up, dx, dwgate, dwup, workspace)
+    rc = (_binding._lib or lib()).rar_gated_ff_backward(
+        dout.data_ptr(), dstride, x.data_ptr(), xstride, wgate.data_ptr(), gstride, wup.data_ptr(), ustride, keep, g,
+        gs, u, us, rows, dim, hidden, dt, act, None if dx is None else dx.data_ptr(), xs, dg, dgs, du, dus, wdt,
+        int(accumulate), ws, nbytes, _stream(stream, x))
+    _check(rc, "rar_gated_ff_backward")

@@ -1,0 +1,109 @@
+// Activation checkpoints in 8 bits: the library's block floating point
+// (bfp_scale, bfp_q in common.hpp) over the rows of a matrix, in blocks of 32
+// columns.
+//
+//   E = max |x| >> 23 as binary32 bits,  e = max(E, 1) - 127,  k = 6 - e
+//   q = clamp(rne(x 2^k), +-127),  value = q 2^-k;  E = 255: NaN, q = 0
+//
+// The scale is a power of two, so x 2^k and q 2^-k are exact and a checkpoint
+// holds the same bytes whichever kernel writes it.  Blocks are as short as
+// that because activations have single columns far above their neighbours,
+// which cost a block its bits; the exponents take 1/32 of the codes' bytes.
+//
+// Layout of rows x dim with nb = ceil(dim / 32) blocks a row: the codes, 32 nb
+// bytes a row (zeros past dim), then the exponents, nb bytes a row.  Rows of
+// codes begin on 32 bytes at any dim, so codes move in whole vectors where
+// the matrix itself cannot.
+#pragma once
+
+#include "row_access.hpp"
+
+namespace rar {
+
+constexpr uint32_t kCkptBlock = 32;
+
+struct Checkpoint {
+  uint8_t* codes;
+  uint8_t* exps;
+  uint64_t nb;
+  __host__ __device__ Checkpoint() : codes(nullptr), exps(nullptr), nb(0) {}
+  __host__ __device__ Checkpoint(void* p, uint64_t rows, uint64_t dim)
+      : codes((uint8_t*)p), exps((uint8_t*)p + rows * ((dim + 31) / 32 * 32)), nb((dim + 31) / 32) {}
+  __device__ __forceinline__ uint8_t* code_row(uint64_t r) const { return codes + r * nb * kCkptBlock; }
+  __device__ __forceinline__ uint8_t* exp_row(uint64_t r) const { return exps + r * nb; }
+};
+
+// 2^-k, NaN for E = 255: every value of a block is its code times this, exactly
+// (the least step, 2^-132, is a subnormal that binary32 still holds).
+__device__ __forceinline__ float ckpt_step(uint32_t E) {
+  const float s = __builtin_amdgcn_ldexpf(1.0f, (int)(E < 1 ? 1 : E) - 133);
+  return E == 255 ? __builtin_nanf("") : s;
+}
+
+// Four codes of a block whose largest |x| has these bits, packed.
+__device__ __forceinline__ uint32_t ckpt_encode4(const float* x, const BfpScale& sc) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = sc.nan ? 0 : (int)bfp_q(x[i], sc.k, 127.0f);
+    w |= (uint32_t)(q & 0xff) << (8 * i);
+  }
+  return w;
+}
+__device__ __forceinline__ float ckpt_code(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
+
+template <int E>
+__device__ __forceinline__ uint32_t vec_absmax(const VecF<E>& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) m = max(m, absbits(x.v[i]));
+  return m;
+}
+
+// A vector of E codes as stored, with its block's exponent.
+template <int E>
+struct CkptRaw {
+  uint32_t w[E / 4];
+  uint32_t e;
+};
+template <int E>
+__device__ __forceinline__ CkptRaw<E> ckpt_load(const uint8_t* codes, const uint8_t* exps, uint32_t col) {
+  static_assert(E == 4 || E == 8, "");
+  CkptRaw<E> r;
+  if constexpr (E == 8) {
+    const u32x2 x = __builtin_nontemporal_load((const u32x2*)(codes + col));
+    r.w[0] = x[0];
+    r.w[1] = x[1];
+  } else {
+    r.w[0] = __builtin_nontemporal_load((const uint32_t*)(codes + col));
+  }
+  r.e = exps[col / kCkptBlock];
+  return r;
+}
+template <int E>
+__device__ __forceinline__ VecF<E> ckpt_unpack(const CkptRaw<E>& r) {
+  VecF<E> f;
+  const float step = ckpt_step(r.e);
+#pragma unroll
+  for (int i = 0; i < E; ++i) f.v[i] = ckpt_code(r.w[i / 4], i % 4) * step;
+  return f;
+}
+__device__ __forceinline__ float ckpt_elem(const uint8_t* codes, const uint8_t* exps, uint64_t col) {
+  return (float)(int8_t)codes[col] * ckpt_step(exps[col / kCkptBlock]);
+}
+
+// Stores a lane's E values as codes, and by the first lane of each block its
+// exponent.  m: the block's largest absolute bits, over the 32 / E lanes that
+// hold it.
+template <int E>
+__device__ __forceinline__ void ckpt_store(uint8_t* codes, uint8_t* exps, uint32_t col, uint32_t m,
+                                           const VecF<E>& x) {
+  const BfpScale sc = bfp_scale(m, 8);
+  if constexpr (E == 8)
+    __builtin_nontemporal_store((u32x2){ckpt_encode4(x.v, sc), ckpt_encode4(x.v + 4, sc)}, (u32x2*)(codes + col));
+  else
+    __builtin_nontemporal_store(ckpt_encode4(x.v, sc), (uint32_t*)(codes + col));
+  if (col % kCkptBlock == 0) exps[col / kCkptBlock] = (uint8_t)(m >> 23);
+}
+
+}  // namespace rar

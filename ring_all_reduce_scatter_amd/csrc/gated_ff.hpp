@@ -1,0 +1,94 @@
+// Gated feed-forward block: what its kernels share.
+//
+//   g = x Wg^T,  u = x Wu^T,  h = round(act(g) u)
+//   dg = round(dh u act'(g)),  du = round(dh act(g))
+//   dx = round(dg Wg + du Wu),  dWg = round(dg^T x [+ dWg]),  dWu the same of du
+//
+// x is rows x dim, Wg and Wu hidden x dim, everything else rows x hidden.
+#pragma once
+
+#include "operator_launch.hpp"
+#include "row_access.hpp"
+
+namespace rar {
+
+enum FfAct : int { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2 };
+
+// 1 / (1 + exp(-z)) from the hardware's 2^x and reciprocal (1 ulp each): the
+// rounding of z log2(e) adds |z| 2^-24 of the exponential, which no rounding
+// to 16 bits shows.  Far below 2^-126 the exponential is infinite, the result 0.
+__device__ __forceinline__ float ff_sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
+
+// act(g) and (D) its derivative.  The tanh form of gelu is g s(2 z) with
+// z = c (g + 0.044715 g^3): (1 + tanh z) / 2 is the logistic function of 2 z.
+// s (1 - s) first: it is zero where g is large.
+template <bool D>
+__device__ __forceinline__ float ff_act(float g, int act, float* d) {
+  if (act == FF_GELU) {
+    const float p = 0.5f + 0.5f * erff(g * 0.70710678f);
+    if constexpr (D) *d = p + g * 0.39894228f * __builtin_amdgcn_exp2f(g * g * -0.72134752f);
+    return g * p;
+  }
+  if (act == FF_SILU) {
+    const float s = ff_sigmoid(g);
+    if constexpr (D) *d = s + g * (s * (1.0f - s));
+    return g * s;
+  }
+  // past 128 the logistic function is 0 or 1, and the square must not overflow
+  const float g2 = __builtin_fminf(g * g, 16384.0f);
+  const float s = ff_sigmoid(1.59576912f * g * (1.0f + 0.044715f * g2));
+  if constexpr (D) *d = s + g * (s * (1.0f - s)) * (1.59576912f * (1.0f + 3.0f * 0.044715f * g2));
+  return g * s;
+}
+
+// n (at most 16) consecutive values from column col of a row, rounded to DT;
+// ordinary stores, since neighbouring instructions fill the same lines.
+template <int DT>
+__device__ __forceinline__ void ff_store16(char* row, uint64_t col, int n, const float* v) {
+  char* p = row + col * DtypeSize<DT>::value;
+  constexpr int E = 16 / DtypeSize<DT>::value;
+  if (n >= 16) {
+#pragma unroll
+    for (int c = 0; c < 16 / E; ++c) {
+      VecF<E> f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) f.v[i] = v[c * E + i];
+      *(u32x4_any*)(p + 16 * c) = pack_vec<DT, E>(f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) store_elem<DT>(row, col + i, v[i]);
+  }
+}
+
+// One product's operands: P indexes the output's columns, Q its rows.
+struct FfProduct {
+  const char* p[2];
+  const char* q[2];
+  uint64_t pstride[2], qstride[2];  // bytes between rows
+  uint64_t m, n, k;                 // rows and columns of the output, terms of a segment
+  uint32_t tiles_m, tiles_n;
+  uint32_t ktiles, per_split, splits;  // k tiles of all segments, of a split
+  int act, saved;
+  char* out[2];
+  uint64_t out_stride[2];  // bytes
+  int out_dt;
+  bool accumulate;
+  Rows gate, up;
+  Checkpoint cgate, cup;
+  float* partials;  // [output][split][m][pitch]
+  uint64_t pitch;
+};
+
+enum FfKind : int { FF_FORWARD = 0, FF_DX = 1, FF_DW = 2 };
+
+// One product's launch (gated_ff_forward.hip, gated_ff_dx.hip,
+// gated_ff_dw.hip).
+hipError_t launch_ff_forward_tiles(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream);
+hipError_t launch_ff_dx(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream);
+hipError_t launch_ff_dw(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream);
+
+}  // namespace rar

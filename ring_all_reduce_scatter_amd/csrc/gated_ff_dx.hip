@@ -1,0 +1,10 @@
+// dx = dg Wg + du Wu of the gated feed-forward block (gated_ff_tile.hpp).
+#include "gated_ff_tile.hpp"
+
+namespace rar {
+
+hipError_t launch_ff_dx(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream) {
+  return ff_launch_kind<FF_DX>(dt, a, wide, direct, stream);
+}
+
+}  // namespace rar

@@ -1,0 +1,367 @@
+// Gated feed-forward block: the kernels around its tiled products
+// (gated_ff_tile.hpp), and which of them a call takes.
+#include <algorithm>
+
+#include "gated_ff.hpp"
+
+namespace rar {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+
+// ------------------------------------------------------------------ few tokens
+
+// Forward for at most 64 tokens: the weights' bytes are all that counts, and
+// they go from memory straight into the matrix instructions.  A workgroup has
+// 16 hidden columns, NT blocks of 16 tokens, and its 8 wavefronts share the
+// terms: pairs of 64-byte pieces of a row in turn, so that the loads of a
+// wavefront cover whole lines and all of them are on their way at once.  The
+// wavefronts' sums are added through LDS in order.
+constexpr int kFewWaves = 8;
+
+template <int DT>
+__device__ __forceinline__ f32x4 few_mfma(u32x4 w, u32x4 x, f32x4 c) {
+  if constexpr (DT == DT_BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, w), __builtin_bit_cast(b16x8, x), c, 0, 0,
+                                                   0);
+  } else if constexpr (DT == DT_F16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, w), __builtin_bit_cast(h16x8, x), c, 0, 0,
+                                                  0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i]), __uint_as_float(x[i]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// A 16-byte chunk of a row from element e on; elements past dim are zeros.
+template <int DT>
+__device__ __forceinline__ u32x4 few_chunk(const char* row, uint64_t e, uint64_t dim) {
+  constexpr int ES = DtypeSize<DT>::value, EC = 16 / ES;
+  const char* at = row + e * ES;
+  if (e + EC <= dim) return *(const u32x4_any*)at;
+  u32x4 x = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < EC; ++j)
+    if (e + j < dim) {
+      if constexpr (ES == 4) x[j] = ((const uint32_t*)at)[j];
+      else x[j / 2] |= (uint32_t)((const uint16_t*)at)[j] << (16 * (j & 1));
+    }
+  return x;
+}
+
+template <int DT, int NT>
+__global__ __launch_bounds__(kFewWaves * 64) void ff_few_kernel(FfProduct a) {
+  constexpr int ES = DtypeSize<DT>::value, EC = 16 / ES;
+  extern __shared__ float sums[];  // [wavefront][2 NT][256]
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = lane & 15, quad = lane >> 4;
+  const uint64_t c0 = (uint64_t)blockIdx.x * 16;
+  // columns and tokens past the last read the last one's row; what comes of
+  // them is not stored
+  const uint64_t c = c0 + r < a.n ? c0 + r : a.n - 1;
+  const char *wg = a.p[0] + c * a.pstride[0], *wu = a.p[1] + c * a.pstride[1];
+  const char* x[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) x[t] = a.q[0] + (t * 16 + r < a.m ? t * 16 + r : a.m - 1) * a.qstride[0];
+  f32x4 g[NT], u[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) g[t] = u[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  const uint64_t pairs = (a.k + 8 * EC - 1) / (8 * EC);  // 128 bytes of a row
+#pragma unroll 4
+  for (uint64_t k = wave; k < pairs; k += kFewWaves) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint64_t e = (k * 8 + s * 4 + quad) * EC;
+      const u32x4 pg = few_chunk<DT>(wg, e, a.k), pu = few_chunk<DT>(wu, e, a.k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const u32x4 q = few_chunk<DT>(x[t], e, a.k);
+        g[t] = few_mfma<DT>(pg, q, g[t]);
+        u[t] = few_mfma<DT>(pu, q, u[t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sums[(wave * 2 * NT + t) * 256 + r * 16 + quad * 4 + i] = g[t][i];
+      sums[(wave * 2 * NT + NT + t) * 256 + r * 16 + quad * 4 + i] = u[t][i];
+    }
+  __syncthreads();
+  for (uint32_t o = threadIdx.x; o < NT * 256; o += kFewWaves * 64) {
+    float vg = 0.0f, vu = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      vg += sums[w * 2 * NT * 256 + o];
+      vu += sums[(w * 2 * NT + NT) * 256 + o];
+    }
+    const uint64_t token = o / 16, col = c0 + o % 16;
+    if (token >= a.m || col >= a.n) continue;
+    if (a.saved == 1) {
+      store_elem<DT>(a.gate.p + token * a.gate.stride * ES, col, vg);
+      store_elem<DT>(a.up.p + token * a.up.stride * ES, col, vu);
+    }
+    store_elem<DT>(a.out[0] + token * a.out_stride[0], col, ff_act<false>(vg, a.act, nullptr) * vu);
+  }
+}
+
+template <int DT>
+hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.n + 15) / 16)), block(kFewWaves * 64);
+  const int nt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
+  const size_t lds = (size_t)kFewWaves * 2 * nt * 256 * sizeof(float);
+  if (nt == 1) hipLaunchKernelGGL((ff_few_kernel<DT, 1>), grid, block, lds, stream, a);
+  else if (nt == 2) hipLaunchKernelGGL((ff_few_kernel<DT, 2>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((ff_few_kernel<DT, 4>), grid, block, lds, stream, a);
+  return launch_status(stream);
+}
+
+// ------------------------------------------------------------------ gradients of the product
+
+// dg and du from dh and the kept projections, a vector a lane over blocks of
+// 32 columns.  dg and du lie in the workspace with rows of whole blocks; the
+// columns past hidden are made zeros, since dx's product reads whole chunks.
+constexpr int kGradUnroll = 2;
+
+template <int DT, bool CK>
+__global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uint64_t blocks, uint32_t nb) {
+  constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value, LB = kCkptBlock / E;
+  const uint64_t pitch = (uint64_t)nb * kCkptBlock;
+#pragma unroll
+  for (int k = 0; k < kGradUnroll; ++k) {
+    const uint64_t block = ((uint64_t)blockIdx.x * kGradUnroll + k) * (kThreads / LB) + threadIdx.x / LB;
+    if (block >= blocks) return;
+    const uint64_t row = block / nb;
+    const uint32_t col = (uint32_t)(block - row * nb) * kCkptBlock + threadIdx.x % LB * E;
+    const int n = vec_count<E>(a.hidden, col);
+    const VecF<E> dh = load_vec_upto<DT, E>(a.dh.p + row * a.dh.stride * ES, col, n);
+    VecF<E> g, u, dg = {}, du = {};
+    if constexpr (CK) {
+      g = ckpt_unpack<E>(ckpt_load<E>(a.cgate.code_row(row), a.cgate.exp_row(row), col));
+      u = ckpt_unpack<E>(ckpt_load<E>(a.cup.code_row(row), a.cup.exp_row(row), col));
+    } else {
+      g = load_vec_upto<DT, E>(a.gate.p + row * a.gate.stride * ES, col, n);
+      u = load_vec_upto<DT, E>(a.up.p + row * a.up.stride * ES, col, n);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i < n) {
+        float d;
+        const float h = ff_act<true>(g.v[i], a.act, &d);
+        dg.v[i] = dh.v[i] * u.v[i] * d;
+        du.v[i] = dh.v[i] * h;
+      }
+    const uint64_t at = (row * pitch + col) * ES;
+    *(u32x4*)(a.dg + at) = pack_vec<DT, E>(dg);
+    *(u32x4*)(a.du + at) = pack_vec<DT, E>(du);
+  }
+}
+
+template <int DT>
+hipError_t act_grad_dt(const FfBackward& a, hipStream_t stream) {
+  constexpr uint64_t wg = kGradUnroll * kThreads / (kCkptBlock / vec_elems<DT, DT>());
+  const uint64_t nb = (a.hidden + kCkptBlock - 1) / kCkptBlock, blocks = a.rows * nb;
+  const dim3 grid((unsigned)((blocks + wg - 1) / wg));
+  if (a.saved == 2)
+    hipLaunchKernelGGL((ff_act_grad_kernel<DT, true>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb);
+  else
+    hipLaunchKernelGGL((ff_act_grad_kernel<DT, false>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb);
+  return launch_status(stream);
+}
+
+// ------------------------------------------------------------------ sums of splits
+
+// Adds the splits of a product in order and rounds; blockIdx.y is the output.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void ff_join_kernel(FfProduct a) {
+  const uint64_t vecs = a.pitch / 4, i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= a.m * vecs) return;
+  const uint64_t row = i / vecs, col = (i - row * vecs) * 4;
+  const uint64_t z = blockIdx.y, plane = a.m * a.pitch;
+  const float* p = a.partials + z * a.splits * plane + row * a.pitch + col;
+  const int n = vec_count<4>(a.n, col);
+  VecF<4> v = load_vec<DT_F32, 4>((const char*)p, 0);
+  for (uint32_t s = 1; s < a.splits; ++s) {
+    const VecF<4> w = load_vec<DT_F32, 4>((const char*)(p + s * plane), 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.v[e] += w.v[e];
+  }
+  char* out = a.out[z] + row * a.out_stride[z];
+  if (a.accumulate)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) v.v[e] += load_elem_dt(out, col + e, a.out_dt);
+  if (a.out_dt == DT_F32) store_vec_upto<DT_F32, 4>(out, col, n, v);
+  else store_vec_upto<DT, 4>(out, col, n, v);
+}
+
+template <int DT>
+hipError_t join_dt(const FfProduct& a, int outputs, hipStream_t stream) {
+  const uint64_t n = a.m * (a.pitch / 4);
+  hipLaunchKernelGGL((ff_join_kernel<DT>), dim3((unsigned)((n + kThreads - 1) / kThreads), outputs), dim3(kThreads), 0,
+                     stream, a);
+  return launch_status(stream);
+}
+
+// ------------------------------------------------------------------ which kernel
+
+constexpr uint64_t kFewTokens = 64;
+constexpr uint64_t kCus = 256;
+
+uint64_t up_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+uint64_t es_of(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+// Direct loads move 16 bytes from a 16-byte boundary, by offsets of 31 bits
+// in a tile of at most 256 rows.
+bool direct_ok(const char* p, uint64_t stride_bytes) {
+  return (((uint64_t)p | stride_bytes) & 15) == 0 && stride_bytes <= (1u << 22);
+}
+
+// Splits of a product whose tiles of 128 x 128 leave CUs without work: as many
+// as fill them, of at least eight stages each.
+uint32_t splits_of(uint64_t m, uint64_t n, uint64_t outputs, uint64_t ktiles) {
+  const uint64_t tiles = up_div(m, 128) * up_div(n, 128) * outputs;
+  if (tiles == 0 || tiles >= kCus) return 1;
+  return (uint32_t)std::max<uint64_t>(1, std::min(kCus / tiles, ktiles / 8));
+}
+uint64_t stage_terms(int dt) { return 128 / es_of(dt); }
+uint32_t dx_splits(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
+  return splits_of(rows, dim, 1, 2 * up_div(hidden, stage_terms(dt)));
+}
+uint32_t dw_splits(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
+  return splits_of(hidden, dim, 2, up_div(rows, stage_terms(dt)));
+}
+uint64_t partial_pitch(uint64_t n) { return up_div(n, 4) * 4; }
+
+void set_tiles(FfProduct& a, uint64_t tile_m, uint64_t tile_n, uint32_t splits) {
+  a.tiles_m = (uint32_t)up_div(a.m, tile_m);
+  a.tiles_n = (uint32_t)up_div(a.n, tile_n);
+  a.splits = splits;
+  a.per_split = (uint32_t)up_div(a.ktiles, splits);
+  // a split without work would leave its partial sums unwritten
+  if (a.per_split) a.splits = (uint32_t)up_div(a.ktiles, a.per_split);
+}
+
+template <class F>
+hipError_t by_type(int dt, F f) {
+  switch (dt) {
+    case DT_F32: return f(std::integral_constant<int, DT_F32>());
+    case DT_F16: return f(std::integral_constant<int, DT_F16>());
+    default: return f(std::integral_constant<int, DT_BF16>());
+  }
+}
+
+}  // namespace
+
+uint64_t ff_tile_count(uint64_t m, uint64_t n) { return up_div(m, 128) * up_div(n, 64); }
+
+FfWorkspace ff_workspace(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
+  FfWorkspace w;
+  w.pitch = up_div(hidden, kCkptBlock) * kCkptBlock;
+  w.du = up_div(rows * w.pitch * es_of(dt), 256) * 256;
+  w.partials = 2 * w.du;
+  const uint64_t sx = dx_splits(rows, dim, hidden, dt), sw = dw_splits(rows, dim, hidden, dt);
+  const uint64_t bx = sx > 1 ? sx * rows : 0, bw = sw > 1 ? sw * 2 * hidden : 0;
+  w.bytes = w.partials + std::max(bx, bw) * partial_pitch(dim) * sizeof(float);
+  return w;
+}
+
+hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream) {
+  const uint64_t es = es_of(f.dt);
+  FfProduct a{};
+  a.p[0] = f.wgate.p;
+  a.p[1] = f.wup.p;
+  a.pstride[0] = f.wgate.stride * es;
+  a.pstride[1] = f.wup.stride * es;
+  a.q[0] = a.q[1] = f.x.p;
+  a.qstride[0] = a.qstride[1] = f.x.stride * es;
+  a.m = f.rows;
+  a.n = f.hidden;
+  a.k = f.dim;
+  a.ktiles = (uint32_t)up_div(f.dim, stage_terms(f.dt));
+  a.act = f.act;
+  a.saved = f.saved;
+  a.out[0] = f.h.p;
+  a.out_stride[0] = f.h.stride * es;
+  a.gate = f.gate;
+  a.up = f.up;
+  a.cgate = f.cgate;
+  a.cup = f.cup;
+  // a checkpoint's block of 32 columns is more than such a workgroup has
+  if (f.rows <= kFewTokens && f.saved != 2)
+    return by_type(f.dt, [&](auto t) { return few_dt<decltype(t)::value>(a, stream); });
+  const bool direct = f.dim % (16 / es) == 0 && direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) &&
+                      direct_ok(a.q[0], a.qstride[0]);
+  const bool wide = direct && f.dt != DT_F32 && up_div(f.rows, 256) * up_div(f.hidden, 128) >= kCus;
+  set_tiles(a, wide ? 256 : 128, wide ? 128 : 64, 1);
+  return launch_ff_forward_tiles(f.dt, a, wide, direct, stream);
+}
+
+hipError_t launch_gated_ff_grad(const FfBackward& b, hipStream_t stream) {
+  const uint64_t es = es_of(b.dt);
+  const FfWorkspace ws = ff_workspace(b.rows, b.dim, b.hidden, b.dt);
+  hipError_t e = hipSuccess;
+  if (b.rows) {
+    e = by_type(b.dt, [&](auto t) { return act_grad_dt<decltype(t)::value>(b, stream); });
+    if (e != hipSuccess) return e;
+  }
+  auto product = [&](bool dx) {
+    FfProduct a{};
+    a.q[0] = b.dg;
+    a.q[1] = b.du;
+    a.qstride[0] = a.qstride[1] = ws.pitch * es;
+    a.partials = b.partials;
+    a.pitch = partial_pitch(b.dim);
+    a.n = b.dim;
+    bool direct;
+    uint32_t splits;
+    if (dx) {
+      a.p[0] = b.wgate.p;
+      a.p[1] = b.wup.p;
+      a.pstride[0] = b.wgate.stride * es;
+      a.pstride[1] = b.wup.stride * es;
+      a.m = b.rows;
+      a.k = b.hidden;
+      a.ktiles = 2 * (uint32_t)up_div(a.k, stage_terms(b.dt));
+      a.out[0] = b.dx.p;
+      a.out_stride[0] = b.dx.stride * es;
+      a.out_dt = b.dt;
+      // one set of offsets serves both segments
+      direct = direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) && a.pstride[0] == a.pstride[1];
+      splits = dx_splits(b.rows, b.dim, b.hidden, b.dt);
+    } else {
+      a.p[0] = a.p[1] = b.x.p;
+      a.pstride[0] = a.pstride[1] = b.x.stride * es;
+      a.m = b.hidden;
+      a.k = b.rows;
+      a.ktiles = (uint32_t)up_div(a.k, stage_terms(b.dt));
+      const uint64_t oes = es_of(b.wdt);
+      a.out[0] = b.dwgate.p;
+      a.out[1] = b.dwup.p;
+      a.out_stride[0] = b.dwgate.stride * oes;
+      a.out_stride[1] = b.dwup.stride * oes;
+      a.out_dt = b.wdt;
+      a.accumulate = b.accumulate;
+      direct = direct_ok(a.p[0], a.pstride[0]);
+      splits = dw_splits(b.rows, b.dim, b.hidden, b.dt);
+    }
+    direct = direct && ws.pitch * es <= (1u << 22);
+    const int outputs = dx ? 1 : 2;
+    const bool wide =
+        direct && b.dt != DT_F32 && splits == 1 && up_div(a.m, 256) * up_div(a.n, 256) * outputs >= kCus;
+    set_tiles(a, wide ? 256 : 128, wide ? 256 : 128, splits);
+    hipError_t r = dx ? launch_ff_dx(b.dt, a, wide, direct, stream) : launch_ff_dw(b.dt, a, wide, direct, stream);
+    if (r != hipSuccess || a.splits == 1) return r;
+    return by_type(b.dt, [&](auto t) { return join_dt<decltype(t)::value>(a, outputs, stream); });
+  };
+  if (b.dx.p && b.rows) e = product(true);
+  if (e == hipSuccess && b.dwgate.p) e = product(false);
+  return e;
+}
+
+}  // namespace rar

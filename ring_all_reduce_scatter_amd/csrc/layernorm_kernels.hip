@@ -24,7 +24,9 @@
 // bf16 218 us (42 at the copy rate), backward 366 (63), backward 4096 x 12,288
 // f32 295 (95).
 #include <algorithm>
+#include <type_traits>
 
+#include "checkpoint.hpp"
 #include "operator_launch.hpp"
 #include "row_access.hpp"
 
@@ -180,15 +182,48 @@ __device__ __forceinline__ void load_weight(const RowShape<DT, NT, V>& sh, const
   }
 }
 
+// Writes a row's checkpoint from its registers, called by all lanes of the
+// wavefront.  A block of 32 columns is 32 / E consecutive lanes' vectors, so
+// its largest value is a maximum over them; lanes past the row's vectors hold
+// zeros and fill the last block up.  Where elements follow the last vector,
+// the block that holds them goes to the first 16 lanes, two elements each,
+// which read it again (from the cache).
+template <int DT, int NT, int V>
+__device__ __forceinline__ void checkpoint_row(const RowShape<DT, NT, V>& sh, const char* x, uint64_t dim, bool live,
+                                               const RowF<vec_elems<DT, DT>(), V>& v, uint8_t* codes, uint8_t* exps) {
+  constexpr int E = RowShape<DT, NT, V>::E;
+  static_assert(NT % (kCkptBlock / E) == 0, "a block lies in one turn of the row's lanes");
+  // columns of the blocks made of vectors
+  const uint32_t whole = (uint32_t)(sh.ntail ? dim / kCkptBlock : (dim + kCkptBlock - 1) / kCkptBlock) * kCkptBlock;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t m = group_max_u32<kCkptBlock / E>(sh.valid(j) ? vec_absmax(v.v[j]) : 0u);
+    if (live && sh.col(j) < whole) ckpt_store<E>(codes, exps, sh.col(j), m, v.v[j]);
+  }
+  if (sh.ntail) {  // uniform
+    const uint32_t c = whole + sh.lane;
+    float a = 0.0f, b = 0.0f;
+    if (sh.lane < 16 && c < dim) a = load_elem<DT>(x, c);
+    if (sh.lane < 16 && c + 16 < dim) b = load_elem<DT>(x, c + 16);
+    const uint32_t m = group_max_u32<16>(max(absbits(a), absbits(b)));
+    if (live && sh.lane < 16) {
+      const BfpScale sc = bfp_scale(m, 8);
+      codes[c] = (uint8_t)(sc.nan ? 0 : (int)bfp_q(a, sc.k, 127.0f));
+      codes[c + 16] = (uint8_t)(sc.nan ? 0 : (int)bfp_q(b, sc.k, 127.0f));
+      if (sh.lane == 0) exps[whole / kCkptBlock] = (uint8_t)(m >> 23);
+    }
+  }
+}
+
 // Forward: a workgroup of NT * RB lanes carries RB rows at a time and
 // strides over the rows; the next row's loads are issued before this one's
-// sums.
-template <int DT, int NT, int V, int RB>
+// sums.  CK: the rows' checkpoints are written too.
+template <int DT, int NT, int V, int RB, bool CK>
 __global__ __launch_bounds__(NT * RB) void layernorm_row_kernel(Rows x, const void* __restrict__ weight,
                                                                       const void* __restrict__ bias, int wdt,
                                                                       uint64_t rows, uint64_t dim, float eps, Rows y,
                                                                       float* __restrict__ mean,
-                                                                      float* __restrict__ rstd) {
+                                                                      float* __restrict__ rstd, Checkpoint ck) {
   extern __shared__ float lds[];
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
   const uint32_t slot = row_slot<NT>();
@@ -207,6 +242,10 @@ __global__ __launch_bounds__(NT * RB) void layernorm_row_kernel(Rows x, const vo
   for (uint64_t r0 = (uint64_t)blockIdx.x * RB; r0 < rows; r0 += step, r += step) {
     RowF<E, V> v = unpack_row<DT, V>(raw);
     if (r0 + step < rows) load_row(sh, x.p + (r + step < rows ? r + step : rows - 1) * x.stride * ES, raw);
+    if constexpr (CK) {
+      const uint64_t q = r < rows ? r : rows - 1;
+      checkpoint_row(sh, x.p + q * x.stride * ES, dim, r < rows, v, ck.code_row(q), ck.exp_row(q));
+    }
     float s = v.t;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -241,10 +280,45 @@ __global__ __launch_bounds__(NT * RB) void layernorm_row_kernel(Rows x, const vo
   }
 }
 
+// An element of the backward pass's x, from its rows or from its checkpoint.
+template <int DT, bool CK>
+__device__ __forceinline__ float x_elem(const LayernormGrad& a, uint64_t r, uint64_t c) {
+  if constexpr (CK) return ckpt_elem(a.ck.code_row(r), a.ck.exp_row(r), c);
+  else return load_elem<DT>(a.x.p, r * a.x.stride + c);
+}
+
+// A row of x as loaded from its checkpoint.
+template <int DT, int V>
+struct CkptRow {
+  CkptRaw<vec_elems<DT, DT>()> v[V];
+  float t;
+};
+template <int DT, int NT, int V>
+__device__ __forceinline__ void load_ckpt_row(const RowShape<DT, NT, V>& sh, const Checkpoint& ck, uint64_t r,
+                                              CkptRow<DT, V>& x) {
+  constexpr int E = RowShape<DT, NT, V>::E;
+  const uint8_t *codes = ck.code_row(r), *exps = ck.exp_row(r);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (sh.valid(j)) x.v[j] = ckpt_load<E>(codes, exps, sh.col(j));
+    else x.v[j] = CkptRaw<E>{};
+  }
+  x.t = 0.0f;
+  if (sh.tail()) x.t = ckpt_elem(codes, exps, sh.tail_col());
+}
+template <int DT, int V>
+__device__ __forceinline__ RowF<vec_elems<DT, DT>(), V> unpack_row(const CkptRow<DT, V>& x) {
+  RowF<vec_elems<DT, DT>(), V> f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) f.v[j] = ckpt_unpack(x.v[j]);
+  f.t = x.t;
+  return f;
+}
+
 // Sums of dy h and dy over all rows for 64 columns, a column a lane, each
 // wavefront of the workgroup every W-th row, the wavefronts in order; the
 // result goes straight to dw and db.
-template <int DT>
+template <int DT, bool CK>
 __device__ __forceinline__ void grad_columns(const LayernormGrad& a, uint64_t rows, uint64_t dim, uint64_t c0,
                                              uint32_t W, float* lds) {
   const uint32_t lane = threadIdx.x & 63, w = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -254,7 +328,7 @@ __device__ __forceinline__ void grad_columns(const LayernormGrad& a, uint64_t ro
 #pragma unroll 8
     for (uint64_t r = w; r < rows; r += W) {
       const float dy = load_elem<DT>(a.dy.p, r * a.dy.stride + c);
-      const float h = (load_elem<DT>(a.x.p, r * a.x.stride + c) - a.mean[r]) * a.rstd[r];
+      const float h = (x_elem<DT, CK>(a, r, c) - a.mean[r]) * a.rstd[r];
       dw = __builtin_fmaf(dy, h, dw);
       db += dy;
     }
@@ -276,12 +350,13 @@ __device__ __forceinline__ void grad_columns(const LayernormGrad& a, uint64_t ro
 // added (through LDS) and stored as the workgroup's partial sums.
 // Of few rows the workgroups carry only dx (`partial` false), and those past
 // `groups` take the sums column by column, in the same launch.
-template <int DT, int NT, int V, int RB>
+// CK: x comes from its checkpoint, a byte an element and one more for 32.
+template <int DT, int NT, int V, int RB, bool CK>
 __global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGrad a, uint64_t rows,
                                                                        uint64_t dim, uint32_t groups, bool partial) {
   extern __shared__ float lds[];
   if (blockIdx.x >= groups) {
-    grad_columns<DT>(a, rows, dim, (uint64_t)(blockIdx.x - groups) * 64, NT * RB / 64, lds);
+    grad_columns<DT, CK>(a, rows, dim, (uint64_t)(blockIdx.x - groups) * 64, NT * RB / 64, lds);
     return;
   }
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
@@ -292,11 +367,13 @@ __global__ __launch_bounds__(NT * RB) void layernorm_grad_row_kernel(LayernormGr
   const uint64_t step = (uint64_t)groups * RB;
   const bool lines = rows_on_lines<DT>(a.dx);
   uint64_t r = (uint64_t)blockIdx.x * RB + slot;
-  RowRaw<DT, V> rx, ry;
+  std::conditional_t<CK, CkptRow<DT, V>, RowRaw<DT, V>> rx;
+  RowRaw<DT, V> ry;
   float mu_next, rs_next;
   auto fetch = [&](uint64_t row) {
     const uint64_t q = row < rows ? row : rows - 1;
-    load_row(sh, a.x.p + q * a.x.stride * ES, rx);
+    if constexpr (CK) load_ckpt_row(sh, a.ck, q, rx);
+    else load_row(sh, a.x.p + q * a.x.stride * ES, rx);
     load_row(sh, a.dy.p + q * a.dy.stride * ES, ry);
     mu_next = a.mean[q];
     rs_next = a.rstd[q];
@@ -487,7 +564,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_kernel(Rows x, const void*
 }
 
 // Sums over one row group of dy h and dy, a column per lane.
-template <int DT>
+template <int DT, bool CK>
 __global__ __launch_bounds__(kThreads) void layernorm_dw_part_kernel(LayernormGrad a, uint64_t rows, uint64_t dim,
                                                                       uint64_t per) {
   const uint64_t c = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -496,7 +573,7 @@ __global__ __launch_bounds__(kThreads) void layernorm_dw_part_kernel(LayernormGr
   float dw = 0.0f, db = 0.0f;
   for (uint64_t r = r0; r < r1; ++r) {
     const float dy = load_elem<DT>(a.dy.p, r * a.dy.stride + c);
-    const float h = (load_elem<DT>(a.x.p, r * a.x.stride + c) - a.mean[r]) * a.rstd[r];
+    const float h = (x_elem<DT, CK>(a, r, c) - a.mean[r]) * a.rstd[r];
     dw = __builtin_fmaf(dy, h, dw);
     db += dy;
   }
@@ -504,11 +581,10 @@ __global__ __launch_bounds__(kThreads) void layernorm_dw_part_kernel(LayernormGr
   a.partials[((uint64_t)blockIdx.y * 2 + 1) * dim + c] = db;
 }
 
-template <int DT>
+template <int DT, bool CK>
 __global__ __launch_bounds__(kThreads) void layernorm_dx_kernel(LayernormGrad a, uint64_t rows, uint64_t dim) {
   extern __shared__ float red[];
   for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const char* xr = a.x.p + r * a.x.stride * DtypeSize<DT>::value;
     const char* yr = a.dy.p + r * a.dy.stride * DtypeSize<DT>::value;
     char* dr = a.dx.p + r * a.dx.stride * DtypeSize<DT>::value;
     const float mu = a.mean[r], rs = a.rstd[r];
@@ -516,13 +592,13 @@ __global__ __launch_bounds__(kThreads) void layernorm_dx_kernel(LayernormGrad a,
     for (uint64_t c = threadIdx.x; c < dim; c += kThreads) {
       const float g = load_elem<DT>(yr, c) * weight_at(a.weight, a.wdt, c, 1.0f);
       sg += g;
-      sgh = __builtin_fmaf(g, (load_elem<DT>(xr, c) - mu) * rs, sgh);
+      sgh = __builtin_fmaf(g, (x_elem<DT, CK>(a, r, c) - mu) * rs, sgh);
     }
     const float mg = block_sum(sg, red) / (float)dim;
     const float mgh = block_sum(sgh, red) / (float)dim;
     for (uint64_t c = threadIdx.x; c < dim; c += kThreads) {
       const float g = load_elem<DT>(yr, c) * weight_at(a.weight, a.wdt, c, 1.0f);
-      const float h = (load_elem<DT>(xr, c) - mu) * rs;
+      const float h = (x_elem<DT, CK>(a, r, c) - mu) * rs;
       store_elem<DT>(dr, c, rs * (g - mg - h * mgh));
     }
   }
@@ -538,24 +614,25 @@ constexpr uint64_t kGradGroups = 256;
 constexpr uint64_t kFewRows = 512, kFewBytes = 2 << 20;
 uint64_t grad_groups(uint64_t rows, int rb) { return std::min<uint64_t>(kGradGroups, (rows + rb - 1) / rb); }
 
-template <int DT, int NT, int V, int RB>
+template <int DT, int NT, int V, int RB, bool CK>
 hipError_t forward_rows(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
-                        float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream) {
+                        float eps, const Rows& y, float* mean, float* rstd, void* ckpt, hipStream_t stream) {
   // twelve wavefronts per CU: 46.6 us for 16,384 x 4096 in binary16, against
   // 50.6 with eight and 48.8 with sixteen
   constexpr uint64_t waves = NT * RB / 64, per_cu = waves < 12 ? 12 / waves : 1;
   const uint64_t groups = std::min<uint64_t>((rows + RB - 1) / RB, 256 * per_cu);
-  hipLaunchKernelGGL((layernorm_row_kernel<DT, NT, V, RB>), dim3((unsigned)groups), dim3(NT * RB),
-                     RB * 2 * NT / 64 * sizeof(float), stream, x, weight, bias, wdt, rows, dim, eps, y, mean, rstd);
+  hipLaunchKernelGGL((layernorm_row_kernel<DT, NT, V, RB, CK>), dim3((unsigned)groups), dim3(NT * RB),
+                     RB * 2 * NT / 64 * sizeof(float), stream, x, weight, bias, wdt, rows, dim, eps, y, mean, rstd,
+                     CK ? Checkpoint(ckpt, rows, dim) : Checkpoint());
   return launch_status(stream);
 }
 
-template <int DT>
+template <int DT, bool CK>
 hipError_t layernorm_dt(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
-                        float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream) {
+                        float eps, const Rows& y, float* mean, float* rstd, void* ckpt, hipStream_t stream) {
   const uint64_t vecs = dim / vec_elems<DT, DT>();
 #define RAR_FORWARD(NT, V, RB) \
-  return forward_rows<DT, NT, V, RB>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream)
+  return forward_rows<DT, NT, V, RB, CK>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, ckpt, stream)
   if (vecs <= 16) RAR_FORWARD(16, 1, 16);
   if (vecs <= 32) RAR_FORWARD(16, 2, 16);
   if (vecs <= 64) RAR_FORWARD(16, 4, 16);
@@ -569,12 +646,20 @@ hipError_t layernorm_dt(const Rows& x, const void* weight, const void* bias, int
   if (vecs <= 512) RAR_FORWARD(256, 2, 1);
   if (vecs <= 1024) RAR_FORWARD(256, 4, 1);
   if (vecs <= 2048) RAR_FORWARD(512, 4, 1);
-  if constexpr (DT == DT_F32)
-    if (vecs <= 4096) RAR_FORWARD(512, 8, 1);
+  if constexpr (CK) {
+    // Longer rows leave no registers for the blocks: they are packed on their
+    // own, before y, which may be written over x.
+    const hipError_t e = launch_ckpt_pack(x, rows, dim, ckpt, stream);
+    if (e != hipSuccess) return e;
+    return layernorm_dt<DT, false>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, nullptr, stream);
+  } else {
+    if constexpr (DT == DT_F32)
+      if (vecs <= 4096) RAR_FORWARD(512, 8, 1);
+    hipLaunchKernelGGL((layernorm_kernel<DT>), dim3(row_grid(rows)), dim3(kThreads), kWaves * sizeof(float), stream, x,
+                       weight, bias, wdt, rows, dim, eps, y, mean, rstd);
+    return launch_status(stream);
+  }
 #undef RAR_FORWARD
-  hipLaunchKernelGGL((layernorm_kernel<DT>), dim3(row_grid(rows)), dim3(kThreads), kWaves * sizeof(float), stream, x,
-                     weight, bias, wdt, rows, dim, eps, y, mean, rstd);
-  return launch_status(stream);
 }
 
 hipError_t join_partials(const LayernormGrad& a, uint64_t splits, uint64_t dim, hipStream_t stream) {
@@ -586,14 +671,14 @@ hipError_t join_partials(const LayernormGrad& a, uint64_t splits, uint64_t dim, 
   return launch_status(stream);
 }
 
-template <int DT, int NT, int V, int RB>
+template <int DT, int NT, int V, int RB, bool CK>
 hipError_t backward_rows(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
   const uint64_t groups = grad_groups(rows, RB);
   const size_t lds = (RB * 4 * NT / 64 + RB / 2 * 2 * NT * (V * vec_elems<DT, DT>() + 1)) * sizeof(float);
   const size_t column_lds = NT * RB / 64 * 128 * sizeof(float);
   const bool sums = a.dweight || a.dbias;
   auto launch = [&](uint64_t row_groups, uint64_t columns, bool partial) {
-    hipLaunchKernelGGL((layernorm_grad_row_kernel<DT, NT, V, RB>), dim3((unsigned)(row_groups + columns)),
+    hipLaunchKernelGGL((layernorm_grad_row_kernel<DT, NT, V, RB, CK>), dim3((unsigned)(row_groups + columns)),
                        dim3(NT * RB), std::max(lds, column_lds), stream, a, rows, dim, (uint32_t)row_groups, partial);
     return launch_status(stream);
   };
@@ -612,31 +697,32 @@ hipError_t backward_rows(const LayernormGrad& a, uint64_t rows, uint64_t dim, hi
   return e != hipSuccess ? e : launch(groups, 0, false);
 }
 
-template <int DT>
+template <int DT, bool CK>
 hipError_t layernorm_grad_dt(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
   if (rows == 0) return join_partials(a, 0, dim, stream);
   const uint64_t vecs = dim / vec_elems<DT, DT>();
-  if (vecs <= 16) return backward_rows<DT, 16, 1, 64>(a, rows, dim, stream);
-  if (vecs <= 32) return backward_rows<DT, 16, 2, 64>(a, rows, dim, stream);
-  if (vecs <= 64) return backward_rows<DT, 16, 4, 32>(a, rows, dim, stream);
-  if (vecs <= 128) return backward_rows<DT, 64, 2, 8>(a, rows, dim, stream);
-  if (vecs <= 256) return backward_rows<DT, 64, 4, 8>(a, rows, dim, stream);
+  if (vecs <= 16) return backward_rows<DT, 16, 1, 64, CK>(a, rows, dim, stream);
+  // (with codes and exponents to unpack, 64 rows do not fit the registers)
+  if (vecs <= 32) return backward_rows<DT, 16, 2, CK ? 32 : 64, CK>(a, rows, dim, stream);
+  if (vecs <= 64) return backward_rows<DT, 16, 4, 32, CK>(a, rows, dim, stream);
+  if (vecs <= 128) return backward_rows<DT, 64, 2, 8, CK>(a, rows, dim, stream);
+  if (vecs <= 256) return backward_rows<DT, 64, 4, 8, CK>(a, rows, dim, stream);
   // 2560 bf16 columns 74 us (87 with 256 lanes), 1200 binary32 140 (148).
-  if (vecs <= 384) return backward_rows<DT, 128, 3, 4>(a, rows, dim, stream);
-  if (vecs <= 512) return backward_rows<DT, 256, 2, 2>(a, rows, dim, stream);
-  if (vecs <= 1024) return backward_rows<DT, 256, 4, 2>(a, rows, dim, stream);
-  if (vecs <= 2048) return backward_rows<DT, 512, 4, 1>(a, rows, dim, stream);
+  if (vecs <= 384) return backward_rows<DT, 128, 3, 4, CK>(a, rows, dim, stream);
+  if (vecs <= 512) return backward_rows<DT, 256, 2, 2, CK>(a, rows, dim, stream);
+  if (vecs <= 1024) return backward_rows<DT, 256, 4, 2, CK>(a, rows, dim, stream);
+  if (vecs <= 2048) return backward_rows<DT, 512, 4, 1, CK>(a, rows, dim, stream);
   hipError_t e = hipSuccess;
   // dw and db first: dx may be written over dy or x
   if (a.dweight || a.dbias) {
     const uint64_t splits = std::min(layernorm_splits(rows), (rows + 63) / 64);
-    hipLaunchKernelGGL((layernorm_dw_part_kernel<DT>), dim3((unsigned)((dim + kThreads - 1) / kThreads), (unsigned)splits),
+    hipLaunchKernelGGL((layernorm_dw_part_kernel<DT, CK>), dim3((unsigned)((dim + kThreads - 1) / kThreads), (unsigned)splits),
                        dim3(kThreads), 0, stream, a, rows, dim, (rows + splits - 1) / splits);
     if ((e = launch_status(stream)) != hipSuccess) return e;
     if ((e = join_partials(a, splits, dim, stream)) != hipSuccess) return e;
   }
   if (a.dx.p) {
-    hipLaunchKernelGGL((layernorm_dx_kernel<DT>), dim3(row_grid(rows)), dim3(kThreads), kWaves * sizeof(float), stream,
+    hipLaunchKernelGGL((layernorm_dx_kernel<DT, CK>), dim3(row_grid(rows)), dim3(kThreads), kWaves * sizeof(float), stream,
                        a, rows, dim);
     e = launch_status(stream);
   }
@@ -645,14 +731,34 @@ hipError_t layernorm_grad_dt(const LayernormGrad& a, uint64_t rows, uint64_t dim
 
 }  // namespace
 
-hipError_t launch_layernorm(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
-                            float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
+namespace {
+
+template <bool CK>
+hipError_t forward_any(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
+                       float eps, const Rows& y, float* mean, float* rstd, void* ckpt, hipStream_t stream) {
   switch (x.dt) {
-    case DT_F32: return layernorm_dt<DT_F32>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream);
-    case DT_F16: return layernorm_dt<DT_F16>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream);
-    default: return layernorm_dt<DT_BF16>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, stream);
+    case DT_F32: return layernorm_dt<DT_F32, CK>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, ckpt, stream);
+    case DT_F16: return layernorm_dt<DT_F16, CK>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, ckpt, stream);
+    default: return layernorm_dt<DT_BF16, CK>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, ckpt, stream);
   }
+}
+
+template <bool CK>
+hipError_t backward_any(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
+  switch (a.dy.dt) {
+    case DT_F32: return layernorm_grad_dt<DT_F32, CK>(a, rows, dim, stream);
+    case DT_F16: return layernorm_grad_dt<DT_F16, CK>(a, rows, dim, stream);
+    default: return layernorm_grad_dt<DT_BF16, CK>(a, rows, dim, stream);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
+                            float eps, const Rows& y, float* mean, float* rstd, void* ckpt, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  return ckpt ? forward_any<true>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, ckpt, stream)
+              : forward_any<false>(x, weight, bias, wdt, rows, dim, eps, y, mean, rstd, nullptr, stream);
 }
 
 uint64_t layernorm_splits(uint64_t rows) {
@@ -660,11 +766,7 @@ uint64_t layernorm_splits(uint64_t rows) {
 }
 
 hipError_t launch_layernorm_grad(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream) {
-  switch (a.x.dt) {
-    case DT_F32: return layernorm_grad_dt<DT_F32>(a, rows, dim, stream);
-    case DT_F16: return layernorm_grad_dt<DT_F16>(a, rows, dim, stream);
-    default: return layernorm_grad_dt<DT_BF16>(a, rows, dim, stream);
-  }
+  return a.ck.codes ? backward_any<true>(a, rows, dim, stream) : backward_any<false>(a, rows, dim, stream);
 }
 
 }  // namespace rar

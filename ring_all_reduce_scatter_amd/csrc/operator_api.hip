@@ -1,7 +1,9 @@
 // C-ABI of the operators next to the rings (argument checks, workspace
 // layout, launches): global gradient norm and clipping, embedding lookup
-// and gradient, layer norm forward and backward.  Kernels live in
-// clip_kernels.hip, embedding_kernels.hip and layernorm_kernels.hip.
+// and gradient, activation checkpoints, layer norm forward and backward, the
+// gated feed-forward block.  Kernels live in clip_kernels.hip,
+// embedding_kernels.hip, checkpoint_kernels.hip, layernorm_kernels.hip and
+// gated_ff*.hip.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -357,23 +359,79 @@ int rar_embedding_backward(const void* dout, size_t dout_stride, int dout_dtype,
   return hip_rc(launch_embedding_grad(a, (hipStream_t)stream));
 }
 
+// ------------------------------------------------------------------ activation checkpoints
+
+namespace {
+
+// Bytes of a checkpoint; false if they do not fit the address space.
+bool ckpt_bytes(size_t rows, size_t dim, size_t* bytes) {
+  const size_t nb = (dim + kCkptBlock - 1) / kCkptBlock;
+  return !__builtin_mul_overflow(rows, nb * (kCkptBlock + 1), bytes) && *bytes < ((size_t)1 << 48);
+}
+
+int check_ckpt(const void* p, size_t have, size_t need) {
+  if (!p) return RAR_EOVERLAP;
+  if (have < need) return RAR_EWORKSPACE;
+  return (uintptr_t)p & 15u ? RAR_EALIGN : RAR_OK;
+}
+
+// pack: m is x; otherwise it is written.
+int ckpt_call(const void* m, size_t stride, size_t rows, size_t dim, int dtype, const void* ckpt, size_t have,
+              bool pack, hipStream_t st) {
+  if (!dt_ok(dtype)) return RAR_EDTYPE;
+  if (dim > kMaxDim) return RAR_ENOTSUP;
+  const size_t es = es_of(dtype);
+  size_t mb, need;
+  if (dim == 0 || (!pack && stride < dim) || !rows_bytes(rows, dim, stride, es, &mb) || !ckpt_bytes(rows, dim, &need))
+    return RAR_EINVAL;
+  if (rows == 0) return RAR_OK;
+  int rc;
+  if ((rc = check_ptr(m, es)) || (rc = check_ckpt(ckpt, have, need))) return rc;
+  const Range r[] = {{(uintptr_t)m, mb, !pack, 0, stride * es, dim * es}, {(uintptr_t)ckpt, need, pack, 0}};
+  if ((rc = check_ranges(r, 2))) return rc;
+  const Rows rows_of{(char*)m, stride, dtype};
+  return hip_rc(pack ? launch_ckpt_pack(rows_of, rows, dim, (void*)ckpt, st)
+                     : launch_ckpt_unpack(ckpt, rows, dim, rows_of, st));
+}
+
+}  // namespace
+
+size_t rar_checkpoint_bytes(size_t rows, size_t dim) {
+  size_t bytes;
+  return dim == 0 || dim > kMaxDim || !ckpt_bytes(rows, dim, &bytes) ? 0 : bytes;
+}
+
+int rar_checkpoint_pack(const void* x, size_t x_stride, size_t rows, size_t dim, int dtype, void* checkpoint,
+                        size_t checkpoint_bytes, void* stream) {
+  return ckpt_call(x, x_stride, rows, dim, dtype, checkpoint, checkpoint_bytes, true, (hipStream_t)stream);
+}
+
+int rar_checkpoint_unpack(const void* checkpoint, size_t checkpoint_bytes, size_t rows, size_t dim, void* out,
+                          size_t out_stride, int out_dtype, void* stream) {
+  return ckpt_call(out, out_stride, rows, dim, out_dtype, checkpoint, checkpoint_bytes, false, (hipStream_t)stream);
+}
+
 // ------------------------------------------------------------------ layer norm
 
-int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, const void* bias, size_t rows,
-                          size_t dim, int dtype, int weight_dtype, float eps, void* y, size_t y_stride, float* mean,
-                          float* rstd, void* stream) {
+namespace {
+
+// saves: x's checkpoint is written too.
+int layernorm_forward(const void* x, size_t x_stride, const void* weight, const void* bias, size_t rows, size_t dim,
+                      int dtype, int weight_dtype, float eps, void* y, size_t y_stride, float* mean, float* rstd,
+                      bool saves, void* ckpt, size_t have, hipStream_t st) {
   if (!dt_ok(dtype) || !dt_ok(weight_dtype)) return RAR_EDTYPE;
   if (dim > kMaxDim) return RAR_ENOTSUP;
-  size_t xb, yb;
+  size_t xb, yb, cb = 0;
   if (dim == 0 || y_stride < dim || !(eps >= 0.0f) || !rows_bytes(rows, dim, x_stride, es_of(dtype), &xb) ||
-      !rows_bytes(rows, dim, y_stride, es_of(dtype), &yb))
+      !rows_bytes(rows, dim, y_stride, es_of(dtype), &yb) || (saves && !ckpt_bytes(rows, dim, &cb)))
     return RAR_EINVAL;
   if (rows == 0) return RAR_OK;
   int rc;
   const size_t ws = es_of(weight_dtype);
   if ((rc = check_ptr(x, es_of(dtype))) || (rc = check_ptr(y, es_of(dtype))) ||
       (weight && (rc = check_ptr(weight, ws))) || (bias && (rc = check_ptr(bias, ws))) ||
-      (mean && (rc = check_ptr(mean, 4))) || (rstd && (rc = check_ptr(rstd, 4))))
+      (mean && (rc = check_ptr(mean, 4))) || (rstd && (rc = check_ptr(rstd, 4))) ||
+      (saves && (rc = check_ckpt(ckpt, have, cb))))
     return rc;
   const size_t es = es_of(dtype);
   const Range r[] = {{(uintptr_t)y, yb, true, 1, y_stride * es, dim * es},
@@ -381,10 +439,79 @@ int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, co
                      {(uintptr_t)weight, weight ? dim * ws : 0, false, 0},
                      {(uintptr_t)bias, bias ? dim * ws : 0, false, 0},
                      {(uintptr_t)mean, mean ? rows * 4 : 0, true, 0},
-                     {(uintptr_t)rstd, rstd ? rows * 4 : 0, true, 0}};
-  if ((rc = check_ranges(r, 6))) return rc;
+                     {(uintptr_t)rstd, rstd ? rows * 4 : 0, true, 0},
+                     {(uintptr_t)ckpt, cb, true, 0}};
+  if ((rc = check_ranges(r, 7))) return rc;
   return hip_rc(launch_layernorm(Rows{(char*)x, x_stride, dtype}, weight, bias, weight_dtype, rows, dim, eps,
-                                 Rows{(char*)y, y_stride, dtype}, mean, rstd, (hipStream_t)stream));
+                                 Rows{(char*)y, y_stride, dtype}, mean, rstd, ckpt, st));
+}
+
+// held: x is its checkpoint, of `have` bytes.
+int layernorm_backward(const void* dy, size_t dy_stride, const void* x, size_t x_stride, bool held, size_t have,
+                       const void* weight, const float* mean, const float* rstd, size_t rows, size_t dim, int dtype,
+                       int weight_dtype, void* dx, size_t dx_stride, void* dweight, void* dbias, int accumulate,
+                       void* workspace, size_t ws_bytes, hipStream_t st) {
+  if (!dt_ok(dtype) || !dt_ok(weight_dtype)) return RAR_EDTYPE;
+  size_t yb, xb, db = 0;
+  const size_t es = es_of(dtype), ws = es_of(weight_dtype);
+  if (dim > kMaxDim) return RAR_ENOTSUP;
+  if (dim == 0 || !rows_bytes(rows, dim, dy_stride, es, &yb) ||
+      !(held ? ckpt_bytes(rows, dim, &xb) : rows_bytes(rows, dim, x_stride, es, &xb)) ||
+      (dx && (dx_stride < dim || !rows_bytes(rows, dim, dx_stride, es, &db))))
+    return RAR_EINVAL;
+  int rc;
+  if (rows && ((rc = check_ptr(dy, es)) || (rc = held ? check_ckpt(x, have, xb) : check_ptr(x, es)) ||
+               (rc = check_ptr(mean, 4)) || (rc = check_ptr(rstd, 4))))
+    return rc;
+  if ((weight && (rc = check_ptr(weight, ws))) || (dx && (rc = check_ptr(dx, es))) ||
+      (dweight && (rc = check_ptr(dweight, ws))) || (dbias && (rc = check_ptr(dbias, ws))))
+    return rc;
+  const bool sums = dweight || dbias;
+  const size_t need = sums ? rar_layernorm_workspace_bytes(rows, dim) : 0;
+  if (sums && (!workspace || ws_bytes < need)) return RAR_EWORKSPACE;
+  if (sums && ((uintptr_t)workspace & 15u)) return RAR_EALIGN;
+  const Range r[] = {{(uintptr_t)dx, db, true, 1, dx_stride * es, dim * es},
+                     {(uintptr_t)dy, yb, false, dy_stride == dx_stride ? 1 : 0, dy_stride * es, dim * es},
+                     held ? Range{(uintptr_t)x, xb, false, 0}
+                          : Range{(uintptr_t)x, xb, false, x_stride == dx_stride ? 1 : 0, x_stride * es, dim * es},
+                     {(uintptr_t)weight, weight ? dim * ws : 0, false, 0},
+                     {(uintptr_t)mean, rows * 4, false, 0},
+                     {(uintptr_t)rstd, rows * 4, false, 0},
+                     {(uintptr_t)dweight, dweight ? dim * ws : 0, true, 0},
+                     {(uintptr_t)dbias, dbias ? dim * ws : 0, true, 0},
+                     {(uintptr_t)workspace, need, true, 0}};
+  if ((rc = check_ranges(r, 9))) return rc;
+  LayernormGrad a{};
+  a.dy = Rows{(char*)dy, dy_stride, dtype};
+  a.x = Rows{held ? nullptr : (char*)x, x_stride, dtype};
+  if (held) a.ck = Checkpoint((void*)x, rows, dim);
+  a.dx = Rows{(char*)dx, dx_stride, dtype};
+  a.weight = weight;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.partials = (float*)workspace;
+  a.wdt = weight_dtype;
+  a.accumulate = accumulate != 0;
+  return hip_rc(launch_layernorm_grad(a, rows, dim, st));
+}
+
+}  // namespace
+
+int rar_layernorm_forward(const void* x, size_t x_stride, const void* weight, const void* bias, size_t rows,
+                          size_t dim, int dtype, int weight_dtype, float eps, void* y, size_t y_stride, float* mean,
+                          float* rstd, void* stream) {
+  return layernorm_forward(x, x_stride, weight, bias, rows, dim, dtype, weight_dtype, eps, y, y_stride, mean, rstd,
+                           false, nullptr, 0, (hipStream_t)stream);
+}
+
+int rar_layernorm_forward_checkpoint(const void* x, size_t x_stride, const void* weight, const void* bias,
+                                     size_t rows, size_t dim, int dtype, int weight_dtype, float eps, void* y,
+                                     size_t y_stride, float* mean, float* rstd, void* checkpoint,
+                                     size_t checkpoint_bytes, void* stream) {
+  return layernorm_forward(x, x_stride, weight, bias, rows, dim, dtype, weight_dtype, eps, y, y_stride, mean, rstd,
+                           true, checkpoint, checkpoint_bytes, (hipStream_t)stream);
 }
 
 size_t rar_layernorm_workspace_bytes(size_t rows, size_t dim) {
@@ -396,47 +523,165 @@ int rar_layernorm_backward(const void* dy, size_t dy_stride, const void* x, size
                            const float* mean, const float* rstd, size_t rows, size_t dim, int dtype,
                            int weight_dtype, void* dx, size_t dx_stride, void* dweight, void* dbias, int accumulate,
                            void* workspace, size_t ws_bytes, void* stream) {
-  if (!dt_ok(dtype) || !dt_ok(weight_dtype)) return RAR_EDTYPE;
-  size_t yb, xb, db = 0;
-  const size_t es = es_of(dtype), ws = es_of(weight_dtype);
-  if (dim > kMaxDim) return RAR_ENOTSUP;
-  if (dim == 0 || !rows_bytes(rows, dim, dy_stride, es, &yb) ||
-      !rows_bytes(rows, dim, x_stride, es, &xb) || (dx && (dx_stride < dim || !rows_bytes(rows, dim, dx_stride, es, &db))))
-    return RAR_EINVAL;
-  int rc;
-  if (rows && ((rc = check_ptr(dy, es)) || (rc = check_ptr(x, es)) || (rc = check_ptr(mean, 4)) ||
-               (rc = check_ptr(rstd, 4))))
+  return layernorm_backward(dy, dy_stride, x, x_stride, false, 0, weight, mean, rstd, rows, dim, dtype, weight_dtype,
+                            dx, dx_stride, dweight, dbias, accumulate, workspace, ws_bytes, (hipStream_t)stream);
+}
+
+int rar_layernorm_backward_checkpoint(const void* dy, size_t dy_stride, const void* checkpoint,
+                                      size_t checkpoint_bytes, const void* weight, const float* mean,
+                                      const float* rstd, size_t rows, size_t dim, int dtype, int weight_dtype,
+                                      void* dx, size_t dx_stride, void* dweight, void* dbias, int accumulate,
+                                      void* workspace, size_t ws_bytes, void* stream) {
+  return layernorm_backward(dy, dy_stride, checkpoint, 0, true, checkpoint_bytes, weight, mean, rstd, rows, dim, dtype,
+                            weight_dtype, dx, dx_stride, dweight, dbias, accumulate, workspace, ws_bytes,
+                            (hipStream_t)stream);
+}
+
+// ------------------------------------------------------------------ gated feed-forward
+
+namespace {
+
+constexpr size_t kFfMaxCols = (size_t)1 << 26, kFfMaxRows = (size_t)1 << 30;
+constexpr uint64_t kFfMaxTiles = (uint64_t)1 << 22;  // of 512 lanes, for two outputs
+
+int ff_sizes(size_t rows, size_t dim, size_t hidden, int dtype) {
+  if (!dt_ok(dtype)) return RAR_EDTYPE;
+  if (dim == 0 || hidden == 0) return RAR_EINVAL;
+  if (dim > kFfMaxCols || hidden > kFfMaxCols || rows > kFfMaxRows) return RAR_ENOTSUP;
+  if (ff_tile_count(rows, hidden) > kFfMaxTiles || ff_tile_count(rows, dim) > kFfMaxTiles ||
+      ff_tile_count(hidden, dim) > kFfMaxTiles || rows * ((hidden + 31) / 32) > kMaxTiles * 64)
+    return RAR_ENOTSUP;
+  return RAR_OK;
+}
+
+// One of the kept projections: rows of `hidden` elements, or (checkpoint)
+// `stride` bytes of one.
+int ff_kept(const void* p, size_t stride, int saved, size_t rows, size_t hidden, size_t es, bool written, Range* r) {
+  *r = Range{0, 0, false, 0};
+  if (saved == RAR_KEEP_NONE) return RAR_OK;
+  size_t bytes;
+  if (saved == RAR_KEEP_CHECKPOINT) {
+    if (!ckpt_bytes(rows, hidden, &bytes)) return RAR_EINVAL;
+    *r = Range{(uintptr_t)p, bytes, written, 0};
+    return rows ? check_ckpt(p, stride, bytes) : RAR_OK;
+  }
+  if ((written && stride < hidden) || !rows_bytes(rows, hidden, stride, es, &bytes)) return RAR_EINVAL;
+  *r = Range{(uintptr_t)p, bytes, written, 0, stride * es, hidden * es};
+  return rows ? check_ptr(p, es) : RAR_OK;
+}
+
+bool ff_modes_ok(int act, int saved) {
+  return (act == RAR_ACT_SILU || act == RAR_ACT_GELU || act == RAR_ACT_GELU_TANH) &&
+         (saved == RAR_KEEP_NONE || saved == RAR_KEEP_ROWS || saved == RAR_KEEP_CHECKPOINT);
+}
+
+// A matrix of rows as a range, with its checks.
+int ff_matrix(const void* p, size_t stride, size_t rows, size_t cols, size_t es, bool written, Range* r) {
+  size_t bytes;
+  if ((written && stride < cols) || !rows_bytes(rows, cols, stride, es, &bytes)) return RAR_EINVAL;
+  *r = Range{(uintptr_t)p, bytes, written, 0, stride * es, cols * es};
+  return rows ? check_ptr(p, es) : RAR_OK;
+}
+
+}  // namespace
+
+int rar_gated_ff_forward(const void* x, size_t x_stride, const void* wgate, size_t wgate_stride, const void* wup,
+                         size_t wup_stride, size_t rows, size_t dim, size_t hidden, int dtype, int act, void* h,
+                         size_t h_stride, int keep, void* gate, size_t gate_stride, void* up, size_t up_stride,
+                         void* stream) {
+  int rc = ff_sizes(rows, dim, hidden, dtype);
+  if (rc) return rc;
+  if (!ff_modes_ok(act, keep)) return RAR_EINVAL;
+  const size_t es = es_of(dtype);
+  Range r[6];
+  if ((rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[0])) ||
+      (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[1])) ||
+      (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[2])) ||
+      (rc = ff_matrix(h, h_stride, rows, hidden, es, true, &r[3])) ||
+      (rc = ff_kept(gate, gate_stride, keep, rows, hidden, es, true, &r[4])) ||
+      (rc = ff_kept(up, up_stride, keep, rows, hidden, es, true, &r[5])))
     return rc;
-  if ((weight && (rc = check_ptr(weight, ws))) || (dx && (rc = check_ptr(dx, es))) ||
-      (dweight && (rc = check_ptr(dweight, ws))) || (dbias && (rc = check_ptr(dbias, ws))))
+  if (rows == 0) return RAR_OK;
+  if ((rc = check_ranges(r, 6))) return rc;
+  FfForward f{};
+  f.x = Rows{(char*)x, x_stride, dtype};
+  f.wgate = Rows{(char*)wgate, wgate_stride, dtype};
+  f.wup = Rows{(char*)wup, wup_stride, dtype};
+  f.h = Rows{(char*)h, h_stride, dtype};
+  f.gate = Rows{(char*)gate, gate_stride, dtype};
+  f.up = Rows{(char*)up, up_stride, dtype};
+  if (keep == RAR_KEEP_CHECKPOINT) {
+    f.cgate = Checkpoint(gate, rows, hidden);
+    f.cup = Checkpoint(up, rows, hidden);
+  }
+  f.rows = rows;
+  f.dim = dim;
+  f.hidden = hidden;
+  f.dt = dtype;
+  f.act = act;
+  f.saved = keep;
+  return hip_rc(launch_gated_ff(f, (hipStream_t)stream));
+}
+
+size_t rar_gated_ff_workspace_bytes(size_t rows, size_t dim, size_t hidden, int dtype) {
+  return ff_sizes(rows, dim, hidden, dtype) ? 0 : ff_workspace(rows, dim, hidden, dtype).bytes;
+}
+
+int rar_gated_ff_backward(const void* dh, size_t dh_stride, const void* x, size_t x_stride, const void* wgate,
+                          size_t wgate_stride, const void* wup, size_t wup_stride, int keep, const void* gate,
+                          size_t gate_stride, const void* up, size_t up_stride, size_t rows, size_t dim,
+                          size_t hidden, int dtype, int act, void* dx, size_t dx_stride, void* dwgate,
+                          size_t dwgate_stride, void* dwup, size_t dwup_stride, int dweight_dtype, int accumulate,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  int rc = ff_sizes(rows, dim, hidden, dtype);
+  if (rc) return rc;
+  if (!ff_modes_ok(act, keep) || keep == RAR_KEEP_NONE || !dwgate != !dwup) return RAR_EINVAL;
+  if (dweight_dtype != dtype && dweight_dtype != RAR_F32) return RAR_EDTYPE;
+  const size_t es = es_of(dtype), we = es_of(dweight_dtype);
+  Range r[10];
+  if ((rc = ff_matrix(dh, dh_stride, rows, hidden, es, false, &r[0])) ||
+      (rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[1])) ||
+      (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[2])) ||
+      (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[3])) ||
+      (rc = ff_kept(gate, gate_stride, keep, rows, hidden, es, false, &r[4])) ||
+      (rc = ff_kept(up, up_stride, keep, rows, hidden, es, false, &r[5])) ||
+      (rc = ff_matrix(dx, dx_stride, dx ? rows : 0, dim, es, true, &r[6])) ||
+      (rc = ff_matrix(dwgate, dwgate_stride, dwgate ? hidden : 0, dim, we, true, &r[7])) ||
+      (rc = ff_matrix(dwup, dwup_stride, dwup ? hidden : 0, dim, we, true, &r[8])))
     return rc;
-  const bool sums = dweight || dbias;
-  const size_t need = sums ? rar_layernorm_workspace_bytes(rows, dim) : 0;
-  if (sums && (!workspace || ws_bytes < need)) return RAR_EWORKSPACE;
-  if (sums && ((uintptr_t)workspace & 15u)) return RAR_EALIGN;
-  const Range r[] = {{(uintptr_t)dx, db, true, 1, dx_stride * es, dim * es},
-                     {(uintptr_t)dy, yb, false, dy_stride == dx_stride ? 1 : 0, dy_stride * es, dim * es},
-                     {(uintptr_t)x, xb, false, x_stride == dx_stride ? 1 : 0, x_stride * es, dim * es},
-                     {(uintptr_t)weight, weight ? dim * ws : 0, false, 0},
-                     {(uintptr_t)mean, rows * 4, false, 0},
-                     {(uintptr_t)rstd, rows * 4, false, 0},
-                     {(uintptr_t)dweight, dweight ? dim * ws : 0, true, 0},
-                     {(uintptr_t)dbias, dbias ? dim * ws : 0, true, 0},
-                     {(uintptr_t)workspace, need, true, 0}};
-  if ((rc = check_ranges(r, 9))) return rc;
-  LayernormGrad a{};
-  a.dy = Rows{(char*)dy, dy_stride, dtype};
-  a.x = Rows{(char*)x, x_stride, dtype};
-  a.dx = Rows{(char*)dx, dx_stride, dtype};
-  a.weight = weight;
-  a.mean = mean;
-  a.rstd = rstd;
-  a.dweight = dweight;
-  a.dbias = dbias;
-  a.partials = (float*)workspace;
-  a.wdt = weight_dtype;
-  a.accumulate = accumulate != 0;
-  return hip_rc(launch_layernorm_grad(a, rows, dim, (hipStream_t)stream));
+  const FfWorkspace l = ff_workspace(rows, dim, hidden, dtype);
+  if (l.bytes && (!workspace || ws_bytes < l.bytes)) return RAR_EWORKSPACE;
+  if ((uintptr_t)workspace & 15u) return RAR_EALIGN;
+  r[9] = Range{(uintptr_t)workspace, l.bytes, true, 0};
+  if ((rc = check_ranges(r, 10))) return rc;
+  if (!dx && !dwgate) return RAR_OK;
+  if (rows == 0 && (!dwgate || accumulate)) return RAR_OK;
+  FfBackward b{};
+  b.dh = Rows{(char*)dh, dh_stride, dtype};
+  b.x = Rows{(char*)x, x_stride, dtype};
+  b.wgate = Rows{(char*)wgate, wgate_stride, dtype};
+  b.wup = Rows{(char*)wup, wup_stride, dtype};
+  b.gate = Rows{(char*)gate, gate_stride, dtype};
+  b.up = Rows{(char*)up, up_stride, dtype};
+  if (keep == RAR_KEEP_CHECKPOINT) {
+    b.cgate = Checkpoint((void*)gate, rows, hidden);
+    b.cup = Checkpoint((void*)up, rows, hidden);
+  }
+  b.dx = Rows{(char*)dx, dx_stride, dtype};
+  b.dwgate = Rows{(char*)dwgate, dwgate_stride, dweight_dtype};
+  b.dwup = Rows{(char*)dwup, dwup_stride, dweight_dtype};
+  b.dg = (char*)workspace;
+  b.du = (char*)workspace + l.du;
+  b.partials = (float*)((char*)workspace + l.partials);
+  b.rows = rows;
+  b.dim = dim;
+  b.hidden = hidden;
+  b.dt = dtype;
+  b.wdt = dweight_dtype;
+  b.act = act;
+  b.saved = keep;
+  b.accumulate = accumulate != 0;
+  return hip_rc(launch_gated_ff_grad(b, (hipStream_t)stream));
 }
 
 }  // extern "C"

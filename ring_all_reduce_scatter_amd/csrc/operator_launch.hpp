@@ -1,11 +1,19 @@
 // Host-side launchers of the operators next to the rings: global gradient
-// norm and clipping, embedding, layer norm (internal to librar.so).  As in
+// norm and clipping, embedding, activation checkpoints, layer norm, gated
+// feed-forward (internal to librar.so).  As in
 // launch.hpp every launcher enqueues asynchronously on `stream`.
 #pragma once
 
+#include "checkpoint.hpp"
 #include "launch.hpp"
 
 namespace rar {
+
+struct Rows {  // rows of `dim` elements, `stride` elements apart
+  char* p;
+  uint64_t stride;
+  int dt;
+};
 
 // -------------------------------------------------------------- norm and clip (clip_kernels.hip)
 
@@ -35,11 +43,6 @@ hipError_t launch_grad_clip(const ClipSet& set, int kind, double scale, double m
 
 // -------------------------------------------------------------- embedding (embedding_kernels.hip)
 
-struct Rows {  // rows of `dim` elements, `stride` elements apart
-  char* p;
-  uint64_t stride;
-  int dt;
-};
 hipError_t launch_embedding(const Rows& weight, uint64_t vocab, uint64_t dim, const void* ids, bool ids64,
                             uint64_t tokens, float scale, const Rows& out, hipStream_t stream);
 
@@ -73,15 +76,22 @@ struct EmbeddingGrad {
 };
 hipError_t launch_embedding_grad(const EmbeddingGrad& a, hipStream_t stream);
 
+// -------------------------------------------------------------- activation checkpoints (checkpoint_kernels.hip)
+
+hipError_t launch_ckpt_pack(const Rows& x, uint64_t rows, uint64_t dim, void* ckpt, hipStream_t stream);
+hipError_t launch_ckpt_unpack(const void* ckpt, uint64_t rows, uint64_t dim, const Rows& out, hipStream_t stream);
+
 // -------------------------------------------------------------- layer norm (layernorm_kernels.hip)
 
+// ckpt: where x's checkpoint is written, or NULL.
 hipError_t launch_layernorm(const Rows& x, const void* weight, const void* bias, int wdt, uint64_t rows, uint64_t dim,
-                            float eps, const Rows& y, float* mean, float* rstd, hipStream_t stream);
+                            float eps, const Rows& y, float* mean, float* rstd, void* ckpt, hipStream_t stream);
 // Row groups whose sums of the weight's and bias's gradients are kept apart
 // in the workspace (2 * splits * dim floats) before they are added.
 uint64_t layernorm_splits(uint64_t rows);
 struct LayernormGrad {
   Rows dy, x, dx;
+  Checkpoint ck;  // of x, in place of x
   const void* weight;
   const float* mean;
   const float* rstd;
@@ -92,5 +102,36 @@ struct LayernormGrad {
   bool accumulate;
 };
 hipError_t launch_layernorm_grad(const LayernormGrad& a, uint64_t rows, uint64_t dim, hipStream_t stream);
+
+// -------------------------------------------------------------- gated feed-forward (gated_ff_kernels.hip)
+
+// saved: 0 nothing, 1 the projections in the activations' type (gate, up), 2
+// their checkpoints (cgate, cup).
+struct FfForward {
+  Rows x, wgate, wup, h, gate, up;
+  Checkpoint cgate, cup;
+  uint64_t rows, dim, hidden;
+  int dt, act, saved;
+};
+hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream);
+
+// Workspace of the backward pass: dg, du (rows x pitch elements each), then
+// the partial sums of split products.
+struct FfWorkspace {
+  uint64_t pitch, du, partials, bytes;
+};
+FfWorkspace ff_workspace(uint64_t rows, uint64_t dim, uint64_t hidden, int dt);
+struct FfBackward {
+  Rows dh, x, wgate, wup, gate, up, dx, dwgate, dwup;
+  Checkpoint cgate, cup;
+  char *dg, *du;
+  float* partials;
+  uint64_t rows, dim, hidden;
+  int dt, wdt, act, saved;
+  bool accumulate;
+};
+hipError_t launch_gated_ff_grad(const FfBackward& b, hipStream_t stream);
+// Workgroups of the smallest tiles over m x n outputs: what launches have to hold.
+uint64_t ff_tile_count(uint64_t m, uint64_t n);
 
 }  // namespace rar
