@@ -690,8 +690,9 @@ typedef enum rar_keep { RAR_KEEP_NONE = 0, RAR_KEEP_ROWS = 1, RAR_KEEP_CHECKPOIN
  * with sums, activation and product in binary32.  keep: gate and up receive g
  * and u, rounded to rows of hidden elements *_stride apart, or as checkpoints
  * of rows x hidden, where *_stride is the buffer's bytes.  x_stride and the
- * weights' strides may be 0.  RAR_ENOTSUP beyond 2^26 columns of dim or
- * hidden, 2^30 rows, or 2^22 tiles of 128 x 64 of any matrix of the call. */
+ * weights' strides may be 0.  RAR_ENOTSUP beyond 2^20 columns of dim or
+ * hidden, 2^30 rows, rows of x or the weights more than 2^22 bytes apart, or
+ * 2^24 tiles of 64 x 64 of any matrix of the call; backward too. */
 int rar_gated_ff_forward(const void* x, size_t x_stride, const void* wgate, size_t wgate_stride,
                          const void* wup, size_t wup_stride, size_t rows, size_t dim, size_t hidden,
                          int dtype, int act, void* h, size_t h_stride, int keep, void* gate,

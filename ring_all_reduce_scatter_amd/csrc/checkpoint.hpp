@@ -40,15 +40,37 @@ __device__ __forceinline__ float ckpt_step(uint32_t E) {
   return E == 255 ? __builtin_nanf("") : s;
 }
 
-// Four codes of a block whose largest |x| has these bits, packed.
-__device__ __forceinline__ uint32_t ckpt_encode4(const float* x, const BfpScale& sc) {
-  uint32_t w = 0;
+// How a block of largest bits m is encoded.  Adding 1.5 * 2^23 to x 2^k in one
+// fused step rounds to a whole number, to even on ties, and leaves it in the
+// sum's low bits; values that would round to 128 are held at 127 before that.
+// Nine instructions for two values then become five.  2^k passes binary32 for
+// the smallest exponents, which go the plain way.
+struct CkptScale {
+  float s, most;  // 2^k, 127 * 2^-k
+  BfpScale plain;
+  bool tiny;
+};
+__device__ __forceinline__ CkptScale ckpt_scale(uint32_t m) {
+  CkptScale c;
+  c.plain = bfp_scale(m, 8);
+  c.tiny = c.plain.k > 127;
+  c.s = __builtin_amdgcn_ldexpf(1.0f, c.plain.k);
+  c.most = __builtin_amdgcn_ldexpf(127.0f, -c.plain.k);
+  return c;
+}
+
+// Four codes of a block, packed.
+__device__ __forceinline__ uint32_t ckpt_encode4(const float* x, const CkptScale& c) {
+  uint32_t q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int q = sc.nan ? 0 : (int)bfp_q(x[i], sc.k, 127.0f);
-    w |= (uint32_t)(q & 0xff) << (8 * i);
+  for (int i = 0; i < 4; ++i)
+    q[i] = __float_as_uint(__builtin_fmaf(__builtin_amdgcn_fmed3f(x[i], -c.most, c.most), c.s, 12582912.0f));
+  if (c.tiny) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = (uint32_t)(int)bfp_q(x[i], c.plain.k, 127.0f);
   }
-  return w;
+  const uint32_t lo = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(q[3], q[2], 0x04000c0c);
+  return c.plain.nan ? 0 : lo | hi;
 }
 __device__ __forceinline__ float ckpt_code(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
@@ -98,7 +120,7 @@ __device__ __forceinline__ float ckpt_elem(const uint8_t* codes, const uint8_t* 
 template <int E>
 __device__ __forceinline__ void ckpt_store(uint8_t* codes, uint8_t* exps, uint32_t col, uint32_t m,
                                            const VecF<E>& x) {
-  const BfpScale sc = bfp_scale(m, 8);
+  const CkptScale sc = ckpt_scale(m);
   if constexpr (E == 8)
     __builtin_nontemporal_store((u32x2){ckpt_encode4(x.v, sc), ckpt_encode4(x.v + 4, sc)}, (u32x2*)(codes + col));
   else

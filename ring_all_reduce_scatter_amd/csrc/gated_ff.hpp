@@ -43,35 +43,14 @@ __device__ __forceinline__ float ff_act(float g, int act, float* d) {
   return g * s;
 }
 
-// n (at most 16) consecutive values from column col of a row, rounded to DT;
-// ordinary stores, since neighbouring instructions fill the same lines.
-template <int DT>
-__device__ __forceinline__ void ff_store16(char* row, uint64_t col, int n, const float* v) {
-  char* p = row + col * DtypeSize<DT>::value;
-  constexpr int E = 16 / DtypeSize<DT>::value;
-  if (n >= 16) {
-#pragma unroll
-    for (int c = 0; c < 16 / E; ++c) {
-      VecF<E> f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) f.v[i] = v[c * E + i];
-      *(u32x4_any*)(p + 16 * c) = pack_vec<DT, E>(f);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) store_elem<DT>(row, col + i, v[i]);
-  }
-}
-
 // One product's operands: P indexes the output's columns, Q its rows.
 struct FfProduct {
   const char* p[2];
   const char* q[2];
-  uint64_t pstride[2], qstride[2];  // bytes between rows
+  uint32_t pstride[2], qstride;  // bytes between rows (dx: the same for both P)
   uint64_t m, n, k;                 // rows and columns of the output, terms of a segment
-  uint32_t tiles_m, tiles_n;
-  uint32_t ktiles, per_split, splits;  // k tiles of all segments, of a split
+  uint32_t splits;                            // wanted; the launch makes it what there is work for
+  uint32_t tiles_m, tiles_n, ktiles, per_split;  // set by the launch; stages of all segments, of a split
   int act, saved;
   char* out[2];
   uint64_t out_stride[2];  // bytes
@@ -86,9 +65,9 @@ struct FfProduct {
 enum FfKind : int { FF_FORWARD = 0, FF_DX = 1, FF_DW = 2 };
 
 // One product's launch (gated_ff_forward.hip, gated_ff_dx.hip,
-// gated_ff_dw.hip).
-hipError_t launch_ff_forward_tiles(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream);
-hipError_t launch_ff_dx(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream);
-hipError_t launch_ff_dw(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream);
+// gated_ff_dw.hip), of at least one term.
+hipError_t launch_ff_forward_tiles(int dt, FfProduct& a, bool wide, bool direct, hipStream_t stream);
+hipError_t launch_ff_dx(int dt, FfProduct& a, bool wide, bool direct, hipStream_t stream);
+hipError_t launch_ff_dw(int dt, FfProduct& a, bool wide, bool direct, hipStream_t stream);
 
 }  // namespace rar

@@ -3,7 +3,7 @@
 
 namespace rar {
 
-hipError_t launch_ff_dx(int dt, const FfProduct& a, bool wide, bool direct, hipStream_t stream) {
+hipError_t launch_ff_dx(int dt, FfProduct& a, bool wide, bool direct, hipStream_t stream) {
   return ff_launch_kind<FF_DX>(dt, a, wide, direct, stream);
 }
 

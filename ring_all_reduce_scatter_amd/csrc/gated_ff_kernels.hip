@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void ff_few_kernel(FfProduct a) {
   const char *wg = a.p[0] + c * a.pstride[0], *wu = a.p[1] + c * a.pstride[1];
   const char* x[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = a.q[0] + (t * 16 + r < a.m ? t * 16 + r : a.m - 1) * a.qstride[0];
+  for (int t = 0; t < NT; ++t) x[t] = a.q[0] + (t * 16 + r < a.m ? t * 16 + r : a.m - 1) * a.qstride;
   f32x4 g[NT], u[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) g[t] = u[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -129,7 +129,8 @@ hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
 constexpr int kGradUnroll = 2;
 
 template <int DT, bool CK>
-__global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uint64_t blocks, uint32_t nb) {
+__global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uint64_t blocks, uint32_t nb,
+                                                                uint64_t du_at) {
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value, LB = kCkptBlock / E;
   const uint64_t pitch = (uint64_t)nb * kCkptBlock;
 #pragma unroll
@@ -157,8 +158,8 @@ __global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uin
         du.v[i] = dh.v[i] * h;
       }
     const uint64_t at = (row * pitch + col) * ES;
-    *(u32x4*)(a.dg + at) = pack_vec<DT, E>(dg);
-    *(u32x4*)(a.du + at) = pack_vec<DT, E>(du);
+    *(u32x4*)(a.ws + at) = pack_vec<DT, E>(dg);
+    *(u32x4*)(a.ws + du_at + at) = pack_vec<DT, E>(du);
   }
 }
 
@@ -167,10 +168,13 @@ hipError_t act_grad_dt(const FfBackward& a, hipStream_t stream) {
   constexpr uint64_t wg = kGradUnroll * kThreads / (kCkptBlock / vec_elems<DT, DT>());
   const uint64_t nb = (a.hidden + kCkptBlock - 1) / kCkptBlock, blocks = a.rows * nb;
   const dim3 grid((unsigned)((blocks + wg - 1) / wg));
+  const uint64_t du_at = ff_workspace(a.rows, a.dim, a.hidden, DT).du;
   if (a.saved == 2)
-    hipLaunchKernelGGL((ff_act_grad_kernel<DT, true>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb);
+    hipLaunchKernelGGL((ff_act_grad_kernel<DT, true>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb,
+                       du_at);
   else
-    hipLaunchKernelGGL((ff_act_grad_kernel<DT, false>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb);
+    hipLaunchKernelGGL((ff_act_grad_kernel<DT, false>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb,
+                       du_at);
   return launch_status(stream);
 }
 
@@ -185,8 +189,8 @@ __global__ __launch_bounds__(kThreads) void ff_join_kernel(FfProduct a) {
   const uint64_t z = blockIdx.y, plane = a.m * a.pitch;
   const float* p = a.partials + z * a.splits * plane + row * a.pitch + col;
   const int n = vec_count<4>(a.n, col);
-  VecF<4> v = load_vec<DT_F32, 4>((const char*)p, 0);
-  for (uint32_t s = 1; s < a.splits; ++s) {
+  VecF<4> v = {};
+  for (uint32_t s = 0; s < a.splits; ++s) {
     const VecF<4> w = load_vec<DT_F32, 4>((const char*)(p + s * plane), 0);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v.v[e] += w.v[e];
@@ -208,6 +212,38 @@ hipError_t join_dt(const FfProduct& a, int outputs, hipStream_t stream) {
   return launch_status(stream);
 }
 
+// ------------------------------------------------------------------ aligned copies
+
+// Rows of `dim` elements copied to rows of whole blocks, zeros after them: what
+// direct loads read where the rows themselves begin off 16 bytes.
+struct FfCopy {
+  const char* from[3];
+  uint64_t stride[3], rows[3];
+  char* to[3];
+};
+template <int DT>
+__global__ __launch_bounds__(kThreads) void ff_copy_kernel(FfCopy a, uint64_t dim, uint32_t nb) {
+  constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value, LB = kCkptBlock / E;
+  const uint32_t m = blockIdx.y;
+  for (uint64_t block = (uint64_t)blockIdx.x * (kThreads / LB) + threadIdx.x / LB; block < a.rows[m] * nb;
+       block += (uint64_t)gridDim.x * (kThreads / LB)) {
+    const uint64_t row = block / nb;
+    const uint32_t col = (uint32_t)(block - row * nb) * kCkptBlock + threadIdx.x % LB * E;
+    const VecF<E> v = load_vec_upto<DT, E>(a.from[m] + row * a.stride[m] * ES, col, vec_count<E>(dim, col));
+    *(u32x4*)(a.to[m] + block * kCkptBlock * ES + threadIdx.x % LB * 16) = pack_vec<DT, E>(v);
+  }
+}
+
+template <int DT>
+hipError_t copy_dt(const FfCopy& a, uint64_t dim, hipStream_t stream) {
+  constexpr uint64_t wg = kThreads / (kCkptBlock / vec_elems<DT, DT>());
+  const uint64_t nb = (dim + kCkptBlock - 1) / kCkptBlock;
+  const uint64_t most = std::max(a.rows[0], std::max(a.rows[1], a.rows[2])) * nb;
+  const dim3 grid((unsigned)std::min<uint64_t>((most + wg - 1) / wg, 1 << 16), 3);
+  hipLaunchKernelGGL((ff_copy_kernel<DT>), grid, dim3(kThreads), 0, stream, a, dim, (uint32_t)nb);
+  return launch_status(stream);
+}
+
 // ------------------------------------------------------------------ which kernel
 
 constexpr uint64_t kFewTokens = 64;
@@ -215,37 +251,37 @@ constexpr uint64_t kCus = 256;
 
 uint64_t up_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 uint64_t es_of(int dt) { return dt == DT_F32 ? 4 : 2; }
+uint64_t blocks_pitch(uint64_t n) { return up_div(n, kCkptBlock) * kCkptBlock; }
 
-// Direct loads move 16 bytes from a 16-byte boundary, by offsets of 31 bits
-// in a tile of at most 256 rows.
-bool direct_ok(const char* p, uint64_t stride_bytes) {
-  return (((uint64_t)p | stride_bytes) & 15) == 0 && stride_bytes <= (1u << 22);
-}
+// Direct loads move 16 bytes from a 16-byte boundary.
+bool direct_ok(const char* p, uint64_t stride_bytes) { return (((uint64_t)p | stride_bytes) & 15) == 0; }
 
-// Splits of a product whose tiles of 128 x 128 leave CUs without work: as many
-// as fill them, of at least eight stages each.
-uint32_t splits_of(uint64_t m, uint64_t n, uint64_t outputs, uint64_t ktiles) {
-  const uint64_t tiles = up_div(m, 128) * up_div(n, 128) * outputs;
-  if (tiles == 0 || tiles >= kCus) return 1;
-  return (uint32_t)std::max<uint64_t>(1, std::min(kCus / tiles, ktiles / 8));
+// How a product is cut: tiles of 256 x 256 or the smaller ones, and splits of
+// its terms for CUs that the tiles leave without work, of at least eight
+// stages each.
+struct FfCut {
+  bool wide;
+  uint32_t splits;
+};
+FfCut cut_of(uint64_t m, uint64_t n, uint64_t outputs, uint64_t ktiles, int dt) {
+  if (dt == DT_F32) {
+    const uint64_t tiles = up_div(m, 64) * up_div(n, 64) * outputs;
+    return {false, (uint32_t)std::max<uint64_t>(1, std::min(4 * kCus / std::max<uint64_t>(tiles, 1), ktiles / 8))};
+  }
+  const uint64_t wide = up_div(m, 256) * up_div(n, 256) * outputs, small = up_div(m, 128) * up_div(n, 128) * outputs;
+  if (wide >= kCus) return {true, 1};
+  if (wide >= kCus / 4 && ktiles >= 64) return {true, (uint32_t)(kCus / wide)};
+  if (small >= kCus) return {false, 1};
+  return {false, (uint32_t)std::max<uint64_t>(1, std::min(kCus / std::max<uint64_t>(small, 1), ktiles / 8))};
 }
 uint64_t stage_terms(int dt) { return 128 / es_of(dt); }
-uint32_t dx_splits(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
-  return splits_of(rows, dim, 1, 2 * up_div(hidden, stage_terms(dt)));
+FfCut dx_cut(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
+  return cut_of(rows, dim, 1, 2 * up_div(hidden, stage_terms(dt)), dt);
 }
-uint32_t dw_splits(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
-  return splits_of(hidden, dim, 2, up_div(rows, stage_terms(dt)));
+FfCut dw_cut(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
+  return cut_of(hidden, dim, 2, up_div(rows, stage_terms(dt)), dt);
 }
 uint64_t partial_pitch(uint64_t n) { return up_div(n, 4) * 4; }
-
-void set_tiles(FfProduct& a, uint64_t tile_m, uint64_t tile_n, uint32_t splits) {
-  a.tiles_m = (uint32_t)up_div(a.m, tile_m);
-  a.tiles_n = (uint32_t)up_div(a.n, tile_n);
-  a.splits = splits;
-  a.per_split = (uint32_t)up_div(a.ktiles, splits);
-  // a split without work would leave its partial sums unwritten
-  if (a.per_split) a.splits = (uint32_t)up_div(a.ktiles, a.per_split);
-}
 
 template <class F>
 hipError_t by_type(int dt, F f) {
@@ -258,14 +294,22 @@ hipError_t by_type(int dt, F f) {
 
 }  // namespace
 
-uint64_t ff_tile_count(uint64_t m, uint64_t n) { return up_div(m, 128) * up_div(n, 64); }
+uint64_t ff_tile_count(uint64_t m, uint64_t n) { return up_div(m, 64) * up_div(n, 64); }
 
 FfWorkspace ff_workspace(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
+  const uint64_t es = es_of(dt);
+  auto room = [](uint64_t bytes) { return up_div(bytes, 256) * 256; };
   FfWorkspace w;
-  w.pitch = up_div(hidden, kCkptBlock) * kCkptBlock;
-  w.du = up_div(rows * w.pitch * es_of(dt), 256) * 256;
-  w.partials = 2 * w.du;
-  const uint64_t sx = dx_splits(rows, dim, hidden, dt), sw = dw_splits(rows, dim, hidden, dt);
+  w.pitch = blocks_pitch(hidden);
+  w.du = room(rows * w.pitch * es);
+  w.x = 2 * w.du;
+  // odd widths: aligned copies of x and the weights
+  const bool copies = rows && dim % (16 / es) != 0;
+  w.copy_pitch = copies ? blocks_pitch(dim) : 0;
+  w.wgate = w.x + room(rows * w.copy_pitch * es);
+  w.wup = w.wgate + room(hidden * w.copy_pitch * es);
+  w.partials = w.wup + room(hidden * w.copy_pitch * es);
+  const uint64_t sx = dx_cut(rows, dim, hidden, dt).splits, sw = dw_cut(rows, dim, hidden, dt).splits;
   const uint64_t bx = sx > 1 ? sx * rows : 0, bw = sw > 1 ? sw * 2 * hidden : 0;
   w.bytes = w.partials + std::max(bx, bw) * partial_pitch(dim) * sizeof(float);
   return w;
@@ -276,14 +320,14 @@ hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream) {
   FfProduct a{};
   a.p[0] = f.wgate.p;
   a.p[1] = f.wup.p;
-  a.pstride[0] = f.wgate.stride * es;
-  a.pstride[1] = f.wup.stride * es;
+  a.pstride[0] = (uint32_t)(f.wgate.stride * es);
+  a.pstride[1] = (uint32_t)(f.wup.stride * es);
   a.q[0] = a.q[1] = f.x.p;
-  a.qstride[0] = a.qstride[1] = f.x.stride * es;
+  a.qstride = (uint32_t)(f.x.stride * es);
   a.m = f.rows;
   a.n = f.hidden;
   a.k = f.dim;
-  a.ktiles = (uint32_t)up_div(f.dim, stage_terms(f.dt));
+  a.splits = 1;
   a.act = f.act;
   a.saved = f.saved;
   a.out[0] = f.h.p;
@@ -296,9 +340,8 @@ hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream) {
   if (f.rows <= kFewTokens && f.saved != 2)
     return by_type(f.dt, [&](auto t) { return few_dt<decltype(t)::value>(a, stream); });
   const bool direct = f.dim % (16 / es) == 0 && direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) &&
-                      direct_ok(a.q[0], a.qstride[0]);
+                      direct_ok(a.q[0], a.qstride);
   const bool wide = direct && f.dt != DT_F32 && up_div(f.rows, 256) * up_div(f.hidden, 128) >= kCus;
-  set_tiles(a, wide ? 256 : 128, wide ? 128 : 64, 1);
   return launch_ff_forward_tiles(f.dt, a, wide, direct, stream);
 }
 
@@ -306,40 +349,56 @@ hipError_t launch_gated_ff_grad(const FfBackward& b, hipStream_t stream) {
   const uint64_t es = es_of(b.dt);
   const FfWorkspace ws = ff_workspace(b.rows, b.dim, b.hidden, b.dt);
   hipError_t e = hipSuccess;
+  Rows x = b.x, wgate = b.wgate, wup = b.wup;
   if (b.rows) {
     e = by_type(b.dt, [&](auto t) { return act_grad_dt<decltype(t)::value>(b, stream); });
     if (e != hipSuccess) return e;
   }
+  if (ws.copy_pitch) {
+    FfCopy c{};
+    auto copy = [&](int i, Rows& m, uint64_t rows, uint64_t at) {
+      c.from[i] = m.p;
+      c.stride[i] = m.stride;
+      c.rows[i] = rows;
+      c.to[i] = b.ws + at;
+      m.p = c.to[i];
+      m.stride = ws.copy_pitch;
+    };
+    if (b.dwgate.p) copy(0, x, b.rows, ws.x);
+    if (b.dx.p) {
+      copy(1, wgate, b.hidden, ws.wgate);
+      copy(2, wup, b.hidden, ws.wup);
+    }
+    e = by_type(b.dt, [&](auto t) { return copy_dt<decltype(t)::value>(c, b.dim, stream); });
+    if (e != hipSuccess) return e;
+  }
   auto product = [&](bool dx) {
     FfProduct a{};
-    a.q[0] = b.dg;
-    a.q[1] = b.du;
-    a.qstride[0] = a.qstride[1] = ws.pitch * es;
-    a.partials = b.partials;
+    a.q[0] = b.ws;
+    a.q[1] = b.ws + ws.du;
+    a.qstride = (uint32_t)(ws.pitch * es);
+    a.partials = (float*)(b.ws + ws.partials);
     a.pitch = partial_pitch(b.dim);
     a.n = b.dim;
+    FfCut cut;
     bool direct;
-    uint32_t splits;
     if (dx) {
-      a.p[0] = b.wgate.p;
-      a.p[1] = b.wup.p;
-      a.pstride[0] = b.wgate.stride * es;
-      a.pstride[1] = b.wup.stride * es;
+      a.p[0] = wgate.p;
+      a.p[1] = wup.p;
+      a.pstride[0] = (uint32_t)(wgate.stride * es);
+      a.pstride[1] = (uint32_t)(wup.stride * es);
       a.m = b.rows;
       a.k = b.hidden;
-      a.ktiles = 2 * (uint32_t)up_div(a.k, stage_terms(b.dt));
       a.out[0] = b.dx.p;
       a.out_stride[0] = b.dx.stride * es;
       a.out_dt = b.dt;
-      // one set of offsets serves both segments
-      direct = direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) && a.pstride[0] == a.pstride[1];
-      splits = dx_splits(b.rows, b.dim, b.hidden, b.dt);
+      cut = dx_cut(b.rows, b.dim, b.hidden, b.dt);
+      direct = direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]);
     } else {
-      a.p[0] = a.p[1] = b.x.p;
-      a.pstride[0] = a.pstride[1] = b.x.stride * es;
+      a.p[0] = a.p[1] = x.p;
+      a.pstride[0] = a.pstride[1] = (uint32_t)(x.stride * es);
       a.m = b.hidden;
       a.k = b.rows;
-      a.ktiles = (uint32_t)up_div(a.k, stage_terms(b.dt));
       const uint64_t oes = es_of(b.wdt);
       a.out[0] = b.dwgate.p;
       a.out[1] = b.dwup.p;
@@ -347,17 +406,18 @@ hipError_t launch_gated_ff_grad(const FfBackward& b, hipStream_t stream) {
       a.out_stride[1] = b.dwup.stride * oes;
       a.out_dt = b.wdt;
       a.accumulate = b.accumulate;
+      cut = dw_cut(b.rows, b.dim, b.hidden, b.dt);
       direct = direct_ok(a.p[0], a.pstride[0]);
-      splits = dw_splits(b.rows, b.dim, b.hidden, b.dt);
     }
-    direct = direct && ws.pitch * es <= (1u << 22);
-    const int outputs = dx ? 1 : 2;
-    const bool wide =
-        direct && b.dt != DT_F32 && splits == 1 && up_div(a.m, 256) * up_div(a.n, 256) * outputs >= kCus;
-    set_tiles(a, wide ? 256 : 128, wide ? 256 : 128, splits);
-    hipError_t r = dx ? launch_ff_dx(b.dt, a, wide, direct, stream) : launch_ff_dw(b.dt, a, wide, direct, stream);
-    if (r != hipSuccess || a.splits == 1) return r;
-    return by_type(b.dt, [&](auto t) { return join_dt<decltype(t)::value>(a, outputs, stream); });
+    hipError_t r = hipSuccess;
+    if (a.k) {
+      a.splits = cut.splits;
+      r = dx ? launch_ff_dx(b.dt, a, cut.wide && direct, direct, stream)
+             : launch_ff_dw(b.dt, a, cut.wide && direct, direct, stream);
+      if (r != hipSuccess || a.splits == 1) return r;
+    }
+    // without rows the weights' gradients are sums of nothing
+    return by_type(b.dt, [&](auto t) { return join_dt<decltype(t)::value>(a, dx ? 1 : 2, stream); });
   };
   if (b.dx.p && b.rows) e = product(true);
   if (e == hipSuccess && b.dwgate.p) e = product(false);

@@ -197,8 +197,10 @@ __device__ __forceinline__ void checkpoint_row(const RowShape<DT, NT, V>& sh, co
   const uint32_t whole = (uint32_t)(sh.ntail ? dim / kCkptBlock : (dim + kCkptBlock - 1) / kCkptBlock) * kCkptBlock;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const uint32_t m = group_max_u32<kCkptBlock / E>(sh.valid(j) ? vec_absmax(v.v[j]) : 0u);
-    if (live && sh.col(j) < whole) ckpt_store<E>(codes, exps, sh.col(j), m, v.v[j]);
+    const uint32_t m = group_max_u32<kCkptBlock / E>(vec_absmax(v.v[j]));
+    uint32_t col = sh.col(j);
+    asm volatile("" : "+v"(col));  // compared anew for each row: the masks of all vectors take too many registers
+    if (live && col < whole) ckpt_store<E>(codes, exps, col, m, v.v[j]);
   }
   if (sh.ntail) {  // uniform
     const uint32_t c = whole + sh.lane;

@@ -541,8 +541,10 @@ int rar_layernorm_backward_checkpoint(const void* dy, size_t dy_stride, const vo
 
 namespace {
 
-constexpr size_t kFfMaxCols = (size_t)1 << 26, kFfMaxRows = (size_t)1 << 30;
-constexpr uint64_t kFfMaxTiles = (uint64_t)1 << 22;  // of 512 lanes, for two outputs
+constexpr size_t kFfMaxCols = (size_t)1 << 20, kFfMaxRows = (size_t)1 << 30;
+// The products address an operand's rows in a tile by 31 bits.
+constexpr size_t kFfMaxStep = (size_t)1 << 22;
+constexpr uint64_t kFfMaxTiles = (uint64_t)1 << 24;  // numbered in 32 bits, with outputs and splits
 
 int ff_sizes(size_t rows, size_t dim, size_t hidden, int dtype) {
   if (!dt_ok(dtype)) return RAR_EDTYPE;
@@ -575,10 +577,12 @@ bool ff_modes_ok(int act, int saved) {
          (saved == RAR_KEEP_NONE || saved == RAR_KEEP_ROWS || saved == RAR_KEEP_CHECKPOINT);
 }
 
-// A matrix of rows as a range, with its checks.
-int ff_matrix(const void* p, size_t stride, size_t rows, size_t cols, size_t es, bool written, Range* r) {
+// A matrix of rows as a range, with its checks; operand: of a product.
+int ff_matrix(const void* p, size_t stride, size_t rows, size_t cols, size_t es, bool written, Range* r,
+              bool operand = false) {
   size_t bytes;
   if ((written && stride < cols) || !rows_bytes(rows, cols, stride, es, &bytes)) return RAR_EINVAL;
+  if (operand && rows > 1 && stride * es > kFfMaxStep) return RAR_ENOTSUP;
   *r = Range{(uintptr_t)p, bytes, written, 0, stride * es, cols * es};
   return rows ? check_ptr(p, es) : RAR_OK;
 }
@@ -594,9 +598,9 @@ int rar_gated_ff_forward(const void* x, size_t x_stride, const void* wgate, size
   if (!ff_modes_ok(act, keep)) return RAR_EINVAL;
   const size_t es = es_of(dtype);
   Range r[6];
-  if ((rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[0])) ||
-      (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[1])) ||
-      (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[2])) ||
+  if ((rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[0], true)) ||
+      (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[1], true)) ||
+      (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[2], true)) ||
       (rc = ff_matrix(h, h_stride, rows, hidden, es, true, &r[3])) ||
       (rc = ff_kept(gate, gate_stride, keep, rows, hidden, es, true, &r[4])) ||
       (rc = ff_kept(up, up_stride, keep, rows, hidden, es, true, &r[5])))
@@ -604,9 +608,9 @@ int rar_gated_ff_forward(const void* x, size_t x_stride, const void* wgate, size
   if (rows == 0) return RAR_OK;
   if ((rc = check_ranges(r, 6))) return rc;
   FfForward f{};
-  f.x = Rows{(char*)x, x_stride, dtype};
-  f.wgate = Rows{(char*)wgate, wgate_stride, dtype};
-  f.wup = Rows{(char*)wup, wup_stride, dtype};
+  f.x = Rows{(char*)x, rows > 1 ? x_stride : dim, dtype};
+  f.wgate = Rows{(char*)wgate, hidden > 1 ? wgate_stride : dim, dtype};
+  f.wup = Rows{(char*)wup, hidden > 1 ? wup_stride : dim, dtype};
   f.h = Rows{(char*)h, h_stride, dtype};
   f.gate = Rows{(char*)gate, gate_stride, dtype};
   f.up = Rows{(char*)up, up_stride, dtype};
@@ -640,9 +644,9 @@ int rar_gated_ff_backward(const void* dh, size_t dh_stride, const void* x, size_
   const size_t es = es_of(dtype), we = es_of(dweight_dtype);
   Range r[10];
   if ((rc = ff_matrix(dh, dh_stride, rows, hidden, es, false, &r[0])) ||
-      (rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[1])) ||
-      (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[2])) ||
-      (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[3])) ||
+      (rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[1], true)) ||
+      (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[2], true)) ||
+      (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[3], true)) ||
       (rc = ff_kept(gate, gate_stride, keep, rows, hidden, es, false, &r[4])) ||
       (rc = ff_kept(up, up_stride, keep, rows, hidden, es, false, &r[5])) ||
       (rc = ff_matrix(dx, dx_stride, dx ? rows : 0, dim, es, true, &r[6])) ||
@@ -658,9 +662,9 @@ int rar_gated_ff_backward(const void* dh, size_t dh_stride, const void* x, size_
   if (rows == 0 && (!dwgate || accumulate)) return RAR_OK;
   FfBackward b{};
   b.dh = Rows{(char*)dh, dh_stride, dtype};
-  b.x = Rows{(char*)x, x_stride, dtype};
-  b.wgate = Rows{(char*)wgate, wgate_stride, dtype};
-  b.wup = Rows{(char*)wup, wup_stride, dtype};
+  b.x = Rows{(char*)x, rows > 1 ? x_stride : dim, dtype};
+  b.wgate = Rows{(char*)wgate, hidden > 1 ? wgate_stride : dim, dtype};
+  b.wup = Rows{(char*)wup, hidden > 1 ? wup_stride : dim, dtype};
   b.gate = Rows{(char*)gate, gate_stride, dtype};
   b.up = Rows{(char*)up, up_stride, dtype};
   if (keep == RAR_KEEP_CHECKPOINT) {
@@ -670,9 +674,7 @@ int rar_gated_ff_backward(const void* dh, size_t dh_stride, const void* x, size_
   b.dx = Rows{(char*)dx, dx_stride, dtype};
   b.dwgate = Rows{(char*)dwgate, dwgate_stride, dweight_dtype};
   b.dwup = Rows{(char*)dwup, dwup_stride, dweight_dtype};
-  b.dg = (char*)workspace;
-  b.du = (char*)workspace + l.du;
-  b.partials = (float*)((char*)workspace + l.partials);
+  b.ws = (char*)workspace;
   b.rows = rows;
   b.dim = dim;
   b.hidden = hidden;

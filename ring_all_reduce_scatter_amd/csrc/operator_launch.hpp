@@ -115,17 +115,17 @@ struct FfForward {
 };
 hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream);
 
-// Workspace of the backward pass: dg, du (rows x pitch elements each), then
-// the partial sums of split products.
+// Workspace of the backward pass: dg, du (rows x pitch elements each), copies
+// of x and the weights (rows of copy_pitch; 0: none), then the partial sums of
+// split products.
 struct FfWorkspace {
-  uint64_t pitch, du, partials, bytes;
+  uint64_t pitch, du, x, copy_pitch, wgate, wup, partials, bytes;
 };
 FfWorkspace ff_workspace(uint64_t rows, uint64_t dim, uint64_t hidden, int dt);
 struct FfBackward {
   Rows dh, x, wgate, wup, gate, up, dx, dwgate, dwup;
   Checkpoint cgate, cup;
-  char *dg, *du;
-  float* partials;
+  char* ws;
   uint64_t rows, dim, hidden;
   int dt, wdt, act, saved;
   bool accumulate;

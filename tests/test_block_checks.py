@@ -164,10 +164,12 @@ def test_gated_ff_forward_c_refusals():
     f = _forward
     assert f(dt=3) == EDTYPE and f(act=3) == EINVAL and f(act=-1) == EINVAL and f(keep=3) == EINVAL
     assert f(dim=0) == EINVAL and f(hidden=0) == EINVAL
-    big = dict(xs=1 << 27, wgs=1 << 27, wus=1 << 27, hs=1 << 27, gs=1 << 27, us=1 << 27)
-    assert f(dim=(1 << 26) + 1, **big) == ENOTSUP and f(hidden=(1 << 26) + 1, **big) == ENOTSUP
+    big = dict(xs=1 << 21, wgs=1 << 21, wus=1 << 21, hs=1 << 21, gs=1 << 21, us=1 << 21)
+    assert f(dim=(1 << 20) + 1, **big) == ENOTSUP and f(hidden=(1 << 20) + 1, **big) == ENOTSUP
+    for name in ("xs", "wgs", "wus"):
+        assert f(**{name: (1 << 21) + 1}) == ENOTSUP and f(dt=0, **{name: (1 << 20) + 1}) == ENOTSUP
     assert f(rows=(1 << 30) + 1) == ENOTSUP
-    assert f(rows=1 << 22, hidden=1 << 20, hs=1 << 20, gs=1 << 20, us=1 << 20) == ENOTSUP
+    assert f(rows=1 << 20, hidden=1 << 20, hs=1 << 20, gs=1 << 20, us=1 << 20) == ENOTSUP
     assert f(hs=79) == EINVAL and f(gs=79) == EINVAL and f(us=79) == EINVAL
     assert f(xs=1 << 50) == EINVAL and f(wus=1 << 50) == EINVAL
     for name in ("x", "wg", "wu", "h", "g", "u"):
@@ -188,6 +190,8 @@ def test_gated_ff_backward_c_refusals():
     f = _backward
     assert f(dt=3) == EDTYPE and f(act=3) == EINVAL and f(keep=0) == EINVAL and f(wdt=1) == EDTYPE
     assert f(dim=0) == EINVAL and f(hidden=0) == EINVAL and f(rows=(1 << 30) + 1) == ENOTSUP
+    for name in ("xs", "wgs", "wus"):
+        assert f(**{name: (1 << 21) + 1}) == ENOTSUP
     assert f(dg=0) == EINVAL and f(du=0) == EINVAL
     assert f(dxs=47) == EINVAL and f(dgs=47) == EINVAL and f(dus=47) == EINVAL
     for name in ("dh", "x", "wg", "wu", "g", "u"):
