@@ -614,6 +614,10 @@ unsigned row_grid(uint64_t rows) { return (unsigned)(rows < 65536 ? rows : 65536
 // row of 2 * dim floats, as far as there are rows for its slots.
 constexpr uint64_t kGradGroups = 256;
 constexpr uint64_t kFewRows = 512, kFewBytes = 2 << 20;
+// From a checkpoint fewer: its bytes come from memory, and a column's rows wait
+// for one another (forward and backward of 512 x 1024 bf16 34 us by columns, 20
+// with partial rows; 128 x 512 f32 17.6 and 20.6).
+constexpr uint64_t kFewHeldRows = 128;
 uint64_t grad_groups(uint64_t rows, int rb) { return std::min<uint64_t>(kGradGroups, (rows + rb - 1) / rb); }
 
 template <int DT, int NT, int V, int RB, bool CK>
@@ -684,7 +688,7 @@ hipError_t backward_rows(const LayernormGrad& a, uint64_t rows, uint64_t dim, hi
                        dim3(NT * RB), std::max(lds, column_lds), stream, a, rows, dim, (uint32_t)row_groups, partial);
     return launch_status(stream);
   };
-  if (rows > kFewRows || rows * dim * DtypeSize<DT>::value > kFewBytes || !sums) {
+  if (rows > (CK ? kFewHeldRows : kFewRows) || rows * dim * DtypeSize<DT>::value > kFewBytes || !sums) {
     const hipError_t e = launch(groups, 0, sums);
     return e != hipSuccess ? e : join_partials(a, groups, dim, stream);
   }
