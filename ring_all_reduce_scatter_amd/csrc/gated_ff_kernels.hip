@@ -13,29 +13,7 @@ typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
 
 // ------------------------------------------------------------------ few tokens
 
-// Forward for at most 64 tokens: the weights' bytes are all that counts, and
-// they go from memory straight into the matrix instructions.  A workgroup has
-// 16 hidden columns, NT blocks of 16 tokens, and its 8 wavefronts share the
-// terms: pairs of 64-byte pieces of a row in turn, so that the loads of a
-// wavefront cover whole lines and all of them are on their way at once.  The
-// wavefronts' sums are added through LDS in order.
-constexpr int kFewWaves = 8;
-
-template <int DT>
-__device__ __forceinline__ f32x4 few_mfma(u32x4 w, u32x4 x, f32x4 c) {
-  if constexpr (DT == DT_BF16) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, w), __builtin_bit_cast(b16x8, x), c, 0, 0,
-                                                   0);
-  } else if constexpr (DT == DT_F16) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, w), __builtin_bit_cast(h16x8, x), c, 0, 0,
-                                                  0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i]), __uint_as_float(x[i]), c, 0, 0, 0);
-    return c;
-  }
-}
+// Forward for at most 64 tokens: the weights' bytes are all that counts.
 
 // A 16-byte chunk of a row from element e on; elements past dim are zeros.
 template <int DT>
@@ -53,72 +31,221 @@ __device__ __forceinline__ u32x4 few_chunk(const char* row, uint64_t e, uint64_t
   return x;
 }
 
-template <int DT, int NT>
-__global__ __launch_bounds__(kFewWaves * 64) void ff_few_kernel(FfProduct a) {
-  constexpr int ES = DtypeSize<DT>::value, EC = 16 / ES;
-  extern __shared__ float sums[];  // [wavefront][2 NT][256]
-  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t r = lane & 15, quad = lane >> 4;
-  const uint64_t c0 = (uint64_t)blockIdx.x * 16;
-  // columns and tokens past the last read the last one's row; what comes of
-  // them is not stored
-  const uint64_t c = c0 + r < a.n ? c0 + r : a.n - 1;
-  const char *wg = a.p[0] + c * a.pstride[0], *wu = a.p[1] + c * a.pstride[1];
-  const char* x[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = a.q[0] + (t * 16 + r < a.m ? t * 16 + r : a.m - 1) * a.qstride;
-  f32x4 g[NT], u[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) g[t] = u[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  const uint64_t pairs = (a.k + 8 * EC - 1) / (8 * EC);  // 128 bytes of a row
-#pragma unroll 4
-  for (uint64_t k = wave; k < pairs; k += kFewWaves) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const uint64_t e = (k * 8 + s * 4 + quad) * EC;
-      const u32x4 pg = few_chunk<DT>(wg, e, a.k), pu = few_chunk<DT>(wu, e, a.k);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const u32x4 q = few_chunk<DT>(x[t], e, a.k);
-        g[t] = few_mfma<DT>(pg, q, g[t]);
-        u[t] = few_mfma<DT>(pu, q, u[t]);
-      }
-    }
+// One element of h and, if asked for, of the projections, from its two sums.
+template <int DT>
+__device__ __forceinline__ void few_store(const FfProduct& a, uint64_t token, uint64_t col, float g, float u) {
+  constexpr int ES = DtypeSize<DT>::value;
+  if (a.saved == 1) {
+    store_elem<DT>(a.gate.p + token * a.gate.stride * ES, col, g);
+    store_elem<DT>(a.up.p + token * a.up.stride * ES, col, u);
   }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sums[(wave * 2 * NT + t) * 256 + r * 16 + quad * 4 + i] = g[t][i];
-      sums[(wave * 2 * NT + NT + t) * 256 + r * 16 + quad * 4 + i] = u[t][i];
-    }
-  __syncthreads();
-  for (uint32_t o = threadIdx.x; o < NT * 256; o += kFewWaves * 64) {
-    float vg = 0.0f, vu = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) {
-      vg += sums[w * 2 * NT * 256 + o];
-      vu += sums[(w * 2 * NT + NT) * 256 + o];
-    }
-    const uint64_t token = o / 16, col = c0 + o % 16;
-    if (token >= a.m || col >= a.n) continue;
-    if (a.saved == 1) {
-      store_elem<DT>(a.gate.p + token * a.gate.stride * ES, col, vg);
-      store_elem<DT>(a.up.p + token * a.up.stride * ES, col, vu);
-    }
-    store_elem<DT>(a.out[0] + token * a.out_stride[0], col, ff_act<false>(vg, a.act, nullptr) * vu);
-  }
+  store_elem<DT>(a.out[0] + token * a.out_stride[0], col, ff_act<false>(g, a.act, nullptr) * u);
 }
 
 template <int DT>
-hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.n + 15) / 16)), block(kFewWaves * 64);
-  const int nt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
-  const size_t lds = (size_t)kFewWaves * 2 * nt * 256 * sizeof(float);
-  if (nt == 1) hipLaunchKernelGGL((ff_few_kernel<DT, 1>), grid, block, lds, stream, a);
-  else if (nt == 2) hipLaunchKernelGGL((ff_few_kernel<DT, 2>), grid, block, lds, stream, a);
-  else hipLaunchKernelGGL((ff_few_kernel<DT, 4>), grid, block, lds, stream, a);
+__device__ __forceinline__ f32x4 few_mfma(u32x4 w, u32x4 x, f32x4 c) {
+  if constexpr (DT == DT_BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, w), __builtin_bit_cast(b16x8, x), c, 0, 0,
+                                                   0);
+  } else if constexpr (DT == DT_F16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, w), __builtin_bit_cast(h16x8, x), c, 0, 0,
+                                                  0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i]), __uint_as_float(x[i]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// On the matrix units, straight from memory.  A workgroup has NR blocks of 16
+// hidden columns and NT blocks of 16 tokens, and its W wavefronts share the
+// terms: 128-byte pieces of a row in turn, PIECES of them on their way at once.
+// The wavefronts' sums are added through LDS in order.  An instruction's 16 rows
+// take halves of each 128-byte line, the next instruction the others, so these
+// loads must not be streaming ones (43 us for one token, 38 with these).
+template <int DT, int NT, int NR, int W, int PIECES>
+__global__ __launch_bounds__(W * 64) void ff_few_kernel(FfProduct a) {
+  constexpr int ES = DtypeSize<DT>::value, EC = 16 / ES;
+  extern __shared__ float sums[];  // [wavefront][gate, up][NR][NT][256]
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = lane & 15, quad = lane >> 4;
+  const uint64_t c0 = (uint64_t)blockIdx.x * (16 * NR);
+  // columns and tokens past the last read the last one's row; what comes of
+  // them is not stored
+  const char *w[2][NR], *x[NT];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const uint64_t c = c0 + n * 16 + r < a.n ? c0 + n * 16 + r : a.n - 1;
+    w[0][n] = a.p[0] + c * a.pstride[0];
+    w[1][n] = a.p[1] + c * a.pstride[1];
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    x[t] = a.q[0] + (uint64_t)(t * 16 + r < a.m ? t * 16 + r : a.m - 1) * a.qstride;
+  f32x4 acc[2][NR][NT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[h][n][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  // a piece is 128 bytes of a row, two steps of four chunks
+  const uint32_t whole = (uint32_t)(a.k / (8 * EC)), pieces = (uint32_t)((a.k + 8 * EC - 1) / (8 * EC));
+  uint32_t k = wave;
+  for (; k + W * (PIECES - 1) < whole; k += W * PIECES) {
+    u32x4 pw[PIECES][2][2][NR], px[PIECES][2][NT];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t at = (k + i * W) * 128 + quad * 32 + s * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < NR; ++n) pw[i][s][h][n] = *(const u32x4_any*)(w[h][n] + at);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) px[i][s][t] = *(const u32x4_any*)(x[t] + at);
+      }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[h][n][t] = few_mfma<DT>(pw[i][s][h][n], px[i][s][t], acc[h][n][t]);
+  }
+  for (; k < pieces; k += W)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint64_t e = ((uint64_t)k * 8 + quad * 2 + s) * EC;
+      u32x4 q[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) q[t] = few_chunk<DT>(x[t], e, a.k);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const u32x4 p = few_chunk<DT>(w[h][n], e, a.k);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[h][n][t] = few_mfma<DT>(p, q[t], acc[h][n][t]);
+        }
+    }
+  constexpr uint32_t kPlane = NR * NT * 256;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sums[(wave * 2 + h) * kPlane + (t * 16 + r) * (16 * NR) + n * 16 + quad * 4 + i] = acc[h][n][t][i];
+  __syncthreads();
+  for (uint32_t o = threadIdx.x; o < kPlane; o += W * 64) {
+    float vg = 0.0f, vu = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      vg += sums[i * 2 * kPlane + o];
+      vu += sums[(i * 2 + 1) * kPlane + o];
+    }
+    const uint64_t token = o / (16 * NR), col = c0 + o % (16 * NR);
+    if (token >= a.m || col >= a.n) continue;
+    few_store<DT>(a, token, col, vg, vu);
+  }
+}
+
+template <int DT, int NT, int NR, int W, int PIECES>
+hipError_t few_launch(const FfProduct& a, hipStream_t stream) {
+  hipLaunchKernelGGL((ff_few_kernel<DT, NT, NR, W, PIECES>), dim3((unsigned)((a.n + 16 * NR - 1) / (16 * NR))),
+                     dim3(W * 64), W * 2 * NR * NT * 256 * sizeof(float), stream, a);
   return launch_status(stream);
+}
+
+// Forward for one or two tokens, on the vector units: a row of a weight is read
+// as 1 KiB an instruction, the pattern that reaches the rate of a copy, and each
+// lane multiplies what it loaded.  A wavefront has one hidden column, which it
+// finishes alone.  Two columns a wavefront share what is read of x and were
+// slower (30.5 and 28.5 us): half as many wavefronts take turns waiting.  The
+// weights' loads are streaming ones; lines of x stay.
+constexpr int kVectorSteps = 4;  // instructions a row on their way; 8 measured the same
+
+template <int DT, int T>
+__global__ __launch_bounds__(kThreads) void ff_vector_kernel(FfProduct a) {
+  constexpr int EC = 16 / DtypeSize<DT>::value, U = kVectorSteps;
+  using Raw = VecRaw<DT, EC>;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t col = (uint64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (col >= a.n) return;
+  const char* const w[2] = {a.p[0] + col * a.pstride[0], a.p[1] + col * a.pstride[1]};
+  float sum[2][T] = {};
+  auto add = [&](const u32x4 (&pw)[2], const u32x4 (&px)[T]) __attribute__((always_inline)) {
+    const VecF<EC> g = unpack<DT, EC>(__builtin_bit_cast(Raw, pw[0])), u = unpack<DT, EC>(__builtin_bit_cast(Raw, pw[1]));
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const VecF<EC> x = unpack<DT, EC>(__builtin_bit_cast(Raw, px[t]));
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        sum[0][t] = __builtin_fmaf(g.v[e], x.v[e], sum[0][t]);
+        sum[1][t] = __builtin_fmaf(u.v[e], x.v[e], sum[1][t]);
+      }
+    }
+  };
+  const uint32_t whole = (uint32_t)(a.k / (64 * EC)), steps = (uint32_t)((a.k + 64 * EC - 1) / (64 * EC));
+  uint32_t k = 0;
+  for (; k + U <= whole; k += U) {
+    u32x4 pw[U][2], px[U][T];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t at = ((k + i) * 64 + lane) * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pw[i][h] = __builtin_nontemporal_load((const u32x4_any*)(w[h] + at));
+#pragma unroll
+      for (int t = 0; t < T; ++t) px[i][t] = *(const u32x4_any*)(a.q[0] + (uint64_t)t * a.qstride + at);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) add(pw[i], px[i]);
+  }
+  for (; k < steps; ++k) {
+    const uint64_t e = ((uint64_t)k * 64 + lane) * EC;
+    u32x4 pw[2], px[T];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) pw[h] = few_chunk<DT>(w[h], e, a.k);
+#pragma unroll
+    for (int t = 0; t < T; ++t) px[t] = few_chunk<DT>(a.q[0] + (uint64_t)t * a.qstride, e, a.k);
+    add(pw, px);
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const float g = wave_sum(sum[0][t]), u = wave_sum(sum[1][t]);
+    if (lane == 0) few_store<DT>(a, t, col, g, u);
+  }
+}
+
+template <int DT, int T>
+hipError_t vector_launch(const FfProduct& a, hipStream_t stream) {
+  constexpr uint64_t wg = kThreads / 64;
+  hipLaunchKernelGGL((ff_vector_kernel<DT, T>), dim3((unsigned)((a.n + wg - 1) / wg)), dim3(kThreads), 0, stream, a);
+  return launch_status(stream);
+}
+
+// One and two tokens go to the vector units: 28.3 and 30.9 us at 4096 x 11264
+// bfloat16 (184 MB, 29 us at the rate of a large copy), the matrix kernel 38 for
+// both; at four tokens the rows of x cost as much as that saves (37 to 41, and 39).
+// The matrix kernel's shapes, us at 4096 x 11264: 16 tokens 47, as with half the
+// pieces or half the wavefronts; 24 tokens 53, and 61 with two blocks of columns;
+// 64 tokens 67, and 78 to 83 with one block of columns, where x is read twice as
+// often.
+template <int DT>
+hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
+  if (a.m == 1) return vector_launch<DT, 1>(a, stream);
+  if (a.m == 2) return vector_launch<DT, 2>(a, stream);
+  if (a.m <= 16) return few_launch<DT, 1, 1, 8, 4>(a, stream);
+  if (a.m <= 32) return few_launch<DT, 2, 1, 8, 2>(a, stream);
+  return few_launch<DT, 4, 2, 4, 1>(a, stream);
 }
 
 // ------------------------------------------------------------------ gradients of the product

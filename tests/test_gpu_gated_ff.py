@@ -91,7 +91,8 @@ def _check_all(x, wg, wu, dh, kind, wdt):
 
 SHAPES = [(1, 1, 1), (1, 8, 32), (2, 3, 5), (1, 128, 96), (16, 64, 64), (17, 100, 33), (31, 200, 70), (64, 64, 130),
           (65, 64, 130), (70, 129, 67), (128, 256, 128), (129, 264, 200), (200, 1001, 77), (3, 1000, 1000),
-          (300, 40, 520), (513, 72, 96), (5, 520, 1100), (1, 4099, 45)]
+          (300, 40, 520), (513, 72, 96), (5, 520, 1100), (1, 4099, 45), (2, 2565, 67), (3, 4099, 33),
+          (31, 4099, 20)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
