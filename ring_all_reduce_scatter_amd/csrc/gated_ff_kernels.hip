@@ -58,13 +58,12 @@ __device__ __forceinline__ f32x4 few_mfma(u32x4 w, u32x4 x, f32x4 c) {
   }
 }
 
-// On the matrix units, straight from memory.  A workgroup has NR blocks of 16
-// hidden columns and NT blocks of 16 tokens, and its W wavefronts share the
-// terms: 128-byte pieces of a row in turn, PIECES of them on their way at once.
-// The wavefronts' sums are added through LDS in order.  An instruction's 16 rows
-// take halves of each 128-byte line, the next instruction the others, so these
-// loads must not be streaming ones (43 us for one token, 38 with these).
-template <int DT, int NT, int NR, int W, int PIECES>
+// On the matrix units, straight from memory.  A workgroup has NR blocks of
+// 16 hidden columns and NT blocks of 16 tokens, and its W wavefronts share the terms, 128-byte pieces of a row in turn; their sums are added through
+// LDS in order.  An instruction's 16 rows take halves of each 128-byte line, the
+// next instruction the others, so these loads must not be streaming ones (72 us
+// for 64 tokens, 67 with these).
+template <int DT, int NT, int NR, int W>
 __global__ __launch_bounds__(W * 64) void ff_few_kernel(FfProduct a) {
   constexpr int ES = DtypeSize<DT>::value, EC = 16 / ES;
   extern __shared__ float sums[];  // [wavefront][gate, up][NR][NT][256]
@@ -93,30 +92,26 @@ __global__ __launch_bounds__(W * 64) void ff_few_kernel(FfProduct a) {
   // a piece is 128 bytes of a row, two steps of four chunks
   const uint32_t whole = (uint32_t)(a.k / (8 * EC)), pieces = (uint32_t)((a.k + 8 * EC - 1) / (8 * EC));
   uint32_t k = wave;
-  for (; k + W * (PIECES - 1) < whole; k += W * PIECES) {
-    u32x4 pw[PIECES][2][2][NR], px[PIECES][2][NT];
+  for (; k < whole; k += W) {
+    u32x4 pw[2][2][NR], px[2][NT];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t at = k * 128 + quad * 32 + s * 16;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t at = (k + i * W) * 128 + quad * 32 + s * 16;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int n = 0; n < NR; ++n) pw[s][h][n] = *(const u32x4_any*)(w[h][n] + at);
 #pragma unroll
-          for (int n = 0; n < NR; ++n) pw[i][s][h][n] = *(const u32x4_any*)(w[h][n] + at);
+      for (int t = 0; t < NT; ++t) px[s][t] = *(const u32x4_any*)(x[t] + at);
+    }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) px[i][s][t] = *(const u32x4_any*)(x[t] + at);
-      }
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[h][n][t] = few_mfma<DT>(pw[i][s][h][n], px[i][s][t], acc[h][n][t]);
+          for (int t = 0; t < NT; ++t) acc[h][n][t] = few_mfma<DT>(pw[s][h][n], px[s][t], acc[h][n][t]);
   }
   for (; k < pieces; k += W)
 #pragma unroll
@@ -158,10 +153,121 @@ __global__ __launch_bounds__(W * 64) void ff_few_kernel(FfProduct a) {
   }
 }
 
-template <int DT, int NT, int NR, int W, int PIECES>
+template <int DT, int NT, int NR, int W>
 hipError_t few_launch(const FfProduct& a, hipStream_t stream) {
-  hipLaunchKernelGGL((ff_few_kernel<DT, NT, NR, W, PIECES>), dim3((unsigned)((a.n + 16 * NR - 1) / (16 * NR))),
+  hipLaunchKernelGGL((ff_few_kernel<DT, NT, NR, W>), dim3((unsigned)((a.n + 16 * NR - 1) / (16 * NR))),
                      dim3(W * 64), W * 2 * NR * NT * 256 * sizeof(float), stream, a);
+  return launch_status(stream);
+}
+
+// The same for at most 32 tokens, with whole lines an instruction: its 16 rows
+// are two halves of 8 columns, so that 8 lanes have the 128 bytes of a column's
+// piece, each lane the chunk 2 quad + half.  A matrix instruction with the even
+// chunks of x is then right for the first half's rows, one with the odd chunks
+// for the second's, and the others are never stored: twice the products, which
+// have time, for streaming loads of whole lines.  16 tokens of 4096 x 11264
+// bfloat16 take 37.6 us, 24 44, the kernel above 47 and 53; 64 tokens have no
+// registers left for it (86 to 104 us, 67 above).
+template <int DT, int NT, int W, int PIECES>
+__global__ __launch_bounds__(W * 64) void ff_lines_kernel(FfProduct a) {
+  constexpr int ES = DtypeSize<DT>::value, EC = 16 / ES;
+  extern __shared__ float sums[];  // [wavefront][gate, up][2][NT][16][16]
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = lane & 15, quad = lane >> 4;
+  const uint64_t c0 = (uint64_t)blockIdx.x * 16;
+  const char *w[2][2], *x[NT];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const uint64_t c = c0 + n * 8 + (r & 7) < a.n ? c0 + n * 8 + (r & 7) : a.n - 1;
+    w[0][n] = a.p[0] + c * a.pstride[0];
+    w[1][n] = a.p[1] + c * a.pstride[1];
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    x[t] = a.q[0] + (uint64_t)(t * 16 + r < a.m ? t * 16 + r : a.m - 1) * a.qstride;
+  f32x4 acc[2][2][2][NT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[h][n][s][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t wq = quad * 2 + (r >> 3);
+  const uint32_t whole = (uint32_t)(a.k / (8 * EC)), pieces = (uint32_t)((a.k + 8 * EC - 1) / (8 * EC));
+  uint32_t k = wave;
+  for (; k + W * (PIECES - 1) < whole; k += W * PIECES) {
+    u32x4 pw[PIECES][2][2], px[PIECES][2][NT];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const uint32_t at = (k + i * W) * 128;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) pw[i][h][n] = __builtin_nontemporal_load((const u32x4_any*)(w[h][n] + (at + wq * 16)));
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) px[i][s][t] = *(const u32x4_any*)(x[t] + (at + quad * 32 + s * 16));
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[h][n][s][t] = few_mfma<DT>(pw[i][h][n], px[i][s][t], acc[h][n][s][t]);
+  }
+  for (; k < pieces; k += W) {
+    u32x4 q[2][NT];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) q[s][t] = few_chunk<DT>(x[t], ((uint64_t)k * 8 + quad * 2 + s) * EC, a.k);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const u32x4 p = few_chunk<DT>(w[h][n], ((uint64_t)k * 8 + wq) * EC, a.k);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[h][n][s][t] = few_mfma<DT>(p, q[s][t], acc[h][n][s][t]);
+      }
+  }
+  constexpr uint32_t kPlane = NT * 512;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sums[(wave * 2 + h) * kPlane + (quad >> 1) * (NT * 256) + (t * 16 + r) * 16 + n * 8 + (quad & 1) * 4 + i] =
+              quad < 2 ? acc[h][n][0][t][i] : acc[h][n][1][t][i];
+  __syncthreads();
+  for (uint32_t o = threadIdx.x; o < NT * 256; o += W * 64) {
+    float vg = 0.0f, vu = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W * 2; ++i) {
+      vg += sums[(i >> 1) * 2 * kPlane + (i & 1) * (NT * 256) + o];
+      vu += sums[((i >> 1) * 2 + 1) * kPlane + (i & 1) * (NT * 256) + o];
+    }
+    const uint64_t token = o / 16, col = c0 + o % 16;
+    if (token >= a.m || col >= a.n) continue;
+    few_store<DT>(a, token, col, vg, vu);
+  }
+}
+
+template <int DT, int NT, int W, int PIECES>
+hipError_t lines_launch(const FfProduct& a, hipStream_t stream) {
+  hipLaunchKernelGGL((ff_lines_kernel<DT, NT, W, PIECES>), dim3((unsigned)((a.n + 15) / 16)), dim3(W * 64),
+                     W * 2 * NT * 512 * sizeof(float), stream, a);
   return launch_status(stream);
 }
 
@@ -233,19 +339,24 @@ hipError_t vector_launch(const FfProduct& a, hipStream_t stream) {
 }
 
 // One and two tokens go to the vector units: 28.3 and 30.9 us at 4096 x 11264
-// bfloat16 (184 MB, 29 us at the rate of a large copy), the matrix kernel 38 for
-// both; at four tokens the rows of x cost as much as that saves (37 to 41, and 39).
-// The matrix kernel's shapes, us at 4096 x 11264: 16 tokens 47, as with half the
-// pieces or half the wavefronts; 24 tokens 53, and 61 with two blocks of columns;
-// 64 tokens 67, and 78 to 83 with one block of columns, where x is read twice as
-// often.
+// bfloat16 (184 MB, 29 us at the rate of a large copy), 32 and 32 by whole lines;
+// at four tokens the rows of x cost more than that saves (37 to 41, and 33).  The
+// shapes, us: 16 tokens 37.6, and 38 to 39.6 with 2 or 8 wavefronts, 2 or 8
+// pieces; 24 tokens 44, and 46 to 58 with 8 wavefronts or 4 pieces; 64 tokens 67,
+// and 78 to 83 with one block of columns, where x is read twice as often.  In
+// binary32 the doubled products of whole lines do not have time beyond 16 tokens:
+// 24 tokens 143 us so, 108 with each product once (16 tokens 85 and 108).
 template <int DT>
 hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
   if (a.m == 1) return vector_launch<DT, 1>(a, stream);
   if (a.m == 2) return vector_launch<DT, 2>(a, stream);
-  if (a.m <= 16) return few_launch<DT, 1, 1, 8, 4>(a, stream);
-  if (a.m <= 32) return few_launch<DT, 2, 1, 8, 2>(a, stream);
-  return few_launch<DT, 4, 2, 4, 1>(a, stream);
+  if (a.m <= 16) return lines_launch<DT, 1, 4, 4>(a, stream);
+  if constexpr (DT == DT_F32) {
+    if (a.m <= 32) return few_launch<DT, 2, 1, 8>(a, stream);
+  } else {
+    if (a.m <= 32) return lines_launch<DT, 2, 4, 2>(a, stream);
+  }
+  return few_launch<DT, 4, 2, 4>(a, stream);
 }
 
 // ------------------------------------------------------------------ gradients of the product
