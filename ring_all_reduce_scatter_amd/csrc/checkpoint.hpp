@@ -16,6 +16,8 @@
 // the matrix itself cannot.
 #pragma once
 
+#include <algorithm>
+
 #include "row_access.hpp"
 
 namespace rar {
@@ -126,6 +128,46 @@ __device__ __forceinline__ void ckpt_store(uint8_t* codes, uint8_t* exps, uint32
   else
     __builtin_nontemporal_store(ckpt_encode4(x.v, sc), (uint32_t*)(codes + col));
   if (col % kCkptBlock == 0) exps[col / kCkptBlock] = (uint8_t)(m >> 23);
+}
+
+// n / d for n < 2^31: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d) the
+// quotient is n m >> (31 + s).
+struct FastDiv {
+  uint32_t m, s, d;
+  explicit FastDiv(uint32_t by) : s(0), d(by) {
+    while (((uint64_t)1 << s) < by) ++s;
+    m = (uint32_t)((((uint64_t)1 << (31 + s)) + by - 1) / by);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)((uint64_t)n * m >> (31 + s)); }
+};
+
+// A walk over blocks of rows, U vectors of E elements a lane: where its k-th
+// vector lies.  Block numbers of a launch stay within 31 bits.
+struct CkptPlace {
+  uint32_t block, row, col;
+  bool live;
+};
+template <int E, int U>
+__device__ __forceinline__ CkptPlace ckpt_place(uint32_t k, uint32_t blocks, const FastDiv& nb) {
+  constexpr uint32_t LB = kCkptBlock / E;  // lanes a block
+  CkptPlace p;
+  p.block = (blockIdx.x * U + k) * (kThreads / LB) + threadIdx.x / LB;
+  p.live = p.block < blocks;
+  p.row = nb.div(p.block);
+  p.col = (p.block - p.row * nb.d) * kCkptBlock + threadIdx.x % LB * E;
+  return p;
+}
+
+// Calls f with the first row, the rows and the grid of each launch.
+template <int E, int U, class F>
+hipError_t by_ckpt_rows(uint64_t rows, uint64_t nb, F f) {
+  const uint64_t per = std::max<uint64_t>(1, ((uint64_t)1 << 30) / nb);
+  for (uint64_t r = 0; r < rows; r += per) {
+    const uint64_t n = std::min(per, rows - r), wg = U * kThreads / (kCkptBlock / E);
+    const hipError_t e = f(r, (uint32_t)(n * nb), dim3((unsigned)((n * nb + wg - 1) / wg)));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace rar

@@ -14,46 +14,16 @@
 namespace rar {
 namespace {
 
-// n / d for n < 2^31: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d) the
-// quotient is n m >> (31 + s).
-struct FastDiv {
-  uint32_t m, s, d;
-  explicit FastDiv(uint32_t by) : s(0), d(by) {
-    while (((uint64_t)1 << s) < by) ++s;
-    m = (uint32_t)((((uint64_t)1 << (31 + s)) + by - 1) / by);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)((uint64_t)n * m >> (31 + s)); }
-};
-
 constexpr int kUnroll = 4;  // vectors a lane has in flight
-// Blocks of one launch: row and block numbers stay within 31 bits.
-constexpr uint64_t kLaunchBlocks = (uint64_t)1 << 30;
-
-// Where a lane's k-th vector lies.
-struct Place {
-  uint32_t block, row, col;
-  bool live;
-};
-template <int E>
-__device__ __forceinline__ Place place(uint32_t k, uint32_t blocks, const FastDiv& nb) {
-  constexpr uint32_t LB = kCkptBlock / E;  // lanes a block
-  Place p;
-  p.block = (blockIdx.x * kUnroll + k) * (kThreads / LB) + threadIdx.x / LB;
-  p.live = p.block < blocks;
-  p.row = nb.div(p.block);
-  p.col = (p.block - p.row * nb.d) * kCkptBlock + threadIdx.x % LB * E;
-  return p;
-}
-
 template <int DT>
 __global__ __launch_bounds__(kThreads) void ckpt_pack_kernel(Rows x, uint64_t dim, FastDiv nb, uint32_t blocks,
                                                               uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
-  Place p[kUnroll];
+  CkptPlace p[kUnroll];
   VecF<E> v[kUnroll];
 #pragma unroll
   for (int k = 0; k < kUnroll; ++k) {
-    p[k] = place<E>(k, blocks, nb);
+    p[k] = ckpt_place<E, kUnroll>(k, blocks, nb);
     v[k] = {};
     if (p[k].live) {
       const char* row = x.p + p[k].row * x.stride * ES;
@@ -76,11 +46,11 @@ __global__ __launch_bounds__(kThreads) void ckpt_unpack_kernel(const uint8_t* __
                                                                 const uint8_t* __restrict__ exps, FastDiv nb,
                                                                 uint32_t blocks, Rows out, uint64_t dim) {
   constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
-  Place p[kUnroll];
+  CkptPlace p[kUnroll];
   CkptRaw<E> raw[kUnroll];
 #pragma unroll
   for (int k = 0; k < kUnroll; ++k) {
-    p[k] = place<E>(k, blocks, nb);
+    p[k] = ckpt_place<E, kUnroll>(k, blocks, nb);
     raw[k] = {};
     if (p[k].live)
       raw[k] = ckpt_load<E>(codes + (uint64_t)p[k].block * kCkptBlock, exps + p[k].block,
@@ -93,21 +63,9 @@ __global__ __launch_bounds__(kThreads) void ckpt_unpack_kernel(const uint8_t* __
                             ckpt_unpack<E>(raw[k]));
 }
 
-// Calls f with the first row, the rows and the grid of each launch.
-template <int E, class F>
-hipError_t by_rows(uint64_t rows, uint64_t nb, F f) {
-  const uint64_t per = std::max<uint64_t>(1, kLaunchBlocks / nb);
-  for (uint64_t r = 0; r < rows; r += per) {
-    const uint64_t n = std::min(per, rows - r), wg = kUnroll * kThreads / (kCkptBlock / E);
-    const hipError_t e = f(r, (uint32_t)(n * nb), dim3((unsigned)((n * nb + wg - 1) / wg)));
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
 template <int DT>
 hipError_t pack_dt(const Rows& x, uint64_t rows, uint64_t dim, const Checkpoint& c, hipStream_t stream) {
-  return by_rows<vec_elems<DT, DT>()>(rows, c.nb, [&](uint64_t r, uint32_t blocks, dim3 grid) {
+  return by_ckpt_rows<vec_elems<DT, DT>(), kUnroll>(rows, c.nb, [&](uint64_t r, uint32_t blocks, dim3 grid) {
     Rows part = x;
     part.p += r * x.stride * DtypeSize<DT>::value;
     hipLaunchKernelGGL((ckpt_pack_kernel<DT>), grid, dim3(kThreads), 0, stream, part, dim, FastDiv((uint32_t)c.nb),
@@ -118,7 +76,7 @@ hipError_t pack_dt(const Rows& x, uint64_t rows, uint64_t dim, const Checkpoint&
 
 template <int DT>
 hipError_t unpack_dt(const Checkpoint& c, uint64_t rows, uint64_t dim, const Rows& out, hipStream_t stream) {
-  return by_rows<vec_elems<DT, DT>()>(rows, c.nb, [&](uint64_t r, uint32_t blocks, dim3 grid) {
+  return by_ckpt_rows<vec_elems<DT, DT>(), kUnroll>(rows, c.nb, [&](uint64_t r, uint32_t blocks, dim3 grid) {
     Rows part = out;
     part.p += r * out.stride * DtypeSize<DT>::value;
     hipLaunchKernelGGL((ckpt_unpack_kernel<DT>), grid, dim3(kThreads), 0, stream, c.codes + r * c.nb * kCkptBlock,

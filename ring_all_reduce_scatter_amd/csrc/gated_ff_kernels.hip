@@ -367,35 +367,42 @@ hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
 constexpr int kGradUnroll = 2;
 
 template <int DT, bool CK>
-__global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uint64_t blocks, uint32_t nb,
+__global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uint64_t row0, uint32_t blocks, FastDiv nb,
                                                                 uint64_t du_at) {
-  constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value, LB = kCkptBlock / E;
-  const uint64_t pitch = (uint64_t)nb * kCkptBlock;
+  constexpr int E = vec_elems<DT, DT>(), ES = DtypeSize<DT>::value;
+  const uint64_t pitch = (uint64_t)nb.d * kCkptBlock;
+  CkptPlace p[kGradUnroll];
+  VecF<E> dh[kGradUnroll], g[kGradUnroll], u[kGradUnroll];
 #pragma unroll
   for (int k = 0; k < kGradUnroll; ++k) {
-    const uint64_t block = ((uint64_t)blockIdx.x * kGradUnroll + k) * (kThreads / LB) + threadIdx.x / LB;
-    if (block >= blocks) return;
-    const uint64_t row = block / nb;
-    const uint32_t col = (uint32_t)(block - row * nb) * kCkptBlock + threadIdx.x % LB * E;
-    const int n = vec_count<E>(a.hidden, col);
-    const VecF<E> dh = load_vec_upto<DT, E>(a.dh.p + row * a.dh.stride * ES, col, n);
-    VecF<E> g, u, dg = {}, du = {};
+    p[k] = ckpt_place<E, kGradUnroll>(k, blocks, nb);
+    dh[k] = g[k] = u[k] = {};
+    if (!p[k].live) continue;
+    const uint64_t row = row0 + p[k].row;
+    const int n = vec_count<E>(a.hidden, p[k].col);
+    dh[k] = load_vec_upto<DT, E>(a.dh.p + row * a.dh.stride * ES, p[k].col, n);
     if constexpr (CK) {
-      g = ckpt_unpack<E>(ckpt_load<E>(a.cgate.code_row(row), a.cgate.exp_row(row), col));
-      u = ckpt_unpack<E>(ckpt_load<E>(a.cup.code_row(row), a.cup.exp_row(row), col));
+      g[k] = ckpt_unpack<E>(ckpt_load<E>(a.cgate.code_row(row), a.cgate.exp_row(row), p[k].col));
+      u[k] = ckpt_unpack<E>(ckpt_load<E>(a.cup.code_row(row), a.cup.exp_row(row), p[k].col));
     } else {
-      g = load_vec_upto<DT, E>(a.gate.p + row * a.gate.stride * ES, col, n);
-      u = load_vec_upto<DT, E>(a.up.p + row * a.up.stride * ES, col, n);
+      g[k] = load_vec_upto<DT, E>(a.gate.p + row * a.gate.stride * ES, p[k].col, n);
+      u[k] = load_vec_upto<DT, E>(a.up.p + row * a.up.stride * ES, p[k].col, n);
     }
+  }
+#pragma unroll
+  for (int k = 0; k < kGradUnroll; ++k) {
+    if (!p[k].live) continue;
+    const int n = vec_count<E>(a.hidden, p[k].col);
+    VecF<E> dg = {}, du = {};
 #pragma unroll
     for (int i = 0; i < E; ++i)
       if (i < n) {
         float d;
-        const float h = ff_act<true>(g.v[i], a.act, &d);
-        dg.v[i] = dh.v[i] * u.v[i] * d;
-        du.v[i] = dh.v[i] * h;
+        const float h = ff_act<true>(g[k].v[i], a.act, &d);
+        dg.v[i] = dh[k].v[i] * u[k].v[i] * d;
+        du.v[i] = dh[k].v[i] * h;
       }
-    const uint64_t at = (row * pitch + col) * ES;
+    const uint64_t at = ((row0 + p[k].row) * pitch + p[k].col) * ES;
     *(u32x4*)(a.ws + at) = pack_vec<DT, E>(dg);
     *(u32x4*)(a.ws + du_at + at) = pack_vec<DT, E>(du);
   }
@@ -403,17 +410,16 @@ __global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uin
 
 template <int DT>
 hipError_t act_grad_dt(const FfBackward& a, hipStream_t stream) {
-  constexpr uint64_t wg = kGradUnroll * kThreads / (kCkptBlock / vec_elems<DT, DT>());
-  const uint64_t nb = (a.hidden + kCkptBlock - 1) / kCkptBlock, blocks = a.rows * nb;
-  const dim3 grid((unsigned)((blocks + wg - 1) / wg));
+  const uint64_t nb = (a.hidden + kCkptBlock - 1) / kCkptBlock;
   const uint64_t du_at = ff_workspace(a.rows, a.dim, a.hidden, DT).du;
-  if (a.saved == 2)
-    hipLaunchKernelGGL((ff_act_grad_kernel<DT, true>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb,
-                       du_at);
-  else
-    hipLaunchKernelGGL((ff_act_grad_kernel<DT, false>), grid, dim3(kThreads), 0, stream, a, blocks, (uint32_t)nb,
-                       du_at);
-  return launch_status(stream);
+  return by_ckpt_rows<vec_elems<DT, DT>(), kGradUnroll>(a.rows, nb, [&](uint64_t r, uint32_t blocks, dim3 grid) {
+    const FastDiv by((uint32_t)nb);
+    if (a.saved == 2)
+      hipLaunchKernelGGL((ff_act_grad_kernel<DT, true>), grid, dim3(kThreads), 0, stream, a, r, blocks, by, du_at);
+    else
+      hipLaunchKernelGGL((ff_act_grad_kernel<DT, false>), grid, dim3(kThreads), 0, stream, a, r, blocks, by, du_at);
+    return launch_status(stream);
+  });
 }
 
 // ------------------------------------------------------------------ sums of splits
