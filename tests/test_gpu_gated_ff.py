@@ -325,3 +325,74 @@ def test_replays_in_a_graph_and_other_streams(rows):
             step(keep, side)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, outs)), k
+
+
+def _whole(g, lo, hi, *shape):
+    return torch.randint(lo, hi + 1, shape, generator=g, device=DEV).to(torch.bfloat16)
+
+
+def _kept_gradients(dh, kept_g, kept_u):
+    """dg and du (64 bits) of gates of 0 and 64 through the gelu, exact."""
+    return dh.double() * kept_u.double() * torch.where(kept_g > 0, 1.0, 0.5), dh.double() * kept_g.double()
+
+
+def test_rows_past_four_gib():
+    """x and dx of 4.2 GiB: the first and the last rows hold whole numbers, the
+    others zeros, so that both gradients of the weights are exact."""
+    rows, dim, hidden, ends = 1_100_003, 2048, 40, 300
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.zeros(rows, dim, dtype=torch.bfloat16, device=DEV)
+    dh, up, gate, out = (torch.zeros(rows, hidden, dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    wg, wu = _whole(g, -1, 1, hidden, dim), _whole(g, -1, 1, hidden, dim)
+    for part in (slice(0, ends), slice(rows - ends, rows)):
+        x[part] = _whole(g, -2, 2, ends, dim)
+    rar.gated_ff_forward(x, wg, wu, out, act=rar.ACT_GELU, gate=gate, up=up)
+    for part in (slice(0, ends), slice(rows - ends, rows)):
+        assert torch.equal(gate[part], (x[part].double() @ wg.double().t()).bfloat16()), part
+        assert torch.equal(up[part], (x[part].double() @ wu.double().t()).bfloat16()), part
+    assert not bool(gate[ends:-ends].any()) and not bool(out[ends:-ends].any())
+    want = [torch.zeros(hidden, dim, dtype=torch.float64, device=DEV) for _ in range(2)]
+    pieces = []
+    for part in (slice(0, ends), slice(rows - ends, rows)):
+        dh[part], gate[part], up[part] = (_whole(g, -1, 1, ends, hidden), 64 * _whole(g, 0, 1, ends, hidden),
+                                          _whole(g, -2, 2, ends, hidden))
+        dg, du = _kept_gradients(dh[part], gate[part], up[part])
+        want[0] += dg.t() @ x[part].double()
+        want[1] += du.t() @ x[part].double()
+        pieces.append((part, (dg @ wg.double() + du @ wu.double()).bfloat16()))
+    dx, dwg, dwu = _backward(dh, x, wg, wu, gate, up, rar.ACT_GELU, torch.float32)
+    for part, value in pieces:
+        assert torch.equal(dx[part], value), part
+    assert not bool(dx[ends:-ends].any())
+    assert torch.equal(dwg, want[0].float()) and torch.equal(dwu, want[1].float())
+
+
+@pytest.mark.parametrize("rows", [2, 5, 40, 70])
+def test_weights_past_four_gib(rows):
+    """Weights and their gradients of 4.3 GiB each, with whole numbers in the
+    first and the last rows and zeros between them."""
+    hidden, dim, ends = 1_048_576, 2200, 200
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    x = _whole(g, -2, 2, rows, dim)
+    wg, wu = (torch.zeros(hidden, dim, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    dh, gate, up, out = (torch.zeros(rows, hidden, dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    parts = (slice(0, ends), slice(hidden - ends, hidden))
+    for part in parts:
+        wg[part], wu[part] = _whole(g, -1, 1, ends, dim), _whole(g, -1, 1, ends, dim)
+    rar.gated_ff_forward(x, wg, wu, out, act=rar.ACT_GELU, gate=gate, up=up)
+    for part in parts:
+        assert torch.equal(gate[:, part], (x.double() @ wg[part].double().t()).bfloat16()), part
+        assert torch.equal(up[:, part], (x.double() @ wu[part].double().t()).bfloat16()), part
+    assert not bool(gate[:, ends:-ends].any()) and not bool(out[:, ends:-ends].any())
+    want_dx, want_dw = 0, []
+    for part in parts:
+        dh[:, part], gate[:, part], up[:, part] = (_whole(g, -1, 1, rows, ends), 64 * _whole(g, 0, 1, rows, ends),
+                                                   _whole(g, -2, 2, rows, ends))
+        dg, du = _kept_gradients(dh[:, part], gate[:, part], up[:, part])
+        want_dx = want_dx + dg @ wg[part].double() + du @ wu[part].double()
+        want_dw.append((part, (dg.t() @ x.double()).bfloat16(), (du.t() @ x.double()).bfloat16()))
+    dx, dwg, dwu = _backward(dh, x, wg, wu, gate, up, rar.ACT_GELU, torch.bfloat16)
+    assert torch.equal(dx, want_dx.bfloat16())
+    for part, value_g, value_u in want_dw:
+        assert torch.equal(dwg[part], value_g) and torch.equal(dwu[part], value_u), part
+    assert not bool(dwg[ends:-ends].any()) and not bool(dwu[ends:-ends].any())
