@@ -361,9 +361,13 @@ hipError_t few_dt(const FfProduct& a, hipStream_t stream) {
 
 // ------------------------------------------------------------------ gradients of the product
 
-// dg and du from dh and the kept projections, a vector a lane over blocks of
+// dg and du from dh and the kept projections, two vectors a lane over blocks of
 // 32 columns.  dg and du lie in the workspace with rows of whole blocks; the
 // columns past hidden are made zeros, since dx's product reads whole chunks.
+// Bound by memory: 8192 x 11,264 bfloat16 from checkpoints 118 us (744 MB, 6.3
+// TB/s), 2048 x 5632 from rows 26 (115 MB, 4.4 TB/s).  dg and du are rounded to
+// the activations' type because the products' matrix instructions take that
+// type; as the two halves of a split sum they would cost twice the products.
 constexpr int kGradUnroll = 2;
 
 template <int DT, bool CK>
@@ -425,6 +429,7 @@ hipError_t act_grad_dt(const FfBackward& a, hipStream_t stream) {
 // ------------------------------------------------------------------ sums of splits
 
 // Adds the splits of a product in order and rounds; blockIdx.y is the output.
+// (2048 x 2048 of four splits 13 us, 71 MB: 5.4 TB/s)
 template <int DT>
 __global__ __launch_bounds__(kThreads) void ff_join_kernel(FfProduct a) {
   const uint64_t vecs = a.pitch / 4, i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -459,7 +464,10 @@ hipError_t join_dt(const FfProduct& a, int outputs, hipStream_t stream) {
 // ------------------------------------------------------------------ aligned copies
 
 // Rows of `dim` elements copied to rows of whole blocks, zeros after them: what
-// direct loads read where the rows themselves begin off 16 bytes.
+// direct loads read where the rows themselves begin off 16 bytes.  1021 x 1001
+// and twice 2731 x 1001 float16: 6 us, for which dx's product and the weights'
+// take direct loads (27 and 25 us; the forward pass, which has no workspace,
+// takes 48 of as many operations through registers).
 struct FfCopy {
   const char* from[3];
   uint64_t stride[3], rows[3];
@@ -500,9 +508,18 @@ uint64_t blocks_pitch(uint64_t n) { return up_div(n, kCkptBlock) * kCkptBlock; }
 // Direct loads move 16 bytes from a 16-byte boundary.
 bool direct_ok(const char* p, uint64_t stride_bytes) { return (((uint64_t)p | stride_bytes) & 15) == 0; }
 
-// How a product is cut: tiles of 256 x 256 or the smaller ones, and splits of
-// its terms for CUs that the tiles leave without work, of at least eight
-// stages each.
+// How a product of the backward pass is cut: tiles of 256 x 256 or the smaller
+// ones, and splits of its terms for CUs that the tiles leave without work, of at
+// least eight stages each.  Both sides, us of bfloat16 with the gradients of the
+// product before it:
+//   large tiles where they give every CU one: 8192 x 4096 x 11,264 towards x
+//   1337 (small ones 3266), towards the weights 1469 (1756);
+//   large tiles and splits where they give every fourth CU one and the sum is
+//   long: 2048 x 2048 x 5632 towards x 120 (small ones, unsplit, 195);
+//   small ones otherwise: 1024 x 1024 x 2816 towards the weights 30.5 (large
+//   44), towards x 38 (40.5);
+//   splits: 1024 x 1024 x 2816 towards x 38 (unsplit 89), 65 x 4096 x 11,264 63
+//   (337), binary32 513 x 1024 x 2816 76 (198).
 struct FfCut {
   bool wide;
   uint32_t splits;
@@ -580,11 +597,16 @@ hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream) {
   a.up = f.up;
   a.cgate = f.cgate;
   a.cup = f.cup;
-  // a checkpoint's block of 32 columns is more than such a workgroup has
+  // At 4096 x 11,264 bfloat16 64 tokens take 67 us, 65 in tiles 73; at 1024 x
+  // 2816 14.9 and 17.6.  A checkpoint's block of 32 columns is more than a
+  // workgroup of whole lines has.
   if (f.rows <= kFewTokens && f.saved != 2)
     return by_type(f.dt, [&](auto t) { return few_dt<decltype(t)::value>(a, stream); });
   const bool direct = f.dim % (16 / es) == 0 && direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) &&
                       direct_ok(a.q[0], a.qstride);
+  // large tiles where they give every CU one: 8192 x 4096 x 11,264 bfloat16 1192
+  // us (small ones 1709), 2048 x 2048 x 5632 117 (127); 511 x 2048 x 5632 53 and
+  // 36, 1024 x 1024 x 2816 34 and 22.6
   const bool wide = direct && f.dt != DT_F32 && up_div(f.rows, 256) * up_div(f.hidden, 128) >= kCus;
   return launch_ff_forward_tiles(f.dt, a, wide, direct, stream);
 }

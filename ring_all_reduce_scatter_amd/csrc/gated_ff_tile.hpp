@@ -23,6 +23,16 @@
 // lane order.  Rows of the operand's own index are read by the transposing
 // LDS load (16 bits), which hands lane i of 16 the i-th of 16 columns and
 // four consecutive k.
+//
+// Bound by the matrix units' rate under power and what the loads leave of it.
+// 8192 x 4096 x 11,264 bfloat16 (1.51 TFLOP a pass of two products): forward 1145
+// us without kept projections (1.32 PFLOP/s) and 1230 with checkpoints, dx 1205,
+// dW 1340; large library products of these layouts reach 1.33-1.53, 1.20-1.40
+// and 0.98-1.08 PFLOP/s.  Measured and left out: instructions of 32 x 32 (power),
+// stages of 64 bytes a row in four turns (their loads move at half the rate:
+// 1418 us where two of 128 took 1319), three to five stages, four wavefronts of
+// 128 x 128, loads of the next rows into the L2 ahead (1262-1281 against 1213),
+// a different first k for each XCD (no change).
 #pragma once
 
 #include <algorithm>
@@ -61,8 +71,8 @@ __device__ __forceinline__ f32x4 ff_mfma(u32x4 p, u32x4 q, f32x4 c) {
 
 // Direct loads are written as assembly because the compiler, which cannot tell
 // the two stages apart, would wait for them before the next transposing read
-// of LDS (dx 1640 us against 1290 at 8192 x 4096 x 11,264 bf16).  They have no
-// output register; the wait for them is ff_meet's.  The nop keeps the five wait
+// of LDS (dx of 8192 x 4096 x 11,264 bf16 took 1640 us instead of 1290 when both
+// were tried).  They have no output register; the wait for them is ff_meet's.  The nop keeps the five wait
 // states that a buffer access needs after a vector instruction wrote its
 // scalar registers.
 __device__ __forceinline__ void ff_load_lds(u32x4 range, uint32_t off, uint32_t to) {
