@@ -31,8 +31,10 @@
 // and 0.98-1.08 PFLOP/s.  Measured and left out: instructions of 32 x 32 (power),
 // stages of 64 bytes a row in four turns (their loads move at half the rate:
 // 1418 us where two of 128 took 1319), three to five stages, four wavefronts of
-// 128 x 128, loads of the next rows into the L2 ahead (1262-1281 against 1213),
-// a different first k for each XCD (no change).
+// 128 x 128, tiles of 256 x 128 (1937 us forward: half the products for three
+// quarters of the loads; 511 x 2048 x 5632 42 instead of 36), loads of the next
+// rows into the L2 ahead (1262-1281 against 1213), a different first k for each
+// XCD (no change).
 #pragma once
 
 #include <algorithm>
@@ -52,8 +54,14 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kRow = 128;  // bytes of k a row of a stage
 
+// A chunk's terms in binary32 take four instructions, of one term in each of a
+// lane quarter's chunks; in 16 bits one takes them all.
 template <int DT>
-__device__ __forceinline__ f32x4 ff_mfma(u32x4 p, u32x4 q, f32x4 c) {
+__host__ __device__ constexpr int ff_turns() {
+  return DT == DT_F32 ? 4 : 1;
+}
+template <int DT>
+__device__ __forceinline__ f32x4 ff_mfma(u32x4 p, u32x4 q, f32x4 c, int turn) {
   if constexpr (DT == DT_BF16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, p), __builtin_bit_cast(b16x8, q), c, 0, 0,
                                                    0);
@@ -61,11 +69,7 @@ __device__ __forceinline__ f32x4 ff_mfma(u32x4 p, u32x4 q, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, p), __builtin_bit_cast(h16x8, q), c, 0, 0,
                                                   0);
   } else {
-    // four terms a lane: the i-th of the four chunks make one instruction's four
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(p[i]), __uint_as_float(q[i]), c, 0, 0, 0);
-    return c;
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(p[turn]), __uint_as_float(q[turn]), c, 0, 0, 0);
   }
 }
 
@@ -510,9 +514,9 @@ __global__ __launch_bounds__(SH::threads) void ff_product_kernel(FfProduct a) {
   constexpr int NTHR = SH::threads, ES = DtypeSize<DT>::value, BK = kRow / ES;
   constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;  // 16 x 16 blocks of a wavefront
   // A stage is 2 steps of k, each of GROUPS groups of QN of Q's blocks.
-  constexpr int QN = NQ == 4 ? 4 : 2, GROUPS = NQ / QN, STEPS = 2 * GROUPS;
+  constexpr int QN = NQ < 2 ? NQ : 2, GROUPS = NQ / QN, STEPS = 2 * GROUPS;
   constexpr bool FWD = KIND == FF_FORWARD;
-  static_assert(NP % 2 == 0 && NQ % 2 == 0 && (!FWD || NP % 4 == 0), "of each 64 columns 32 are gate's and 32 up's");
+  static_assert(NP % 2 == 0 && (!FWD || NP % 4 == 0), "of each 64 columns 32 are gate's and 32 up's");
   using LP = FfLoader<DT, FWD, TP, NTHR, DIRECT, FWD, FWD>;
   using LQ = FfLoader<DT, KIND != FF_DW, TQ, NTHR, DIRECT, false, false>;
   constexpr uint32_t kStageP = TP * kRow, kStage = (TP + TQ) * kRow;
@@ -623,10 +627,12 @@ __global__ __launch_bounds__(SH::threads) void ff_product_kernel(FfProduct a) {
   auto multiply = [&](auto step) __attribute__((always_inline)) {
     constexpr int ks = decltype(step)::value / GROUPS, group = decltype(step)::value % GROUPS;
 #pragma unroll
-    for (int j = 0; j < QN; ++j)
+    for (int t = 0; t < ff_turns<DT>(); ++t)
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
-        acc[i][group * QN + j] = ff_mfma<DT>(fp[ks][i], fq[decltype(step)::value & 1][j], acc[i][group * QN + j]);
+      for (int j = 0; j < QN; ++j)
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          acc[i][group * QN + j] = ff_mfma<DT>(fp[ks][i], fq[decltype(step)::value & 1][j], acc[i][group * QN + j], t);
   };
   constexpr std::integral_constant<int, 0> kFirstStep;
   constexpr std::integral_constant<int, STEPS - 1> kLastStep;
@@ -712,11 +718,14 @@ hipError_t ff_launch(FfProduct& a, hipStream_t stream) {
 template <int DT, int KIND>
 hipError_t ff_launch_dt(FfProduct& a, bool wide, bool direct, hipStream_t stream) {
   if constexpr (DT == DT_F32) {
-    // in binary32 the matrix instructions take sixteen times as long for a
-    // stage, so that small tiles cost nothing and fill the CUs evenly
-    constexpr int TP = KIND == FF_FORWARD ? 128 : 64;
-    return direct ? ff_launch<DT, KIND, FfShape<TP, 64, 2, 2>, true>(a, stream)
-                  : ff_launch<DT, KIND, FfShape<TP, 64, 2, 2>, false>(a, stream);
+    // In binary32 the matrix instructions take sixteen times as long for a
+    // stage, so that small tiles cost little and fill the CUs evenly: forward of
+    // 513 x 1024 x 2816 67 us (80 by 64 rows), 65 x 1024 x 2816 31.5 (52), 2048 x
+    // 2048 x 5632 794 (784).  The backward products are split, which does that
+    // for tiles of 64 rows.
+    constexpr int TP = KIND == FF_FORWARD ? 128 : 64, TQ = KIND == FF_FORWARD ? 32 : 64;
+    return direct ? ff_launch<DT, KIND, FfShape<TP, TQ, 2, 2>, true>(a, stream)
+                  : ff_launch<DT, KIND, FfShape<TP, TQ, 2, 2>, false>(a, stream);
   } else {
     if (wide) return ff_launch<DT, KIND, FfShape<256, 256, 4, 2>, true>(a, stream);
     return direct ? ff_launch<DT, KIND, FfShape<128, 128, 2, 4>, true>(a, stream)
