@@ -47,8 +47,8 @@ __device__ __forceinline__ float ff_act(float g, int act, float* d) {
 struct FfProduct {
   const char* p[2];
   const char* q[2];
-  uint32_t pstride[2], qstride;  // bytes between rows (dx: the same for both P)
-  uint64_t m, n, k;                 // rows and columns of the output, terms of a segment
+  uint32_t pstride[2], qstride;  // bytes between rows
+  uint64_t m, n, k;              // rows and columns of the output, terms of a segment
   uint32_t splits;                            // wanted; the launch makes it what there is work for
   uint32_t tiles_m, tiles_n, ktiles, per_split;  // set by the launch; stages of all segments, of a split
   int act, saved;

@@ -540,7 +540,7 @@ __global__ __launch_bounds__(SH::threads) void ff_product_kernel(FfProduct a) {
   uint64_t done;  // terms of the segment before the next stage
   uint32_t seg;
   const uint32_t seg_tiles = KIND == FF_DX ? a.ktiles / 2 : a.ktiles;
-  const uint64_t pstep = FWD ? kRow : (uint64_t)BK * a.pstride[0];
+  uint64_t pstep = FWD ? kRow : (uint64_t)BK * a.pstride[0];  // dx: of the segment
   const uint64_t qstep = KIND == FF_DW ? (uint64_t)BK * a.qstride : kRow;
   // the operands of the item's stage kt (dx: gate's terms, then up's)
   auto aim = [&](uint32_t kt) __attribute__((always_inline)) {
@@ -548,6 +548,12 @@ __global__ __launch_bounds__(SH::threads) void ff_product_kernel(FfProduct a) {
     seg = KIND == FF_DX && kt >= seg_tiles;
     const uint32_t k = kt - (seg ? seg_tiles : 0);
     done = (uint64_t)k * BK;
+    if constexpr (KIND == FF_DX) {
+      // the weights' rows may lie differently far apart
+      const uint32_t stride = seg ? args->pstride[1] : args->pstride[0];
+      pstep = (uint64_t)BK * stride;
+      lp.init(args->n - want.n0, stride, stride);
+    }
     const uint64_t prow = FWD ? want.n0 * args->pstride[0] : want.n0 * ES;
     pcur = (seg ? args->p[1] : args->p[0]) + prow + k * pstep;
     if (FWD) pcur1 = args->p[1] + want.n0 * args->pstride[1] + k * pstep;
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(SH::threads) void ff_product_kernel(FfProduct a) {
   auto begin = [&]() __attribute__((always_inline)) {
     want = ff_item<KIND, TQ, kCols>(ask.next);
     const FfArguments args = ff_arguments();
-    lp.init(args->n - want.n0, args->pstride[0], args->pstride[1]);
+    if constexpr (KIND != FF_DX) lp.init(args->n - want.n0, args->pstride[0], args->pstride[1]);
     lq.init(args->m - want.m0, args->qstride, args->qstride);
     want_kt = want.k_begin;
     aim(want_kt);
