@@ -508,39 +508,46 @@ uint64_t blocks_pitch(uint64_t n) { return up_div(n, kCkptBlock) * kCkptBlock; }
 // Direct loads move 16 bytes from a 16-byte boundary.
 bool direct_ok(const char* p, uint64_t stride_bytes) { return (((uint64_t)p | stride_bytes) & 15) == 0; }
 
-// How a product of the backward pass is cut: tiles of 256 x 256 or the smaller
-// ones, and splits of its terms for CUs that the tiles leave without work, of at
-// least eight stages each.  Both sides, us of bfloat16 with the gradients of the
-// product before it:
+// How a product of the backward pass is cut: tiles of 256 x 256 (of direct loads
+// only) or the smaller ones, and splits of its terms for CUs that the tiles leave
+// without work, of at least eight stages each.  Both sides, us of bfloat16 with
+// the gradients of the product before it:
 //   large tiles where they give every CU one: 8192 x 4096 x 11,264 towards x
 //   1337 (small ones 3266), towards the weights 1469 (1756);
-//   large tiles and splits where they give every fourth CU one and the sum is
-//   long: 2048 x 2048 x 5632 towards x 120 (small ones, unsplit, 195);
+//   large tiles, split as often as every CU gets one, where there are at least a
+//   quarter as many tiles as CUs and the sum is long: towards x 64 tiles of 2048
+//   x 2048 x 5632 120 (small ones, unsplit, 192), 72 of 2304 x 2048 x 5632 138
+//   (344); unsplit above half as many, 130 of 2560 x 3328 x 2816 142 (250), 220
+//   of 2816 x 5120 x 2816 155 (332), 240 of 3840 x 4096 x 2816 163 (339);
+//   towards the weights 130 of 8192 x 3328 x 1280 198 (266), 220 of 8192 x 2816 x
+//   2560 234 (310);
 //   small ones otherwise: 1024 x 1024 x 2816 towards the weights 30.5 (large
 //   44), towards x 38 (40.5);
 //   splits: 1024 x 1024 x 2816 towards x 38 (unsplit 89), 65 x 4096 x 11,264 63
 //   (337), binary32 513 x 1024 x 2816 76 (198).
+// Small tiles of rows off 16 bytes are split by their own number, not the large
+// ones': 1024 x 4096 x 4096 towards x 152 (split as the large ones 216).
 struct FfCut {
   bool wide;
   uint32_t splits;
 };
-FfCut cut_of(uint64_t m, uint64_t n, uint64_t outputs, uint64_t ktiles, int dt) {
+FfCut cut_of(uint64_t m, uint64_t n, uint64_t outputs, uint64_t ktiles, int dt, bool direct) {
   if (dt == DT_F32) {
     const uint64_t tiles = up_div(m, 64) * up_div(n, 64) * outputs;
     return {false, (uint32_t)std::max<uint64_t>(1, std::min(4 * kCus / std::max<uint64_t>(tiles, 1), ktiles / 8))};
   }
   const uint64_t wide = up_div(m, 256) * up_div(n, 256) * outputs, small = up_div(m, 128) * up_div(n, 128) * outputs;
-  if (wide >= kCus) return {true, 1};
-  if (wide >= kCus / 4 && ktiles >= 64) return {true, (uint32_t)(kCus / wide)};
+  if (direct && wide >= kCus) return {true, 1};
+  if (direct && wide >= kCus / 4 && ktiles >= 64) return {true, (uint32_t)(kCus / wide)};
   if (small >= kCus) return {false, 1};
   return {false, (uint32_t)std::max<uint64_t>(1, std::min(kCus / std::max<uint64_t>(small, 1), ktiles / 8))};
 }
 uint64_t stage_terms(int dt) { return 128 / es_of(dt); }
-FfCut dx_cut(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
-  return cut_of(rows, dim, 1, 2 * up_div(hidden, stage_terms(dt)), dt);
+FfCut dx_cut(uint64_t rows, uint64_t dim, uint64_t hidden, int dt, bool direct) {
+  return cut_of(rows, dim, 1, 2 * up_div(hidden, stage_terms(dt)), dt, direct);
 }
-FfCut dw_cut(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
-  return cut_of(hidden, dim, 2, up_div(rows, stage_terms(dt)), dt);
+FfCut dw_cut(uint64_t rows, uint64_t dim, uint64_t hidden, int dt, bool direct) {
+  return cut_of(hidden, dim, 2, up_div(rows, stage_terms(dt)), dt, direct);
 }
 uint64_t partial_pitch(uint64_t n) { return up_div(n, 4) * 4; }
 
@@ -570,7 +577,12 @@ FfWorkspace ff_workspace(uint64_t rows, uint64_t dim, uint64_t hidden, int dt) {
   w.wgate = w.x + room(rows * w.copy_pitch * es);
   w.wup = w.wgate + room(hidden * w.copy_pitch * es);
   w.partials = w.wup + room(hidden * w.copy_pitch * es);
-  const uint64_t sx = dx_cut(rows, dim, hidden, dt).splits, sw = dw_cut(rows, dim, hidden, dt).splits;
+  // whether the loads are direct ones is not known here: room for either cut
+  uint64_t sx = 1, sw = 1;
+  for (const bool direct : {false, true}) {
+    sx = std::max<uint64_t>(sx, dx_cut(rows, dim, hidden, dt, direct).splits);
+    sw = std::max<uint64_t>(sw, dw_cut(rows, dim, hidden, dt, direct).splits);
+  }
   const uint64_t bx = sx > 1 ? sx * rows : 0, bw = sw > 1 ? sw * 2 * hidden : 0;
   w.bytes = w.partials + std::max(bx, bw) * partial_pitch(dim) * sizeof(float);
   return w;
@@ -658,8 +670,8 @@ hipError_t launch_gated_ff_grad(const FfBackward& b, hipStream_t stream) {
       a.out[0] = b.dx.p;
       a.out_stride[0] = b.dx.stride * es;
       a.out_dt = b.dt;
-      cut = dx_cut(b.rows, b.dim, b.hidden, b.dt);
       direct = direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]);
+      cut = dx_cut(b.rows, b.dim, b.hidden, b.dt, direct);
     } else {
       a.p[0] = a.p[1] = x.p;
       a.pstride[0] = a.pstride[1] = (uint32_t)(x.stride * es);
@@ -672,14 +684,14 @@ hipError_t launch_gated_ff_grad(const FfBackward& b, hipStream_t stream) {
       a.out_stride[1] = b.dwup.stride * oes;
       a.out_dt = b.wdt;
       a.accumulate = b.accumulate;
-      cut = dw_cut(b.rows, b.dim, b.hidden, b.dt);
       direct = direct_ok(a.p[0], a.pstride[0]);
+      cut = dw_cut(b.rows, b.dim, b.hidden, b.dt, direct);
     }
     hipError_t r = hipSuccess;
     if (a.k) {
       a.splits = cut.splits;
-      r = dx ? launch_ff_dx(b.dt, a, cut.wide && direct, direct, stream)
-             : launch_ff_dw(b.dt, a, cut.wide && direct, direct, stream);
+      r = dx ? launch_ff_dx(b.dt, a, cut.wide, direct, stream)
+             : launch_ff_dw(b.dt, a, cut.wide, direct, stream);
       if (r != hipSuccess || a.splits == 1) return r;
     }
     // without rows the weights' gradients are sums of nothing

@@ -63,3 +63,32 @@ def test_weights_of_different_strides(rows, dim, hidden, dt, steps, first):
     assert torch.equal(dx, (dg @ wg.double() + du @ wu.double()).to(t)), "dx"
     assert torch.equal(dwg, (dg.t() @ x.double()).float()), "dwgate"
     assert torch.equal(dwu, (du.t() @ x.double()).float()), "dwup"
+
+
+# products of which large tiles, had they been taken, would be split more often
+# than the small ones that rows off 16 bytes take: dx unsplit and in two splits,
+# the weights' gradients in two
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,dim,hidden", [(1024, 4096, 2056), (16384, 104, 2100), (4100, 104, 8192)])
+def test_rows_off_16_bytes_in_small_tiles(rows, dim, hidden, dt):
+    t = DTYPES[dt]
+    g = torch.Generator(device=DEV).manual_seed(rows + dim + hidden)
+
+    def ints(lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=g, device=DEV).to(t)
+
+    aligned = ints(-2, 2, rows, dim), ints(-1, 1, hidden, dim), ints(-1, 1, hidden, dim)
+    off = [_matrix(m, 0, 1, m.numel() + 8) for m in aligned]
+    gate, up, dh = 64 * ints(0, 1, rows, hidden), ints(-2, 2, rows, hidden), ints(-1, 1, rows, hidden)
+    dg = dh.double() * up.double() * torch.where(gate > 0, 1.0, 0.5)
+    du = dh.double() * gate.double()
+    x, wg, wu = (m.double() for m in aligned)
+    old = [ints(-8, 8, hidden, dim).float() for _ in range(2)]
+    want = [(dg @ wg + du @ wu).to(t), (old[0].double() + dg.t() @ x).float(), (old[1].double() + du.t() @ x).float()]
+    ws = torch.empty(rar.gated_ff_workspace_bytes(rows, dim, hidden, t), dtype=torch.uint8, device=DEV)
+    for operands in (aligned, off):
+        dx = torch.full((rows, dim), 7.0, dtype=t, device=DEV)
+        dw = [o.clone() for o in old]
+        rar.gated_ff_backward(dh, *operands, gate, up, dx, *dw, ws, act=rar.ACT_GELU, accumulate=True)
+        for got, value, name in zip((dx, *dw), want, ("dx", "dwgate", "dwup")):
+            assert torch.equal(got, value), name
