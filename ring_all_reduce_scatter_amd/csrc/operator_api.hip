@@ -642,16 +642,16 @@ int rar_gated_ff_backward(const void* dh, size_t dh_stride, const void* x, size_
   if (!ff_modes_ok(act, keep) || keep == RAR_KEEP_NONE || !dwgate != !dwup) return RAR_EINVAL;
   if (dweight_dtype != dtype && dweight_dtype != RAR_F32) return RAR_EDTYPE;
   const size_t es = es_of(dtype), we = es_of(dweight_dtype);
-  Range r[10];
+  Range r[10] = {};  // outputs left out: empty ones
   if ((rc = ff_matrix(dh, dh_stride, rows, hidden, es, false, &r[0])) ||
       (rc = ff_matrix(x, x_stride, rows, dim, es, false, &r[1], true)) ||
       (rc = ff_matrix(wgate, wgate_stride, hidden, dim, es, false, &r[2], true)) ||
       (rc = ff_matrix(wup, wup_stride, hidden, dim, es, false, &r[3], true)) ||
       (rc = ff_kept(gate, gate_stride, keep, rows, hidden, es, false, &r[4])) ||
       (rc = ff_kept(up, up_stride, keep, rows, hidden, es, false, &r[5])) ||
-      (rc = ff_matrix(dx, dx_stride, dx ? rows : 0, dim, es, true, &r[6])) ||
-      (rc = ff_matrix(dwgate, dwgate_stride, dwgate ? hidden : 0, dim, we, true, &r[7])) ||
-      (rc = ff_matrix(dwup, dwup_stride, dwup ? hidden : 0, dim, we, true, &r[8])))
+      (dx && (rc = ff_matrix(dx, dx_stride, rows, dim, es, true, &r[6]))) ||
+      (dwgate && (rc = ff_matrix(dwgate, dwgate_stride, hidden, dim, we, true, &r[7]))) ||
+      (dwup && (rc = ff_matrix(dwup, dwup_stride, hidden, dim, we, true, &r[8]))))
     return rc;
   const FfWorkspace l = ff_workspace(rows, dim, hidden, dtype);
   if (l.bytes && (!workspace || ws_bytes < l.bytes)) return RAR_EWORKSPACE;
