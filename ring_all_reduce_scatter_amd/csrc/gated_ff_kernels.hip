@@ -11,6 +11,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
 
+uint64_t up_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
 // ------------------------------------------------------------------ few tokens
 
 // Forward for at most 64 tokens: the weights' bytes are all that counts.
@@ -432,32 +434,34 @@ hipError_t act_grad_dt(const FfBackward& a, hipStream_t stream) {
 // (2048 x 2048 of four splits 13 us, 71 MB: 5.4 TB/s)
 template <int DT>
 __global__ __launch_bounds__(kThreads) void ff_join_kernel(FfProduct a) {
-  const uint64_t vecs = a.pitch / 4, i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= a.m * vecs) return;
-  const uint64_t row = i / vecs, col = (i - row * vecs) * 4;
-  const uint64_t z = blockIdx.y, plane = a.m * a.pitch;
-  const float* p = a.partials + z * a.splits * plane + row * a.pitch + col;
-  const int n = vec_count<4>(a.n, col);
-  VecF<4> v = {};
-  for (uint32_t s = 0; s < a.splits; ++s) {
-    const VecF<4> w = load_vec<DT_F32, 4>((const char*)(p + s * plane), 0);
+  const uint64_t vecs = a.pitch / 4, z = blockIdx.y, plane = a.m * a.pitch;
+  for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < a.m * vecs;
+       i += (uint64_t)gridDim.x * kThreads) {
+    const uint64_t row = i / vecs, col = (i - row * vecs) * 4;
+    const float* p = a.partials + z * a.splits * plane + row * a.pitch + col;
+    const int n = vec_count<4>(a.n, col);
+    VecF<4> v = {};
+    for (uint32_t s = 0; s < a.splits; ++s) {
+      const VecF<4> w = load_vec<DT_F32, 4>((const char*)(p + s * plane), 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v.v[e] += w.v[e];
+      for (int e = 0; e < 4; ++e) v.v[e] += w.v[e];
+    }
+    char* out = a.out[z] + row * a.out_stride[z];
+    if (a.accumulate)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) v.v[e] += load_elem_dt(out, col + e, a.out_dt);
+    if (a.out_dt == DT_F32) store_vec_upto<DT_F32, 4>(out, col, n, v);
+    else store_vec_upto<DT, 4>(out, col, n, v);
   }
-  char* out = a.out[z] + row * a.out_stride[z];
-  if (a.accumulate)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) v.v[e] += load_elem_dt(out, col + e, a.out_dt);
-  if (a.out_dt == DT_F32) store_vec_upto<DT_F32, 4>(out, col, n, v);
-  else store_vec_upto<DT, 4>(out, col, n, v);
 }
 
+// Sums of splits are few enough for a vector a thread; the zeros of gradients
+// without rows can be more than a launch has threads, and go round.
 template <int DT>
 hipError_t join_dt(const FfProduct& a, int outputs, hipStream_t stream) {
-  const uint64_t n = a.m * (a.pitch / 4);
-  hipLaunchKernelGGL((ff_join_kernel<DT>), dim3((unsigned)((n + kThreads - 1) / kThreads), outputs), dim3(kThreads), 0,
-                     stream, a);
+  const uint64_t n = a.m * (a.pitch / 4), groups = std::min<uint64_t>(up_div(n, kThreads), 1 << 20);
+  hipLaunchKernelGGL((ff_join_kernel<DT>), dim3((unsigned)groups, outputs), dim3(kThreads), 0, stream, a);
   return launch_status(stream);
 }
 
@@ -501,7 +505,6 @@ hipError_t copy_dt(const FfCopy& a, uint64_t dim, hipStream_t stream) {
 constexpr uint64_t kFewTokens = 64;
 constexpr uint64_t kCus = 256;
 
-uint64_t up_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 uint64_t es_of(int dt) { return dt == DT_F32 ? 4 : 2; }
 uint64_t blocks_pitch(uint64_t n) { return up_div(n, kCkptBlock) * kCkptBlock; }
 
