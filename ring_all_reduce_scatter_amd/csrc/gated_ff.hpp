@@ -14,33 +14,57 @@ namespace rar {
 
 enum FfAct : int { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2 };
 
-// 1 / (1 + exp(-z)) from the hardware's 2^x and reciprocal (1 ulp each): the
-// rounding of z log2(e) adds |z| 2^-24 of the exponential, which no rounding
-// to 16 bits shows.  Far below 2^-126 the exponential is infinite, the result 0.
-__device__ __forceinline__ float ff_sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+// The logistic function s = 1 / (1 + exp(-z)) and s (1 - s).  For 16 bits from
+// the hardware's 2^x and reciprocal (1 ulp each): the rounding of z log2(e) adds
+// |z| 2^-24 of the exponential, which no rounding to 16 bits shows, and below
+// 2^-126 the result is 0.  In binary32 from exp(-|z|), which never overflows, so
+// that far negative z keep their digits, down to the subnormals (1 % of the
+// gradients of 2048 x 2048 x 5632, nothing that shows of the forward pass).
+struct FfLogistic {
+  float s, slope;
+};
+template <int DT>
+__device__ __forceinline__ FfLogistic ff_logistic(float z) {
+  if constexpr (DT == DT_F32) {
+    const float t = expf(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + t);
+    return {z >= 0.0f ? r : t * r, t * r * r};
+  } else {
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+    return {s, s * (1.0f - s)};
+  }
 }
 
-// act(g) and (D) its derivative.  The tanh form of gelu is g s(2 z) with
-// z = c (g + 0.044715 g^3): (1 + tanh z) / 2 is the logistic function of 2 z.
-// s (1 - s) first: it is zero where g is large.
-template <bool D>
+// act(g), for results of type DT, and (D) its derivative.  The tanh form of gelu
+// is g s(2 z) with z = c (g + 0.044715 g^3): (1 + tanh z) / 2 is the logistic
+// function of 2 z.  s (1 - s) first: it is zero where g is large.  The sum (1 +
+// erf) / 2 loses its digits where erf is near -1, so in binary32 it is taken as
+// erfc(-x) / 2; in 16 bits the sum's error, 2^-24, passes their rounding only
+// where act(g) is below 2^-10, and erfc costs 3 us of 116 forward (2048 x 2048 x
+// 5632).
+template <int DT, bool D>
 __device__ __forceinline__ float ff_act(float g, int act, float* d) {
   if (act == FF_GELU) {
-    const float p = 0.5f + 0.5f * erff(g * 0.70710678f);
-    if constexpr (D) *d = p + g * 0.39894228f * __builtin_amdgcn_exp2f(g * g * -0.72134752f);
+    float p, e;
+    if constexpr (DT == DT_F32) {
+      p = 0.5f * erfcf(g * -0.70710678f);
+      if constexpr (D) e = expf(g * g * -0.5f);
+    } else {
+      p = 0.5f + 0.5f * erff(g * 0.70710678f);
+      if constexpr (D) e = __builtin_amdgcn_exp2f(g * g * -0.72134752f);
+    }
+    if constexpr (D) *d = p + g * 0.39894228f * e;
     return g * p;
   }
   if (act == FF_SILU) {
-    const float s = ff_sigmoid(g);
-    if constexpr (D) *d = s + g * (s * (1.0f - s));
-    return g * s;
+    const FfLogistic f = ff_logistic<DT>(g);
+    if constexpr (D) *d = f.s + g * f.slope;
+    return g * f.s;
   }
   // past 128 the logistic function is 0 or 1, and the square must not overflow
   const float g2 = __builtin_fminf(g * g, 16384.0f);
-  const float s = ff_sigmoid(1.59576912f * g * (1.0f + 0.044715f * g2));
-  if constexpr (D) *d = s + g * (s * (1.0f - s)) * (1.59576912f * (1.0f + 3.0f * 0.044715f * g2));
-  return g * s;
+  const FfLogistic f = ff_logistic<DT>(1.59576912f * g * (1.0f + 0.044715f * g2));
+  if constexpr (D) *d = f.s + g * f.slope * (1.59576912f * (1.0f + 3.0f * 0.044715f * g2));
+  return g * f.s;
 }
 
 // One product's operands: P indexes the output's columns, Q its rows.

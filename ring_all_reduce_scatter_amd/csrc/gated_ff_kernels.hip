@@ -41,7 +41,7 @@ __device__ __forceinline__ void few_store(const FfProduct& a, uint64_t token, ui
     store_elem<DT>(a.gate.p + token * a.gate.stride * ES, col, g);
     store_elem<DT>(a.up.p + token * a.up.stride * ES, col, u);
   }
-  store_elem<DT>(a.out[0] + token * a.out_stride[0], col, ff_act<false>(g, a.act, nullptr) * u);
+  store_elem<DT>(a.out[0] + token * a.out_stride[0], col, ff_act<DT, false>(g, a.act, nullptr) * u);
 }
 
 template <int DT>
@@ -404,7 +404,7 @@ __global__ __launch_bounds__(kThreads) void ff_act_grad_kernel(FfBackward a, uin
     for (int i = 0; i < E; ++i)
       if (i < n) {
         float d;
-        const float h = ff_act<true>(g[k].v[i], a.act, &d);
+        const float h = ff_act<DT, true>(g[k].v[i], a.act, &d);
         dg.v[i] = dh[k].v[i] * u[k].v[i] * d;
         du.v[i] = dh[k].v[i] * h;
       }

@@ -477,7 +477,7 @@ __device__ __forceinline__ void ff_finish(const FfItem& it, uint32_t wp, uint32_
       const uint64_t stride = args->out_stride[0];
       ff_store_blocks<DT, NP / 4, true>(
           scratch, args->out[0] + r0 * stride + c0 * ES, stride, rows, cols,
-          [&](int b, int e) { return ff_act<false>(at(2 * b, e), act, nullptr) * at(2 * b + 1, e); });
+          [&](int b, int e) { return ff_act<DT, false>(at(2 * b, e), act, nullptr) * at(2 * b + 1, e); });
     } else {
       const bool second = KIND == FF_DW && it.z;
       const uint64_t stride = second ? args->out_stride[1] : args->out_stride[0];
