@@ -707,7 +707,9 @@ size_t rar_gated_ff_workspace_bytes(size_t rows, size_t dim, size_t hidden, int 
  *   dx     <- round(dg wgate + du wup)
  *   dwgate <- round(dg^T x),  dwup <- round(du^T x),
  * with accumulate added to what dwgate and dwup hold.  dg and du are rounded
- * to dtype, as the matrix instructions take them; all sums are binary32.
+ * to dtype, as the matrix instructions take them; all sums are binary32.  In
+ * binary16 a dg or du beyond 65,504 is infinite, and with it its row of dx and
+ * its row of dwgate or dwup: a loss is scaled with these in mind too.
  * dweight_dtype: dtype or RAR_F32.  dx may be NULL, dwgate and dwup may both
  * be NULL.  rows == 0 makes dwgate and dwup zero (untouched with accumulate).
  * No output may overlap anything else.  dh_stride, x_stride and the strides of

@@ -502,7 +502,8 @@ def gated_ff_backward(dout, x, wgate, wup, gate, up, dx, dwgate, dwup, workspace
     """Gradients of gated_ff_forward from what it kept in gate and up.  dx (x's
     shape and type) may be None, dwgate and dwup (the weights' shape, x's type
     or float32) may both be None; with accumulate the weights' gradients are
-    added to what they hold."""
+    added to what they hold.  The projections' own gradients are rounded to
+    x's type on the way: in float16 one beyond 65,504 becomes infinite."""
     dim, hidden, gstride, ustride = _ff_weights(x, wgate, wup)
     rows, xstride = _rows(x, dim, "x")
     n, dstride = _rows(dout, hidden, "dout")

@@ -105,3 +105,26 @@ def test_bounds_hold_for_the_reference():
         a, d = block_ref.act(g, kind)
         assert torch.allclose(_value(g, kind)[0], a, rtol=1e-9, atol=1e-15)
         assert torch.allclose(_slope(g, kind)[0], d, rtol=1e-9, atol=1e-14)
+
+
+@pytest.mark.parametrize("dtype,finite", [(torch.float16, False), (torch.bfloat16, True), (torch.float32, True)])
+def test_gradients_beyond_binary16(dtype, finite):
+    """dg of 10^5 at one place is infinite in binary16 only, and spoils its row
+    of dx and its row of dwgate, no others."""
+    rows, dim, hidden, r, c = 150, 72, 96, 5, 40
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, wg, wu, dh, gate, up = (torch.randn(*s, generator=g, device=DEV).to(dtype) for s in (
+        (rows, dim), (hidden, dim), (hidden, dim), (rows, hidden), (rows, hidden), (rows, hidden)))
+    dh[r, c], gate[r, c] = 1000.0, 20.0
+    ws = torch.empty(rar.gated_ff_workspace_bytes(rows, dim, hidden, dtype), dtype=torch.uint8, device=DEV)
+    runs = []
+    for u in (1.0, 100.0):
+        up[r, c] = u
+        out = torch.empty_like(x), *(torch.empty(hidden, dim, device=DEV) for _ in range(2))
+        rar.gated_ff_backward(dh, x, wg, wu, gate, up, *out, ws)
+        runs.append(out)
+    (dx0, dg0, du0), (dx, dg, du) = runs
+    assert bool(dx[r].isfinite().all()) == bool(dg[c].isfinite().all()) == finite
+    others = [torch.arange(n, device=DEV) != i for n, i in ((rows, r), (hidden, c))]
+    assert torch.equal(dx[others[0]], dx0[others[0]]) and torch.equal(dg[others[1]], dg0[others[1]])
+    assert torch.equal(du, du0) and all(bool(t.isfinite().all()) for t in (dx0, dg0, du0))
