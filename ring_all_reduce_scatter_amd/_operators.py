@@ -83,9 +83,19 @@ def _floats(t, n: int, what: str):
 
 
 def _on_gpu(*ts):
+    """Refuses host tensors and tensors of two GPUs: a kernel reads all of them
+    from one."""
+    device = None
     for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"expected a GPU tensor, got one on {t.device}")
+        if t is None:
+            continue
+        index = t.get_device()
+        if index != device:
+            if index < 0:
+                raise ValueError(f"expected a GPU tensor, got one on {t.device}")
+            if device is not None:
+                raise ValueError(f"tensors must be on one device, got some on cuda:{device} and some on cuda:{index}")
+            device = index
 
 
 _id_codes: dict = {}  # filled by the first call, so importing needs no torch
@@ -103,20 +113,28 @@ def _ids(ids):
     return code
 
 
-_current_stream = None
+_current_stream = _current_device = None
 
 
 def _stream(stream, t):
-    """Address of the given stream, or of the current one on t's device."""
+    """Address of the given stream, or of the current one on t's device.  A
+    device's default stream has no address of its own: a launch with none runs
+    on the current device, which must then be t's."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    global _current_stream
+    global _current_stream, _current_device
     if _current_stream is None:
         import torch
         # the address without a Stream object around it, where torch offers that
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _current_stream(t.get_device())
+    index = t.get_device()
+    address = _current_stream(index)
+    if not address and _current_device() != index:
+        raise ValueError(f"tensors on cuda:{index} need it as the current device (cuda:{_current_device()} is), or a "
+                         "stream of it")
+    return address
 
 
 def _check(rc: int, what: str):
@@ -219,14 +237,14 @@ class GradClip:
         """norm (one float32 on the device, apart from the tensors) <- |scale|
         * the norm of all gradients."""
         address = _floats(norm, 1, "norm")
-        _on_gpu(norm)
+        _on_gpu(self._ws, norm)
         rc = (_binding._lib or lib()).rar_grad_norm(self._ref, norm_type, scale, address, _stream(stream, self._ws))
         _check(rc, "rar_grad_norm")
 
     def clip(self, max_norm: float, norm, norm_type: int = NORM_L2, scale: float = 1.0, stream=None):
         """The same norm, and every gradient times scale * min(1, max_norm / (norm + 1e-6))."""
         address = _floats(norm, 1, "norm")
-        _on_gpu(norm)
+        _on_gpu(self._ws, norm)
         rc = (_binding._lib or lib()).rar_grad_clip(
             self._ref, norm_type, scale, max_norm, address, _stream(stream, self._ws))
         _check(rc, "rar_grad_clip")
