@@ -612,9 +612,11 @@ hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream) {
   a.up = f.up;
   a.cgate = f.cgate;
   a.cup = f.cup;
-  // At 4096 x 11,264 bfloat16 64 tokens take 67 us, 65 in tiles 73; at 1024 x
-  // 2816 14.9 and 17.6.  A checkpoint's block of 32 columns is more than a
-  // workgroup of whole lines has.
+  // At 4096 x 11,264 bfloat16 64 tokens take 68 us, 65 in tiles 76; at 1024 x
+  // 2816 15 and 17.6.  Kept as checkpoints few tokens go through the tiles too, 71
+  // us for one and 77 for 64 (with kept rows 29 and 68): they find a block's
+  // largest value in registers, the kernels of few tokens store their sums one by
+  // one.
   if (f.rows <= kFewTokens && f.saved != 2)
     return by_type(f.dt, [&](auto t) { return few_dt<decltype(t)::value>(a, stream); });
   const bool direct = f.dim % (16 / es) == 0 && direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) &&
