@@ -621,9 +621,9 @@ hipError_t launch_gated_ff(const FfForward& f, hipStream_t stream) {
     return by_type(f.dt, [&](auto t) { return few_dt<decltype(t)::value>(a, stream); });
   const bool direct = f.dim % (16 / es) == 0 && direct_ok(a.p[0], a.pstride[0]) && direct_ok(a.p[1], a.pstride[1]) &&
                       direct_ok(a.q[0], a.qstride);
-  // large tiles where they give every CU one: 8192 x 4096 x 11,264 bfloat16 1192
-  // us (small ones 1709), 2048 x 2048 x 5632 117 (127); 511 x 2048 x 5632 53 and
-  // 36, 1024 x 1024 x 2816 34 and 22.6
+  // large tiles where they give every CU one: 8192 x 4096 x 11,264 bfloat16 1150
+  // us (small ones 1636), 2048 x 2048 x 5632 104 (103); where they do not: 511 x
+  // 2048 x 5632 50 and 34, 1024 x 1024 x 2816 31 and 20.7
   const bool wide = direct && f.dt != DT_F32 && up_div(f.rows, 256) * up_div(f.hidden, 128) >= kCus;
   return launch_ff_forward_tiles(f.dt, a, wide, direct, stream);
 }

@@ -25,9 +25,9 @@
 // four consecutive k.
 //
 // Bound by the matrix units' rate under power and what the loads leave of it.
-// 8192 x 4096 x 11,264 bfloat16 (1.51 TFLOP a pass of two products): forward 1145
-// us without kept projections (1.32 PFLOP/s) and 1230 with checkpoints, dx 1205,
-// dW 1340; large library products of these layouts reach 1.33-1.53, 1.20-1.40
+// 8192 x 4096 x 11,264 bfloat16 (1.51 TFLOP a pass of two products): forward 1149
+// us without kept projections (1.32 PFLOP/s) and 1212 with checkpoints, dx 1201,
+// dW 1312, medians; large library products of these layouts reach 1.33-1.53, 1.20-1.40
 // and 0.98-1.08 PFLOP/s.  Measured and left out: instructions of 32 x 32 (power),
 // stages of 64 bytes a row in four turns (their loads move at half the rate:
 // 1418 us where two of 128 took 1319), three to five stages, four wavefronts of
@@ -758,9 +758,9 @@ hipError_t ff_launch_dt(FfProduct& a, bool wide, bool direct, hipStream_t stream
   if constexpr (DT == DT_F32) {
     // In binary32 the matrix instructions take sixteen times as long for a
     // stage, so that small tiles cost little and fill the CUs evenly: forward of
-    // 513 x 1024 x 2816 67 us (80 by 64 rows), 65 x 1024 x 2816 31.5 (52), 2048 x
-    // 2048 x 5632 794 (784).  The backward products are split, which does that
-    // for tiles of 64 rows.
+    // 65 x 1024 x 2816 33 us (43 by 64 rows), 513 x 1024 x 2816 66 (75).  Many
+    // tokens would take the larger ones: 2048 x 2048 x 5632 795 (729).  The
+    // backward products are split, which fills the CUs for tiles of 64 rows.
     constexpr int TP = KIND == FF_FORWARD ? 128 : 64, TQ = KIND == FF_FORWARD ? 32 : 64;
     return direct ? ff_launch<DT, KIND, FfShape<TP, TQ, 2, 2>, true>(a, stream)
                   : ff_launch<DT, KIND, FfShape<TP, TQ, 2, 2>, false>(a, stream);
