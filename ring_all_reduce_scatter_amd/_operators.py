@@ -126,12 +126,13 @@ def _stream(stream, t):
     if _current_stream is None:
         import torch
         # the address without a Stream object around it, where torch offers that
-        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        if torch.cuda.device_count() > 1:  # the only one is the current one
+            _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda index: torch.cuda.current_stream(index).cuda_stream)
     index = t.get_device()
     address = _current_stream(index)
-    if not address and _current_device() != index:
+    if not address and _current_device and _current_device() != index:
         raise ValueError(f"tensors on cuda:{index} need it as the current device (cuda:{_current_device()} is), or a "
                          "stream of it")
     return address

@@ -37,3 +37,5 @@ def test_default_stream_of_another_device(monkeypatch):
     assert _operators._stream(0x30, On(1)) == 0x30
     with pytest.raises(ValueError, match="cuda:1 need it as the current device"):
         _operators._stream(None, On(1))
+    monkeypatch.setattr(_operators, "_current_device", None)  # a process that sees one GPU
+    assert _operators._stream(None, On(0)) == 0
